@@ -53,6 +53,12 @@ extern "C" {
 #define APA_ERR_ALIGN (-8)     /* q, k or v not 16-byte aligned */
 #define APA_ERR_SCRATCH (-9)   /* too large for the fixed scratch of apa_quantize_noalloc */
 #define APA_ERR_FLAGS (-10)    /* an unknown bit in `flags` */
+#define APA_ERR_DTYPE (-11)    /* an unknown element type */
+#define APA_ERR_WINDOW (-12)   /* window or sinks out of range */
+
+/* Element types of the cache entry points. */
+#define APA_DTYPE_BF16 0
+#define APA_DTYPE_F16 1
 
 /* Options of the _ex entry points. */
 #define APA_FLAG_Q_RESIDUAL 1u /* Q as two FP4 terms in pass 1 (see apa_attention_ex) */
@@ -240,6 +246,123 @@ int apa_quantize_noalloc(const void* q, const void* k, const void* v, int B, int
 /* Scratch bytes apa_quantize_noalloc needs for this problem (0 for invalid sizes). */
 size_t apa_quantize_noalloc_scratch_bytes(int B, int Hq, int Hkv, int Nkv, int d);
 size_t apa_q_blob_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
+/* ------------------------------------------------------------------ sliding window
+ * Causal attention with a sliding window and sinks (first keys that stay visible):
+ * query row i, at position p = i + Nkv - Nq, sees key j iff
+ *     j <= p  and  (j > p - window  or  j < sinks).
+ *   q        bf16 [B, Hq, Nq, d], contiguous
+ *   k, v     bf16 [B, Hkv, Nkv, d], contiguous, Nkv >= Nq
+ *   window   >= 1 keys, the row's own among them; sinks >= 0
+ *   out      bf16 [B, Hq, Nq, d] (required)
+ *   lse      fp32 [B, Hq, Nq], natural-log log-sum-exp of the scaled scores (nullable)
+ * Exact attention, as the eps = 0 form of apa_attention: BF16 Q K^T and FP32
+ * softmax statistics; here P is rounded to BF16 for the product with V itself
+ * (relative error 2^-8 at most per weight, as the rounding of the output).  Only the
+ * key tiles that a row block sees are read.  No workspace. */
+int apa_attention_window(const void* q, const void* k, const void* v, int B, int Hq, int Hkv, int Nq, int Nkv, int d,
+                         int window, int sinks, void* out, float* lse, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ 4-bit K/V cache
+ * Keys and values of decoding sequences in NVFP4 (E2M1 codes, one UE4M3 scale per
+ * 16 channels of a key, one FP32 scale per KV head), in pages of 64 keys:
+ *   pages    uint8 [num_pages][Hkv][72*d], 16-byte aligned, num_pages < 2^25
+ * A page holds, per KV head, four blocks of 16 keys of 18*d bytes each:
+ *   K codes   8*d bytes  key i, byte x: codes of channels 2x (low nibble), 2x + 1
+ *   V codes   8*d bytes  key i, channels 16t + g (low nibble) and 16t + 8 + g, g < 8:
+ *                        byte 512*(t/4) + 16*(4*g + i/4) + 4*(t%4) + i%4
+ *   K scales    d bytes  key i, channels 16t .. 16t + 15: byte i*d/16 + t
+ *   V scales    d bytes  key i, channels 16t .. 16t + 15: byte 4*((i/4)*d/16 + t) + i%4
+ * (the V order is the one the attention's matrix products read in place, and every
+ * key owns whole bytes, so tokens are appended independently of each other).
+ * A value is E2M1 * UE4M3 * the head's FP32 scale.  Quantization is apa_quantize's,
+ * bit for bit, with the caller's head scales (positive and finite; the largest
+ * magnitude expected divided by 2688; larger values saturate): scale code
+ * b = UE4M3(fp32(max|x| / fp32(6 s))); codes 0 if b is 0, else
+ * E2M1(fp32(x * fp32(1 / fp32(b s)))).  Keys are not mean-centred (the mean would
+ * change with every appended key).
+ * A slot names a key's place in the pool: page * 64 + key within the page. */
+size_t apa_cache_page_bytes(int Hkv, int d); /* bytes of one page: Hkv * 72 * d */
+
+/* Grows, shrinks and places requests, and maps their new tokens to slots, on the
+ * GPU: no length is read on the host.  Request b goes from old_lens[b] to
+ * new_lens[b] keys (ends: to 0; begins: from 0).
+ *   old_lens, new_lens  int32 [B], each in [0, 64 * max_pages]; 1 <= B <= 8192
+ *   block_table  int32 [B][max_pages], updated in place: entries below
+ *                ceil(old/64) are the request's pages; a request that grows gets
+ *                entries ceil(old/64) .. ceil(new/64)-1; all others are left alone
+ *   free_pages   int32 [free_capacity], a stack of free pages, updated in place;
+ *                *free_count of them are free, the last one is on top
+ * First the pages that shrinking requests give up, entries ceil(new/64) ..
+ * ceil(old/64)-1, go on top of the stack, in request and entry order; then the
+ * pages that growing requests need come off the top, in that order.
+ *   slots      int32 [max_tokens]: the slots of the tokens old_lens[b] ..
+ *              new_lens[b]-1 of request 0, then of request 1, ...; -1 behind the last
+ *   positions  int32 [max_tokens]: their positions in the request; 0 behind the last
+ *   starts     int32 [B+1]: where each request's tokens start in slots, and the end
+ *   free_count_out  int32 [1]: the free pages left; may be free_count itself
+ *   status     int32 [1]: 0, or why nothing was changed (all slots are -1, positions
+ *              and starts 0, *free_count_out = *free_count): APA_TABLES_LENGTH a
+ *              length out of range, APA_TABLES_TOKENS more tokens than max_tokens,
+ *              APA_TABLES_PAGES too few free pages, APA_TABLES_FREE the stack's
+ *              count out of range, or too many pages given back for its capacity
+ * One launch, no workspace; the results do not depend on the launch's shape. */
+#define APA_TABLES_LENGTH 1
+#define APA_TABLES_TOKENS 2
+#define APA_TABLES_PAGES 3
+#define APA_TABLES_FREE 4
+int apa_cache_tables(const int32_t* old_lens, const int32_t* new_lens, int B, int32_t* block_table, int max_pages,
+                     int32_t* free_pages, int free_capacity, const int32_t* free_count, int max_tokens, int32_t* slots,
+                     int32_t* positions, int32_t* starts, int32_t* free_count_out, int32_t* status,
+                     cudaStream_t stream);
+
+/* Quantizes T tokens' keys and values into their slots of the cache.
+ *   k, v     dtype (APA_DTYPE_*) [Hkv][T][d]; channels contiguous, heads and tokens
+ *            at the given strides (in elements, multiples of 8); 16-byte aligned.
+ *            (A projection's [T][Hkv][d] output is such an array.)
+ *   slots    int32 [T]; a negative slot's token is skipped (padding), one outside the
+ *            pool is skipped and reported by apa_check_error.  Slots of one call differ
+ *            (of two tokens with one slot, each byte there is from one or the other).
+ *   k_scale, v_scale  fp32 [Hkv]
+ * Everything else in the pool is left as it is.  T = 0 does nothing. */
+int apa_cache_write(const void* k, const void* v, int dtype, int Hkv, int T, int d, long long k_head_stride,
+                    long long k_token_stride, long long v_head_stride, long long v_token_stride, const int32_t* slots,
+                    uint8_t* pages, int num_pages, const float* k_scale, const float* v_scale, cudaStream_t stream);
+
+/* The values that cached tokens stand for: k, v of `dtype`, contiguous [Hkv][T][d]
+ * (the layout of one sequence in apa_attention), fp32(fp32(E2M1 * UE4M3) * scale)
+ * rounded to dtype.  Tokens of negative slots are zero; a slot outside the pool
+ * gives zeros and is reported by apa_check_error.  T = 0 does nothing. */
+int apa_cache_read(const uint8_t* pages, int num_pages, int dtype, int Hkv, int T, int d, const int32_t* slots,
+                   const float* k_scale, const float* v_scale, void* k, void* v, cudaStream_t stream);
+
+/* Attention of the last Nq query rows of each sequence over the cache (Nq = 1:
+ * decoding; a few: drafted tokens, or the end of a prompt).  Row i of sequence b, at
+ * position p = lens[b] - Nq + i, sees key j iff j <= p and, with window >= 1,
+ * (j > p - window or j < sinks); window = 0: every key up to p.
+ *   q        dtype [B][Hq][Nq][d]; channels contiguous, the rest at the given strides
+ *            (in elements, multiples of 8); 16-byte aligned
+ *   block_table  int32 [B][max_pages]: entry t of sequence b is the page of its keys
+ *            64t .. 64t+63; an entry outside the pool reads page 0 and is reported by
+ *            apa_check_error (only entries of visible keys are read)
+ *   lens     int32 [B]: keys per sequence, the rows' own among them, in
+ *            [0, 64 * max_pages] (others are clamped to it and reported).  Keys past
+ *            lens[b], and whatever a page holds there, are never used.
+ *   out      dtype [B][Hq][Nq][d], contiguous; a row that sees no key is zero
+ *   lse      fp32 [B][Hq][Nq], natural log (nullable); -inf for such a row
+ *   workspace  apa_attention_cache_workspace_bytes() bytes, 256-byte aligned, or null
+ *            to have it allocated stream-ordered for the call.  Two calls that overlap
+ *            on the GPU must not share one.
+ * K, V and Q enter the products exactly (E2M1 * UE4M3 and a row of Q divided by a
+ * power of two are FP16 values), with FP32 accumulation; the softmax weights are
+ * rounded to FP16 for the product with V.  B <= 8192.  The work is split over the GPU
+ * by the lengths alone, so reruns are bitwise equal. */
+int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
+                        long long q_row_stride, const uint8_t* pages, int num_pages, const int32_t* block_table,
+                        int max_pages, const int32_t* lens, const float* k_scale, const float* v_scale, int B, int Hq,
+                        int Hkv, int Nq, int d, int window, int sinks, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
 
 /* Measurement aid, off by default.  While enabled, every apa_attention* call
  * records CUDA events on its stream around its three stages (quantizer, pass 1,

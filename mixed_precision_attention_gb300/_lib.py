@@ -17,7 +17,7 @@ APA_OK = 0
 _lock = threading.Lock()
 _lib = None
 
-P, I, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+P, I, F, SZ, LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 _SIGS = {
     "apa_attention": (I, [P, P, P, I, I, I, I, I, I, I, F, P, P, P, P]),
     "apa_attention_ws": (I, [P, P, P, I, I, I, I, I, I, I, F, P, P, P, P, SZ, P]),
@@ -33,6 +33,13 @@ _SIGS = {
     "apa_quantize_noalloc_scratch_bytes": (SZ, [I, I, I, I, I]),
     "apa_kv_blob_bytes": (SZ, [I, I, I, I]),
     "apa_q_blob_bytes": (SZ, [I, I, I, I, I]),
+    "apa_attention_window": (I, [P, P, P, I, I, I, I, I, I, I, I, P, P, P]),
+    "apa_cache_page_bytes": (SZ, [I, I]),
+    "apa_cache_tables": (I, [P, P, I, P, I, P, I, P, I, P, P, P, P, P, P]),
+    "apa_cache_write": (I, [P, P, I, I, I, I, LL, LL, LL, LL, P, P, I, P, P, P]),
+    "apa_cache_read": (I, [P, I, I, I, I, I, P, P, P, P, P, P]),
+    "apa_attention_cache": (I, [P, I, LL, LL, LL, P, I, P, I, P, P, P, I, I, I, I, I, I, I, P, P, P, SZ, P]),
+    "apa_attention_cache_workspace_bytes": (SZ, [I, I, I, I, I]),
     "apa_check_error": (I, [P]),
     "apa_stage_timing": (I, [I]),
     "apa_stage_timing_read": (I, [P, P]),

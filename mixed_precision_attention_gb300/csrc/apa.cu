@@ -322,6 +322,18 @@ int apa_attention_paged(const void* q, const void* k_pages, const void* v_pages,
   return st;
 }
 
+int apa_attention_window(const void* q, const void* k, const void* v, int B, int Hq, int Hkv, int Nq, int Nkv, int d,
+                         int window, int sinks, void* out, float* lse, cudaStream_t stream) {
+  const int st = apa::validate(q, k, v, static_cast<const float*>(out), B, Hq, Hkv, Nq, Nkv, d, 1, 0.f, true);
+  if (st) return st;
+  if (window < 1 || sinks < 0) return APA_ERR_WINDOW;
+  if ((uintptr_t)out & 15) return APA_ERR_ALIGN;
+  Shape s{B, Hq, Hkv, Nq, Nkv, d, 1};
+  if (window > Nkv) window = Nkv;  // (the kernels' index arithmetic stays within 32 bits)
+  if (sinks > Nkv) sinks = Nkv;
+  return apa::launch_window(s, q, k, v, window, sinks, out, lse, stream) == cudaSuccess ? APA_OK : APA_ERR_CUDA;
+}
+
 size_t apa_workspace_bytes_ex(int B, int Hq, int Hkv, int Nq, int Nkv, int d, float eps, unsigned flags) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nkv < 1 || Hq % Hkv || (flags & ~apa::kKnownFlags)) return 0;
   Shape s{B, Hq, Hkv, Nq, Nkv, d, 1};
@@ -546,6 +558,8 @@ const char* apa_status_string(int status) {
     case APA_ERR_ALIGN: return "q, k and v must be 16-byte aligned";
     case APA_ERR_SCRATCH: return "problem too large for the fixed scratch of apa_quantize_noalloc";
     case APA_ERR_FLAGS: return "unknown option flag";
+    case APA_ERR_DTYPE: return "unknown element type (bf16 or fp16)";
+    case APA_ERR_WINDOW: return "window or sinks out of range";
   }
   return "unknown status";
 }

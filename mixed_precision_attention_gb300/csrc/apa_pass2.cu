@@ -77,6 +77,38 @@ struct P2Params {
   float* part_o;              // [BH*nblk*nsplit][128][d]
   float2* part_ml;            // [BH*nblk*nsplit][128]
   float* part_qmu;            // [BH*nblk][128], APA mode only
+  // the sliding-window form: see WindowTiles
+  int window, sinks;
+  uint16_t* out16;            // [B,Hq,Nq,d] bf16
+};
+
+// The sliding-window form of the kernels (template parameter W; apa_attention_window):
+// row position x (x = pos + off) sees the keys j <= x with j > x - window or j < sinks.
+// A block walks the tiles that hold sinks, then those its rows' windows reach, every
+// row group taking part; P and V go to the product in BF16, V straight from the
+// caller's array, so there is no copy of V and no workspace; out is bf16.
+struct WindowTiles {
+  int n_sink, t_lo, n;  // entries 0 .. n_sink-1: tiles 0 ..; then tiles t_lo ..
+  __device__ __forceinline__ WindowTiles(const P2Params& p, int p0, int t_hi) {
+    const int first = p0 / p.s.G() + p.s.off();  // position of the block's first row
+    t_lo = max(0, first - p.window + 1) / kTile;
+    n_sink = min((int)(((long long)p.sinks + kTile - 1) / kTile), t_lo);
+    n = n_sink + t_hi - t_lo + 1;
+  }
+  __device__ __forceinline__ int tile(int i) const { return i < n_sink ? i : t_lo + i - n_sink; }
+};
+// The keys of tile j0 .. j0+63 that a row at position x sees: indices 0 .. nvis-1 but
+// for gap_lo .. gap_hi-1.  nvis = 0 if there is none.
+struct RowKeys {
+  int nvis, gap_lo, gap_hi;
+  __device__ __forceinline__ RowKeys(const P2Params& p, int x, int j0, bool valid) {
+    nvis = valid ? min(kTile, x + 1 - j0) : 0;
+    gap_hi = min(kTile, x - p.window + 1 - j0);  // first key of the window
+    gap_lo = max(0, min(kTile, p.sinks - j0));   // first key that is no sink
+    if (gap_lo == 0 && gap_hi >= nvis) nvis = 0;
+  }
+  __device__ __forceinline__ bool all() const { return nvis == kTile && gap_lo >= gap_hi; }
+  __device__ __forceinline__ bool sees(int i) const { return i < nvis && (i < gap_lo || i >= gap_hi); }
 };
 
 constexpr int kThreads = 224;
@@ -122,9 +154,23 @@ __device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, int*
 }
 
 // P of eight consecutive keys, 2^(x*c2 + nb), as four FP16x2 words (key 2k in the
-// low half of word k); the FP32 values are added into (s0, s1): even keys into s0,
-// odd keys into s1.  The affine step and the sums run as packed FP32 pairs.
-__device__ __forceinline__ void p8_f16(const float* x, float c2, float nb, uint32_t* h, float& s0, float& s1) {
+// low half of word k; BF16x2 in the sliding-window form); the FP32 values are added
+// into (s0, s1): even keys into s0, odd keys into s1.  The affine step and the sums
+// run as packed FP32 pairs.
+template <bool W>
+__device__ __forceinline__ void p8(const float* x, float c2, float nb, uint32_t* h, float& s0, float& s1) {
+  if constexpr (W) {
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = ex2_approx(fmaf(x[k], c2, nb));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(y[2 * k + 1]), "f"(y[2 * k]));
+      s0 += y[2 * k];
+      s1 += y[2 * k + 1];
+    }
+    return;
+  }
   asm("{\n.reg .b64 a0, a1, a2, a3, c, n, s, one;\n"
       ".reg .f32 y0, y1, y2, y3, y4, y5, y6, y7;\n"
       "mov.b64 c, {%14, %14};\n"
@@ -169,7 +215,22 @@ __device__ __forceinline__ void p8_f16(const float* x, float c2, float nb, uint3
         "f"(1.f));
 }
 
-template <int D>
+// 32 FP32 values of a row -> bf16, 64 bytes.
+__device__ __forceinline__ void store_bf16x32(uint16_t* dst, const uint32_t* o) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    uint4 w;
+    uint32_t* r = &w.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+          : "=r"(r[e])
+          : "f"(__uint_as_float(o[j + 2 * e + 1])), "f"(__uint_as_float(o[j + 2 * e])));
+    *reinterpret_cast<uint4*>(dst + j) = w;
+  }
+}
+
+template <int D, bool W = false>
 __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
     pass2_kernel(const P2Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = P2Cfg<D>;
@@ -223,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
   const bool apa_mode = p.hot_list != nullptr;
   const int last_row = min(R, p0 + kBlockRows) - 1;
   const int t_hi = s.causal ? min(T - 1, (last_row / G + off) / kTile) : T - 1;
-  const int n_all = apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
+  const WindowTiles wt(p, p0, t_hi);  // (used in the sliding-window form only)
+  const int n_all = W ? wt.n : apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
   const int i0 = p.nsplit > 1 ? (int)((long long)n_all * part / p.nsplit) : 0;
   const int n = p.nsplit > 1 ? (int)((long long)n_all * (part + 1) / p.nsplit) - i0 : n_all;
   const uint32_t* list = apa_mode ? p.hot_list + ((size_t)bh * nblk + blk) * T : nullptr;
@@ -234,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
       return (int)(e & 0xFFFFu);
     }
     gmask = 0xFFu;
+    if constexpr (W) return wt.tile(i0 + i);
     const int g = i0 + i;
     return g == 0 ? 0 : t_hi + 1 - g;
   };
@@ -361,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
   } else if (warp == 6) {
     // ------------------------------------------------------------ PV issuer
     if (lane == 0 && n > 0) {
-      const uint32_t idO = idesc_f16(128, D, 1);
+      const uint32_t idO = W ? idesc_bf16(128, D, 1) : idesc_f16(128, D, 1);
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         if (!(ok = mbar_wait(p_full(i & 1), (i >> 1) & 1, &abort_flag, p.err))) break;
@@ -399,7 +462,9 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
       if (!(ok = warp_wait(s_full(i & 1), (i >> 1) & 1))) break;
       const bool row_hot = row_valid && ((gm >> (r >> 4)) & 1u);
       const int j0 = t * kTile;
-      const int nvis = row_hot ? min(kTile, vis_last + 1 - j0) : 0;  // keys j0 .. j0+nvis-1 visible
+      const RowKeys rk(p, vis_last, j0, row_hot);  // (used in the sliding-window form only)
+      // keys j0 .. j0+nvis-1 visible (but for the gap behind the sinks)
+      const int nvis = W ? rk.nvis : row_hot ? min(kTile, vis_last + 1 - j0) : 0;
       // P (FP16, two keys per column) goes over the first 32 columns of the S slot it
       // came from; the slot's previous P had been read before S was written into it
       const uint32_t pslot = tmem + lane_base + C::kSCol + 64u * (i & 1);
@@ -428,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
       float sv[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) sv[j] = __uint_as_float(raw[j]);
-      if (__any_sync(0xffffffffu, nvis > 0 && nvis < 64)) {
+      if (__any_sync(0xffffffffu, nvis > 0 && (W ? !rk.all() : nvis < 64))) {
 #pragma unroll
         for (int j = 0; j < 64; ++j)
-          if (j >= nvis) sv[j] = -INFINITY;
+          if (W ? !rk.sees(j) : j >= nvis) sv[j] = -INFINITY;
       }
       // row maximum as a tree of 3-input maxima; the logit map x*c2 - shift is monotone
       // (c2 > 0), so its maximum is the map of the raw maximum, rounded the same way
@@ -463,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
           const int ch = 4 * hf + c4;
-          p8_f16(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
+          p8<W>(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
         }
         tmem_st_x16(pslot + 16u * hf, pk);
       }
@@ -553,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
       const float w1 = e1 == -INFINITY ? 0.f : exp2f(e1 - M), w2 = e2 == -INFINITY ? 0.f : exp2f(e2 - M);
       const float L = w1 * l1 + w2 * l2;
       const float invL = 1.f / L;
-      const float w2o = w2 * v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
-      float* orow = p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
+      const float w2o = W ? w2 : w2 * v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
+      float* orow = W ? nullptr : p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t o[32];
@@ -565,7 +630,13 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
-        if (row_valid) {
+        if constexpr (W) {
+          if (row_valid) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * (w2o * invL));
+            store_bf16x32(p.out16 + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D + c0, o);
+          }
+        } else if (row_valid) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             float4 res;
@@ -658,7 +729,7 @@ struct P2DualCfg {
   static_assert(kSBase + 256 <= kTmemCols, "TMEM budget");
 };
 
-template <int D>
+template <int D, bool W = false>
 __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
     pass2_dual_kernel(const P2Params p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
@@ -712,9 +783,11 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
   const bool apa_mode = p.hot_list != nullptr;
   const int last_row = min(R, p0 + kBlockRows) - 1;
   const int t_hi = s.causal ? min(T - 1, (last_row / G + off) / kTile) : T - 1;
-  const int n = apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
+  const WindowTiles wt(p, p0, t_hi);  // (used in the sliding-window form only)
+  const int n = W ? wt.n : apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
   const uint32_t* list = apa_mode ? p.hot_list + ((size_t)bh * nblk + blk) * T : nullptr;
   auto entry = [&](int i) -> uint32_t {
+    if constexpr (W) return (uint32_t)wt.tile(i) | (0xFFu << 16);
     return apa_mode ? list[i] : ((uint32_t)(i == 0 ? 0 : t_hi + 1 - i) | (0xFFu << 16));
   };
 
@@ -849,7 +922,7 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
   } else if (warp == kMmaPV) {
     // ------------------------------------------------------------ PV issuer: tile i into group i % 2's O
     if (lane == 0 && n > 0) {
-      const uint32_t idO = idesc_f16(128, D, 1);
+      const uint32_t idO = W ? idesc_bf16(128, D, 1) : idesc_f16(128, D, 1);
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         const int st = i % C::NSV, v = i & 1, j = i >> 1, b2 = j & 1;
@@ -888,7 +961,9 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
       if (!(ok = warp_wait(s_full(u, j & 1), (j >> 1) & 1))) break;
       const bool row_hot = row_valid && ((gm >> (r >> 4)) & 1u);
       const int j0 = t * kTile;
-      const int nvis = row_hot ? min(kTile, vis_last + 1 - j0) : 0;  // keys j0 .. j0+nvis-1 visible
+      const RowKeys rk(p, vis_last, j0, row_hot);  // (used in the sliding-window form only)
+      // keys j0 .. j0+nvis-1 visible (but for the gap behind the sinks)
+      const int nvis = W ? rk.nvis : row_hot ? min(kTile, vis_last + 1 - j0) : 0;
       // P (FP16, two keys per column) goes over the first 32 columns of the S slot it
       // came from; the slot's previous P had been read before S was written into it
       const uint32_t pslot = tmem + lane_base + tS + 64u * (j & 1);
@@ -913,10 +988,10 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
       float sv[64];
 #pragma unroll
       for (int x = 0; x < 64; ++x) sv[x] = __uint_as_float(raw[x]);
-      if (__any_sync(0xffffffffu, nvis > 0 && nvis < 64)) {
+      if (__any_sync(0xffffffffu, nvis > 0 && (W ? !rk.all() : nvis < 64))) {
 #pragma unroll
         for (int x = 0; x < 64; ++x)
-          if (x >= nvis) sv[x] = -INFINITY;
+          if (W ? !rk.sees(x) : x >= nvis) sv[x] = -INFINITY;
       }
       float g8[8];
 #pragma unroll
@@ -942,7 +1017,7 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
           const int ch = 4 * hf + c4;
-          p8_f16(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
+          p8<W>(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
         }
         tmem_st_x16(pslot + 16u * hf, pk);
       }
@@ -993,9 +1068,9 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
                   wB = eB == -INFINITY ? 0.f : exp2f(eB - M);
       const float L = (w1 * l1 + wA * lA) + wB * lB;
       const float invL = 1.f / L;
-      const float vsc = v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
+      const float vsc = W ? 1.f : v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
       const float wAo = wA * vsc, wBo = wB * vsc;
-      float* orow = p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
+      float* orow = W ? nullptr : p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t oa[32], ob[32];
@@ -1014,7 +1089,14 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) ob[x] = 0u;
         }
-        if (row_valid) {
+        if constexpr (W) {
+          if (row_valid) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              oa[x] = __float_as_uint((wAo * __uint_as_float(oa[x]) + wBo * __uint_as_float(ob[x])) * invL);
+            store_bf16x32(p.out16 + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D + c0, oa);
+          }
+        } else if (row_valid) {
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             float4 res;
@@ -1112,6 +1194,23 @@ __global__ void __launch_bounds__(D) combine_kernel(const P2Params p) {
 }
 
 template <int D>
+cudaError_t launch_window_d(const P2Params& prm, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  const int grid = prm.s.BH() * prm.s.nblk();
+  cudaError_t e;
+  if constexpr (D <= 128) {
+    const int smem = P2DualCfg<D>::kSmem;
+    if ((e = cudaFuncSetAttribute(pass2_dual_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+      return e;
+    pass2_dual_kernel<D, true><<<grid, P2DualCfg<D>::kThreads, smem, st>>>(prm, km, vm);
+  } else {
+    const int smem = P2Cfg<D>::kSmem;
+    if ((e = cudaFuncSetAttribute(pass2_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    pass2_kernel<D, true><<<grid, kThreads, smem, st>>>(prm, km, vm);
+  }
+  return cudaGetLastError();
+}
+
+template <int D>
 cudaError_t launch_d(const P2Params& prm, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   const int grid = prm.s.BH() * prm.s.nblk();
   cudaError_t e;
@@ -1154,6 +1253,29 @@ cudaError_t launch_pass2_order(const Shape& s, const Workspace& ws, cudaStream_t
   if (n > (size_t)kMaxRanked) return cudaSuccess;  // pass 2 keeps the position order
   rank_kernel<<<1, 1024, 0, st>>>(ws.hot_count, (int)n, ws.p2_order);
   return cudaGetLastError();
+}
+
+cudaError_t launch_window(const Shape& s, const void* q, const void* k, const void* v, int window, int sinks, void* out,
+                          float* lse, cudaStream_t st) {
+  CUtensorMap km, vm;
+  if (!make_kv_map(&km, k, s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false) ||
+      !make_kv_map(&vm, v, s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false))
+    return cudaErrorInvalidValue;
+  P2Params prm{};
+  prm.s = s;
+  prm.q = (const uint16_t*)q;
+  prm.lse = lse;
+  prm.err = device_error_word();
+  prm.nsplit = 1;
+  prm.window = window;
+  prm.sinks = sinks;
+  prm.out16 = (uint16_t*)out;
+  switch (s.d) {
+    case 64: return launch_window_d<64>(prm, km, vm, st);
+    case 128: return launch_window_d<128>(prm, km, vm, st);
+    case 256: return launch_window_d<256>(prm, km, vm, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_pass2(const Shape& s, const void* q, const void* k, const void* v, const Workspace* ws, float* out,
