@@ -16,15 +16,15 @@
 //   into FP16's range.  P is rounded to FP16 (2^-11), lifted by 2^6 so that weights
 //   down to 2^-30 of the row's largest keep a value; l sums the FP32 weights.
 //
-// Split: every warp works for itself.  The units (32 keys of one KV head, one
-// contiguous half page) of all sequences, heads and row blocks form one list, which is
-// cut evenly over the warps of the GPU, so lengths need not be alike and no length is
-// read on the host.  A warp streams its units through a ring of its own with bulk
-// copies (no barrier with other warps), keeps its own running maximum and sum, and
-// moves the maximum only when a score exceeds it by 8 (log2 units).  An item (sequence,
-// head, row block) that one warp holds entirely is written out at once; otherwise the
-// parts go to the workspace, the warps of a CTA that works on one item joined
-// first, and a second kernel joins them in order, so results do not depend on timing.
+// Split: the units (32 keys of one KV head, one contiguous half page) of all sequences,
+// heads and row blocks form one list, cut evenly over the CTAs, one per SM, and again
+// over each CTA's warps, so lengths need not be alike and no length is read on the host.
+// Every warp works for itself: it streams its units through a ring of its own with bulk
+// copies (no barrier with other warps), keeps its own running maximum and sum, and moves
+// the maximum only when a score exceeds it by 8 (log2 units).  An item (sequence, head,
+// row block) that one warp holds entirely is written out at once; then the CTA joins its
+// warps' parts of the others in order, and a second kernel those that span CTAs, so
+// results do not depend on timing.
 #include <cmath>
 
 #include "../../include/apa.h"
@@ -57,25 +57,30 @@ struct DecodeParams {
   int* err;
   int nstages;
   // workspace
-  int* pref;       // [B + 1] units before each sequence (of one head and row block)
-  float2* part_ml; // [slots][rows] (m, l)
-  float* part_o;   // [slots][rows][d]
+  int* pref;        // [B + 1] units before each sequence (of one head and row block)
+  float2* part_ml;  // [slots][rows] (m, l): slots 2 cta + 1 and 2 cta are the CTA's part of the item
+  float* part_o;    // [slots][rows][d]      that ends in it, and of the one that goes on behind it;
+                    // slot 2 kCtas + warp is a warp's part of an item that ends in it
 };
 
-// Registers set the number of warps: O takes d * NT / 4 per thread, Q's fragments
-// d * NT / 8.
-template <int D, int NT>
+// kRows rows share the keys: 8 per n = 8 tile, or 4, which then take a tile of V^T P^T
+// twice (see there).  Registers set the number of warps.
+template <int D, int ROWS>
 struct DecCfg {
-  static constexpr int kRegs = D * NT * 3 / 8;
-  static constexpr int W = kRegs <= 64 ? 16 : kRegs <= 96 ? 12 : 8;
-  static constexpr int kRows = 8 * NT;
+  static constexpr int kRows = ROWS;
+  static constexpr int NT = ROWS < 8 ? 1 : ROWS / 8;
+  static constexpr bool kQuad = ROWS == 4;
+  static constexpr int kAcc = kQuad ? D / 32 : D / 16;   // product tiles of O^T per n tile
+  static constexpr int kRegs = (kAcc * 4 + D / 8) * NT;  // O and Q
+  static constexpr int W = D == 256 ? 8 : kRegs <= 48 ? 16 : kRegs <= 96 ? 12 : 8;  // (d = 256: two stages must fit)
   static constexpr int kUnitBytes = 36 * D;
+  static constexpr int kScaleBytes = 8 * D;  // a unit's V scales as FP16 pairs, per warp
   static constexpr int kMaxStages = 6;
-  static constexpr int kSlots = 2 * kCtas * W;
+  static constexpr int kSlots = kCtas * (2 + W);
   static constexpr int kBarBytes = W * kMaxStages * 8 + 16;
   static constexpr int kMergeBytes = W * kRows * (D + 2) * 4;
   static int stages(int B) {
-    const int room = 232448 - kBarBytes - (B + 1) * 4 - 256;  // (256: the static arrays)
+    const int room = 232448 - W * kScaleBytes - kBarBytes - (B + 1) * 4 - 1536;  // (1536: the static arrays)
     const int n = room / (W * kUnitBytes);
     return n > kMaxStages ? kMaxStages : n;
   }
@@ -83,7 +88,7 @@ struct DecCfg {
     const int r = stages(B) * W * kUnitBytes;
     return r > kMergeBytes ? r : kMergeBytes;
   }
-  static int smem(int B) { return ring_bytes(B) + kBarBytes + (B + 1) * 4; }
+  static int smem(int B) { return ring_bytes(B) + W * kScaleBytes + kBarBytes + (B + 1) * 4; }
   static size_t ws_bytes(int B) {
     return align256((size_t)(B + 1) * 4) + align256((size_t)kSlots * kRows * 8) + (size_t)kSlots * kRows * D * 4;
   }
@@ -106,7 +111,6 @@ struct SeqUnits {
     }
     n = n_sink + (len + kUnit - 1) / kUnit - lo;
   }
-  __device__ __forceinline__ int key(int u) const { return (u < n_sink ? u : lo + u - n_sink) * kUnit; }
 };
 
 // The list of units: sequence, then head, then row block, then the item's units in order.
@@ -114,9 +118,25 @@ struct Item {
   int b, h, rb;
   long long first, end;  // the item's units in the list
 };
-__device__ __forceinline__ long long warp_first(long long total, int w, int nwarps) { return total * w / nwarps; }
+// x / n for x >= 0 below 2^63; nearly always a 32-bit division.
+__device__ __forceinline__ long long quotient(long long x, int n) {
+  if (((unsigned long long)x >> 32) == 0) return (unsigned)x / (unsigned)n;
+  return x / n;
+}
+// n things in k nearly equal runs, the longer ones first.
+struct Cut {
+  long long q;
+  int r;
+  __device__ __forceinline__ Cut(long long n, int k) : q(quotient(n, k)) { r = (int)(n - q * k); }
+  __device__ __forceinline__ long long first(int i) const { return q * i + min(i, r); }
+  __device__ __forceinline__ int of(long long x) const {  // the run that holds x < n
+    const long long y = r * (q + 1);
+    if (x < y) return (int)(q < 0x7FFFFFFF ? quotient(x, (int)q + 1) : x / (q + 1));
+    return r + (int)(q < 0x7FFFFFFF ? quotient(x - y, (int)q) : (x - y) / q);
+  }
+};
 __device__ __forceinline__ Item find_item(const int* pref, int B, int heads_rb, int nrb, long long x) {
-  const int y = (int)(x / heads_rb);
+  const int y = (int)quotient(x, heads_rb);
   int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -129,7 +149,7 @@ __device__ __forceinline__ Item find_item(const int* pref, int B, int heads_rb, 
   it.b = lo;
   const int n = pref[lo + 1] - pref[lo];
   const long long base = (long long)pref[lo] * heads_rb;
-  const int k = (int)((x - base) / n);
+  const int k = (int)quotient(x - base, n);
   it.h = k / nrb;
   it.rb = k % nrb;
   it.first = base + (long long)k * n;
@@ -139,7 +159,7 @@ __device__ __forceinline__ Item find_item(const int* pref, int B, int heads_rb, 
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -170,25 +190,19 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+template <typename T>
+__device__ __forceinline__ T lds(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+
+// The channel of o[t][.][2 i + k] in lane (g, c), and the row of the block (of n tile nt).
+template <bool QUAD>
+__device__ __forceinline__ int channel_of(int t, int i, int g, int c) {
+  return QUAD ? 32 * t + 16 * i + 8 * (c >> 1) + g : 16 * ((t & ~1) + i) + 8 * (t & 1) + g;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+template <bool QUAD>
+__device__ __forceinline__ int row_of(int nt, int c, int k) {
+  return QUAD ? (2 * c + k) & 3 : 8 * nt + 2 * c + k;
 }
 
 template <bool F16>
@@ -198,25 +212,33 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, int D, int b, i
   p.out[row * D + ch] = (uint16_t)pack2<F16>(v, 0.f);
 }
 
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const DecodeParams p) {
-  using C = DecCfg<D, NT>;
-  constexpr int W = C::W, kRows = C::kRows;
+struct Seg {  // an item that a warp holds units of; counted from the CTA's first unit
+  int first, end, b, h, rb;
+};
+
+template <int D, int ROWS, bool F16>
+__global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(const DecodeParams p) {
+  using C = DecCfg<D, ROWS>;
+  constexpr int W = C::W, kRows = C::kRows, NT = C::NT, kAcc = C::kAcc;
+  constexpr bool kQuad = C::kQuad;
   constexpr int kHalves = D == 256 ? 2 : 1;      // 128-channel halves of a K row
   constexpr int kSteps = D / 16 / kHalves;       // products of 16 channels per half
   constexpr int kTiles = D / 16;                 // 16-channel tiles of V
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int ring = p.nstages * W * C::kUnitBytes > C::kMergeBytes ? p.nstages * W * C::kUnitBytes : C::kMergeBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + ring) + warp * C::kMaxStages;
-  int* abort_flag = reinterpret_cast<int*>(smem + ring + W * C::kMaxStages * 8);
-  int* pref = reinterpret_cast<int*>(smem + ring + C::kBarBytes);
+  uint8_t* scales = smem + ring + warp * C::kScaleBytes;
+  uint8_t* behind = smem + ring + W * C::kScaleBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(behind) + warp * C::kMaxStages;
+  int* abort_flag = reinterpret_cast<int*>(behind + W * C::kMaxStages * 8);
+  int* pref = reinterpret_cast<int*>(behind + C::kBarBytes);
   const uint32_t bar0 = smem_u32(bars), stage0 = smem_u32(smem) + warp * p.nstages * C::kUnitBytes;
 
   if (lane < C::kMaxStages) mbar_init(bar0 + 8 * lane, 1);
   if (tid == 0) *abort_flag = 0;
   fence_mbar_init();
 
+  __shared__ Seg seg[W][2];  // each warp's first and last item
   // ---- units before each sequence: every CTA scans the lengths for itself
   {
     __shared__ int wsum[W];
@@ -256,74 +278,85 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const 
 
   const int G = p.Hq / p.Hkv, R = G * p.Nq, nrb = (R + kRows - 1) / kRows, heads_rb = p.Hkv * nrb;
   const long long total = (long long)pref[p.B] * heads_rb;
-  const int nwarps = gridDim.x * W, gw = blockIdx.x * W + warp;
-  const long long x0 = warp_first(total, gw, nwarps), x1 = warp_first(total, gw + 1, nwarps);
-  const long long c0 = warp_first(total, blockIdx.x * W, nwarps), c1 = warp_first(total, (blockIdx.x + 1) * W, nwarps);
-  // one item for the whole CTA, in more than one warp: the warps are joined here
-  bool alone = c1 - c0 > 1 && x1 - x0 < c1 - c0;
-  if (alone) alone = find_item(pref, p.B, heads_rb, nrb, c0).end >= c1;
-  const bool joined = __syncthreads_and(alone);
+  const Cut ctas(total, kCtas);
+  const long long c0 = ctas.first(blockIdx.x);
+  const int cta_count = (int)(ctas.first(blockIdx.x + 1) - c0);
+  if (cta_count == 0) return;
+  const Cut warps(cta_count, W);
+  const int w0 = (int)warps.first(warp), count = (int)warps.first(warp + 1) - w0;
+  const long long x0 = c0 + w0;
 
-  bool ok = true;
-  float o[kTiles][NT][4];
+  bool ok = true, waiting = false;  // waiting: the last item is in o, m, l for the CTA to join
+  // o[t][.][0 .. 1] and [2 .. 3]: the columns 2c, 2c + 1 of the rows g and g + 8 of product tile t
+  // (channel_of, row_of)
+  float o[kAcc][NT][4];
   float m[NT][2], l[NT][2];
 
-  if (x1 > x0) {
-    // ---- producer cursor: unit px of the list goes into stage ps
-    Item pit = find_item(pref, p.B, heads_rb, nrb, x0);
-    SeqUnits psu(p, p.lens[pit.b]);
-    long long px = x0;
-    int ps = 0, tbase = -64, tid_page = 0;  // this lane's entry of the 32 table entries from tbase
+  if (count > 0) {
+    // Units are counted from the warp's first one, x0, from here on.
+    // ---- producer cursor: unit px, of an item [pfirst, pend), goes into stage ps next
+    int px = 0, pfirst, pend, pb, plo, psink, plast;
+    const uint8_t* head;  // the KV head's part of page 0
+    auto enter = [&]() {
+      const Item it = find_item(pref, p.B, heads_rb, nrb, x0 + px);
+      const SeqUnits su(p, p.lens[it.b]);
+      pb = it.b;
+      plo = su.lo - su.n_sink;
+      psink = su.n_sink;
+      plast = (su.len - 1) / kTile;
+      pfirst = (int)(it.first - x0);
+      pend = (int)(it.end - x0);
+      head = p.pages + (size_t)it.h * page_head_bytes(D);
+    };
+    enter();
+    int ps = 0, tbase = -64, entry = 0;  // entry: this lane's of the 32 table entries from tbase
     auto issue = [&]() {
-      if (px >= pit.end) {
-        pit = find_item(pref, p.B, heads_rb, nrb, px);
-        psu = SeqUnits(p, p.lens[pit.b]);
+      if (px == pend) {
+        enter();
         tbase = -64;
       }
-      const int key = psu.key((int)(px - pit.first)), e = key / kTile;
-      if (e < tbase || e >= tbase + 32) {
+      const int u = px - pfirst, half = u < psink ? u : u + plo, e = half / 2;
+      if ((unsigned)(e - tbase) >= 32u) {
         tbase = e;
-        const int last = (psu.len - 1) / kTile;
-        tid_page = e + lane <= last ? p.table[(size_t)pit.b * p.max_pages + e + lane] : 0;
-        if (tid_page < 0 || tid_page >= p.num_pages) {
-          // reported only for entries of visible keys: those that are really used, below
-          tid_page = -1;
-        }
+        entry = e + lane <= plast ? p.table[(size_t)pb * p.max_pages + e + lane] : 0;
       }
-      int page = __shfl_sync(0xffffffffu, tid_page, e - tbase);
+      int page = __shfl_sync(0xffffffffu, entry, e - tbase);
       if (lane == 0) {
-        if (page < 0) {
+        if ((unsigned)page >= (unsigned)p.num_pages) {  // reads page 0, and is reported
           if (p.err) atomicCAS(p.err, 0, APA_DEVERR_BOUNDS);
           page = 0;
         }
-        const uint8_t* src = p.pages + ((size_t)page * p.Hkv + pit.h) * page_head_bytes(D) +
-                             (key % kTile / kUnit) * C::kUnitBytes;
         mbar_arrive_expect_tx(bar0 + 8 * ps, C::kUnitBytes);
-        bulk_g2s(stage0 + ps * C::kUnitBytes, src, C::kUnitBytes, bar0 + 8 * ps);
+        bulk_g2s(stage0 + ps * C::kUnitBytes,
+                 head + (size_t)page * p.Hkv * page_head_bytes(D) + (half & 1) * C::kUnitBytes, C::kUnitBytes,
+                 bar0 + 8 * ps);
       }
       ++px;
       ps = ps + 1 == p.nstages ? 0 : ps + 1;
     };
-    for (int i = 0; i < p.nstages && px < x1; ++i) issue();
+    for (int i = 0; i < p.nstages && px < count; ++i) issue();
 
-    long long x = x0;
-    int st = 0;
+    int x = 0, st = 0;
     uint32_t parity = 0;
-    while (x < x1 && ok) {
+    while (x < count) {
       // ---- one segment: the units of one item that are this warp's
-      const Item it = find_item(pref, p.B, heads_rb, nrb, x);
+      const Item it = find_item(pref, p.B, heads_rb, nrb, x0 + x);
       const SeqUnits su(p, p.lens[it.b]);
-      const long long seg_end = min(it.end, x1);
-      const int r0 = it.rb * kRows;
+      const int len = su.len, sink = su.n_sink, lo = su.lo - su.n_sink, r0 = it.rb * kRows;
+      if (lane == 0) {
+        const Seg sg{(int)(it.first - c0), (int)(it.end - c0), it.b, it.h, it.rb};
+        if (x == 0) seg[warp][0] = sg;
+        seg[warp][1] = sg;
+      }
+      const int first = (int)(it.first - x0), seg_end = min((int)min(it.end - x0, (long long)count), count);
 
       // Q rows as the B operand: lane (g, c) has row 8 nt + g, channels 128 hf + (D/4 or 32) c + 4 s ..
       uint32_t qf[NT][kHalves][kSteps][2];
       float rf[NT][2];  // score factor of rows 2c, 2c + 1: the power of two back, and k_scale log2(e) / sqrt(d)
-      int pos[NT][2];   // their positions
       const float sc = p.k_scale[it.h] * kLog2e * rsqrtf((float)D);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + 8 * nt + g;
+        const int r = r0 + (kQuad ? g & 3 : 8 * nt + g);
         uint2 raw[kHalves][kSteps];
         float amax = 0.f;
         const uint16_t* src =
@@ -354,64 +387,65 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const 
           }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          rf[nt][k] = __shfl_sync(0xffffffffu, down, (2 * c + k) * 4) * sc;
-          const int rr = r0 + 8 * nt + 2 * c + k;
-          pos[nt][k] = su.len - p.Nq + (rr < R ? rr / G : p.Nq - 1);
+          rf[nt][k] = __shfl_sync(0xffffffffu, down, (kQuad ? (2 * c + k) & 3 : 2 * c + k) * 4) * sc;
           m[nt][k] = -INFINITY;
           l[nt][k] = 0.f;
         }
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+        for (int t = 0; t < kAcc; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[t][nt][k] = 0.f;
       }
-      const int pmin = su.len - p.Nq + r0 / G;              // positions of the block's first row
-      const int pmax = su.len - p.Nq + min(r0 + kRows - 1, R - 1) / G;  // and of its last
+      const int pmin = len - p.Nq + r0 / G;                             // positions of the block's first row
+      const int pmax = len - p.Nq + min(r0 + kRows - 1, R - 1) / G;  // and of its last
 
       for (; x < seg_end; ++x) {
         if (!__all_sync(0xffffffffu, mbar_test_wait(bar0 + 8 * st, parity))) {
           ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, parity, abort_flag, p.err));
           if (!ok) break;
         }
-        const uint32_t unit = stage0 + st * C::kUnitBytes;
-        const int j0 = su.key((int)(x - it.first));
+        const uint8_t* unit = smem + (warp * p.nstages + st) * C::kUnitBytes;
+        const int u = x - first, j0 = (u < sink ? u : u + lo) * kUnit;
+        // ---- S^T = K Q^T.  Rows g and g + 8 of the product are keys 4 (g/2) + g%2 and that + 2, so
+        // that a lane's four keys of V^T below are neighbours.  Both blocks go side by side.
         float s[2][NT][4];
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
+        for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[mb][nt][k] = 0.f;
-          // rows r = g and g + 8 of the product are keys 4 (g/2) + g%2 and that + 2, so that
-          // a lane's four keys of V^T below are neighbours
-          const uint32_t blk = unit + mb * blk_bytes(D);
-          const int kg = 4 * (g >> 1) + (g & 1);
+        const int kg = 4 * (g >> 1) + (g & 1);
 #pragma unroll
-          for (int hf = 0; hf < kHalves; ++hf) {
-            uint32_t wa[4], wb[4], sa, sb;
-            const uint32_t ka = blk + kg * (D / 2) + 64 * hf + c * (2 * kSteps);
-            if constexpr (kSteps == 8) {
-              const uint4 a = lds128(ka), b = lds128(ka + D);
-              wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
-              wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
-              const uint32_t sp = blk + blk_ks(D) + kg * (D / 16) + 8 * hf + 2 * c;
-              sa = e4m3x2(lds16(sp));
-              sb = e4m3x2(lds16(sp + 2 * (D / 16)));
-            } else {
-              const uint2 a = lds64(ka), b = lds64(ka + D);
-              wa[0] = a.x, wa[1] = a.y, wb[0] = b.x, wb[1] = b.y;
-              const uint32_t sp = blk + blk_ks(D) + kg * (D / 16) + c;
-              sa = e4m3x2(lds8(sp));
-              sb = e4m3x2(lds8(sp + 2 * (D / 16)));
+        for (int hf = 0; hf < kHalves; ++hf) {
+          uint32_t wk[2][2][4], sk[2][2];  // [block][key kg, kg + 2]
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint8_t* blk = unit + mb * blk_bytes(D);
+              const uint8_t* ka = blk + (kg + 2 * i) * (D / 2) + 64 * hf + c * (2 * kSteps);
+              const uint8_t* sp = blk + blk_ks(D) + (kg + 2 * i) * (D / 16);
+              if constexpr (kSteps == 8) {
+                const uint4 a = lds<uint4>(ka);
+                wk[mb][i][0] = a.x, wk[mb][i][1] = a.y, wk[mb][i][2] = a.z, wk[mb][i][3] = a.w;
+                sk[mb][i] = e4m3x2(lds<uint16_t>(sp + 8 * hf + 2 * c));
+              } else {
+                const uint2 a = lds<uint2>(ka);
+                wk[mb][i][0] = a.x, wk[mb][i][1] = a.y;
+                sk[mb][i] = e4m3x2(lds<uint8_t>(sp + c));
+              }
             }
 #pragma unroll
-            for (int w = 0; w < kSteps / 2; ++w) {
+          for (int w = 0; w < kSteps / 2; ++w)
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb) {
               // a lane's words 0, 1 (16 codes) share its first scale, words 2, 3 the second
-              const uint32_t fa = __byte_perm(sa, sa, w < 2 ? 0x1010 : 0x3232);
-              const uint32_t fb = __byte_perm(sb, sb, w < 2 ? 0x1010 : 0x3232);
+              const uint32_t fa = __byte_perm(sk[mb][0], 0, w < 2 ? 0x1010 : 0x3232);
+              const uint32_t fb = __byte_perm(sk[mb][1], 0, w < 2 ? 0x1010 : 0x3232);
               uint32_t ha[4], hb[4];
-              e2m1x8(wa[w], ha);
-              e2m1x8(wb[w], hb);
+              e2m1x8(wk[mb][0][w], ha);
+              e2m1x8(wk[mb][1][w], hb);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 ha[k] = hmul2(ha[k], fa);
@@ -423,31 +457,36 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const 
                 mma_f16(s[mb][nt], ha[2], hb[2], ha[3], hb[3], qf[nt][hf][2 * w + 1][0], qf[nt][hf][2 * w + 1][1]);
               }
             }
-          }
         }
-        // ---- softmax: s[mb][nt] = keys kg (0, 1) and kg + 2 (2, 3) of block mb, rows 2c and 2c + 1
-        const bool edge = j0 + kUnit - 1 > pmin || (p.window && j0 <= pmax - p.window && j0 + kUnit > p.sinks);
+        // ---- softmax: s[mb][nt] = keys kg (0, 1) and kg + 2 (2, 3) of block mb, rows 2c and 2c + 1,
+        // still without the row's factor rf
+        if (j0 + kUnit - 1 > pmin || (p.window && j0 <= pmax - p.window && j0 + kUnit > p.sinks)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < 4; ++k) {
+              const int rr = r0 + row_of<kQuad>(nt, c, k & 1), pr = rr < R ? len - p.Nq + rr / G : pmax;
+#pragma unroll
+              for (int mb = 0; mb < 2; ++mb) {
+                const int j = j0 + 16 * mb + 4 * (g >> 1) + (g & 1) + (k & 2);
+                if (j > pr || (p.window && j <= pr - p.window && j >= p.sinks)) s[mb][nt][k] = -INFINITY;
+              }
+            }
+        }
+        float top[NT][2];  // the largest of this lane's scores (rf > 0, so of the scaled ones too)
         bool lift = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float y = s[mb][nt][k] * rf[nt][k & 1];
-              if (edge) {
-                const int j = j0 + 16 * mb + 4 * (g >> 1) + (g & 1) + (k & 2), pr = pos[nt][k & 1];
-                if (j > pr || (p.window && j <= pr - p.window && j >= p.sinks)) y = -INFINITY;
-              }
-              s[mb][nt][k] = y;
-              lift |= y > m[nt][k & 1] + kTauDec;
-            }
+          for (int k = 0; k < 2; ++k) {
+            top[nt][k] = rf[nt][k] * fmaxf(max3(s[0][nt][k], s[0][nt][k + 2], s[1][nt][k]), s[1][nt][k + 2]);
+            lift |= top[nt][k] > m[nt][k] + kTauDec;
+          }
         if (__any_sync(0xffffffffu, lift)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float y = fmaxf(fmaxf(s[0][nt][k], s[0][nt][k + 2]), fmaxf(s[1][nt][k], s[1][nt][k + 2]));
+              float y = top[nt][k];
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
               if (y > m[nt][k]) {
@@ -455,13 +494,13 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const 
                 m[nt][k] = y;
                 l[nt][k] *= f;
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                  o[t][nt][k] *= f;
-                  o[t][nt][k + 2] *= f;
-                }
+                for (int t = 0; t < kAcc; ++t)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) o[t][nt][2 * i + k] *= f;
               }
             }
         }
+        // P^T: pf[mb][nt] = the weights of row g for keys 4c, 4c + 1 and 4c + 2, 4c + 3
         uint32_t pf[2][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -470,43 +509,88 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const 
           const float b1 = m[nt][1] == -INFINITY ? 0.f : kLift - m[nt][1];
 #pragma unroll
           for (int mb = 0; mb < 2; ++mb) {
-            const float p0 = ex2_approx(s[mb][nt][0] + b0), p1 = ex2_approx(s[mb][nt][1] + b1);
-            const float p2 = ex2_approx(s[mb][nt][2] + b0), p3 = ex2_approx(s[mb][nt][3] + b1);
+            const float p0 = ex2_approx(fmaf(s[mb][nt][0], rf[nt][0], b0));
+            const float p1 = ex2_approx(fmaf(s[mb][nt][1], rf[nt][1], b1));
+            const float p2 = ex2_approx(fmaf(s[mb][nt][2], rf[nt][0], b0));
+            const float p3 = ex2_approx(fmaf(s[mb][nt][3], rf[nt][1], b1));
             l[nt][0] += p0 + p2;
             l[nt][1] += p1 + p3;
             pf[mb][nt][0] = transpose8(pack2<true>(p0, p1));
             pf[mb][nt][1] = transpose8(pack2<true>(p2, p3));
           }
         }
-        // ---- O^T += V^T P^T
+        // ---- O^T += V^T P^T.  A code byte holds channels g and 8 + g of a tile for one key; its
+        // FP16 pair goes into the product as it is, as two steps of the summed axis, against P
+        // with zeros at every other step: (P, 0) gives the channels g, (0, P) the channels 8 + g.
+        // That spares the integer pipe the permutes that pairing two keys would take, for twice
+        // the products; with up to four rows both forms of P share one product's eight columns.
+        // Rows g and g + 8 of a product are tiles t and t + 1.
+        // The scales come as FP16 pairs (s, s), converted once per warp: word i of a block holds
+        // those of keys 4 (i / kTiles) .. + 3 for tile i % kTiles.  Keys past the end: whatever
+        // the page holds there (NaN too) counts as 0.
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int i = lane; i < 4 * kTiles; i += 32) {
+            const int kc = i / kTiles, left = len - (j0 + 16 * mb + 4 * kc);
+            uint32_t w = lds<uint32_t>(unit + mb * blk_bytes(D) + blk_vs(D) + 4 * i);
+            if (left < 4) w &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            const uint32_t f0 = e4m3x2(w & 0xFFFFu), f1 = e4m3x2(w >> 16);
+            *reinterpret_cast<uint4*>(scales + 4 * D * mb + 16 * (4 * (i % kTiles) + kc)) =
+                make_uint4(__byte_perm(f0, 0, 0x1010), __byte_perm(f0, 0, 0x3232), __byte_perm(f1, 0, 0x1010),
+                           __byte_perm(f1, 0, 0x3232));
+          }
+        __syncwarp();
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
-          const uint32_t blk = unit + mb * blk_bytes(D);
-          // keys past the end: whatever scales the page holds there (NaN too) count as 0
-          const int left = su.len - (j0 + 16 * mb + 4 * c);
-          const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+          const uint8_t* blk = unit + mb * blk_bytes(D);
+          // [keys 4c, 4c + 1 | 4c + 2, 4c + 3][(P, 0) of both, (0, P) of both]; with four rows lanes
+          // g < 4 take (P, 0) and the others (0, P)
+          uint32_t pz[NT][2][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t w = pf[mb][nt][i];
+              if constexpr (kQuad) {
+                pz[nt][i][0] = __byte_perm(w, 0, g < 4 ? 0x4410 : 0x1044);
+                pz[nt][i][1] = __byte_perm(w, 0, g < 4 ? 0x4432 : 0x3244);
+              } else {
+                pz[nt][i][0] = w & 0xFFFFu;
+                pz[nt][i][1] = w >> 16;
+                pz[nt][i][2] = w << 16;
+                pz[nt][i][3] = w & 0xFFFF0000u;
+              }
+            }
 #pragma unroll
           for (int tq = 0; tq < kTiles / 4; ++tq) {
-            const uint4 vw = lds128(blk + blk_v(D) + 512 * tq + 16 * lane);
-            const uint4 vs = lds128(blk + blk_vs(D) + 4 * (c * kTiles + 4 * tq));
-            const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w}, s4[4] = {vs.x, vs.y, vs.z, vs.w};
+            const uint4 vw = lds<uint4>(blk + blk_v(D) + 512 * tq + 16 * lane);
+            const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t h[4];
-              e2m1x8(w4[k], h);  // h[j]: key 4c + j, channels g (low) and g + 8
-              const uint32_t sw = s4[k] & keep, f0 = e4m3x2(sw & 0xFFFFu), f1 = e4m3x2(sw >> 16);
-              const uint32_t a0 = hmul2(__byte_perm(h[0], h[1], 0x5410), f0);
-              const uint32_t a1 = hmul2(__byte_perm(h[0], h[1], 0x7632), f0);
-              const uint32_t a2 = hmul2(__byte_perm(h[2], h[3], 0x5410), f1);
-              const uint32_t a3 = hmul2(__byte_perm(h[2], h[3], 0x7632), f1);
+            for (int k = 0; k < 4; k += 2) {
+              const int t = 4 * tq + k;
+              const uint4 sa = lds<uint4>(scales + 4 * D * mb + 16 * (4 * t + c));
+              const uint4 sb = lds<uint4>(scales + 4 * D * mb + 16 * (4 * t + 4 + c));
+              uint32_t ha[4], hb[4];
+              e2m1x8(w4[k], ha);  // [key 4c + i]
+              e2m1x8(w4[k + 1], hb);
+              ha[0] = hmul2(ha[0], sa.x), ha[1] = hmul2(ha[1], sa.y), ha[2] = hmul2(ha[2], sa.z), ha[3] = hmul2(ha[3], sa.w);
+              hb[0] = hmul2(hb[0], sb.x), hb[1] = hmul2(hb[1], sb.y), hb[2] = hmul2(hb[2], sb.z), hb[3] = hmul2(hb[3], sb.w);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(o[4 * tq + k][nt], a0, a1, a2, a3, pf[mb][nt][0], pf[mb][nt][1]);
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  float* od = o[kQuad ? t / 2 : t][nt];
+                  mma_f16(od, ha[2 * i], hb[2 * i], ha[2 * i + 1], hb[2 * i + 1], pz[nt][i][0], pz[nt][i][1]);
+                  if constexpr (!kQuad)
+                    mma_f16(o[t + 1][nt], ha[2 * i], hb[2 * i], ha[2 * i + 1], hb[2 * i + 1], pz[nt][i][2], pz[nt][i][3]);
+                }
             }
           }
         }
         st = st + 1 == p.nstages ? (parity ^= 1, 0) : st + 1;
         __syncwarp();
-        if (px < x1) issue();
+        if (px < count) issue();
       }
       if (!ok) break;
 
@@ -517,47 +601,48 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const 
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], d);
-      if (joined) break;  // (its only segment)
-      const long long a = x0;
-      if (it.first >= a && it.end <= x1) {
+      waiting = false;
+      if (first >= 0 && first + (int)(it.end - it.first) <= count) {
+        // the whole item
         const float vsc = p.v_scale[it.h];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int r = r0 + 8 * nt + 2 * c + k;
+            const int r = r0 + row_of<kQuad>(nt, c, k);
             if (r >= R) continue;
             const float inv = l[nt][k] == 0.f ? 0.f : vsc / l[nt][k];
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              write_row<F16>(p, D, it.b, it.h, r, 16 * t + g, o[t][nt][k] * inv);
-              write_row<F16>(p, D, it.b, it.h, r, 16 * t + 8 + g, o[t][nt][k + 2] * inv);
-            }
+            for (int t = 0; t < kAcc; ++t)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                write_row<F16>(p, D, it.b, it.h, r, channel_of<kQuad>(t, i, g, c), o[t][nt][2 * i + k] * inv);
             if (g == 0 && p.lse)
               p.lse[((size_t)it.b * p.Hq + it.h * G + r % G) * p.Nq + r / G] =
                   l[nt][k] == 0.f ? -INFINITY : kLn2 * (m[nt][k] - kLift + log2f(l[nt][k]));
           }
-      } else {
-        // slot 2 gw: the warp's last (or only) item; 2 gw + 1: one that began before and ends here
-        const size_t slot = 2 * (size_t)gw + (it.end < x1 ? 1 : 0);
+      } else if (x < count) {
+        // one that began before this warp and ends in it, while the warp goes on to others
+        const size_t slot = 2 * kCtas + (size_t)blockIdx.x * W + warp;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const size_t row = slot * kRows + 8 * nt + 2 * c + k;
+            const size_t row = slot * kRows + row_of<kQuad>(nt, c, k);
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              p.part_o[row * D + 16 * t + g] = o[t][nt][k];
-              p.part_o[row * D + 16 * t + 8 + g] = o[t][nt][k + 2];
-            }
+            for (int t = 0; t < kAcc; ++t)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) p.part_o[row * D + channel_of<kQuad>(t, i, g, c)] = o[t][nt][2 * i + k];
             if (g == 0) p.part_ml[row] = make_float2(m[nt][k], l[nt][k]);
           }
+      } else {
+        waiting = true;
       }
     }
     if (!ok) {
       // a wait gave up: the copies in flight land before the CTA ends (waited with a limit again)
       const unsigned long long t0 = clock64();
-      for (long long y = x; y < px; ++y) {
+      for (; x < px; ++x) {
         while (!mbar_test_wait(bar0 + 8 * st, parity) && clock64() - t0 < APA_WAIT_LIMIT_CYCLES) {
         }
         st = st + 1 == p.nstages ? (parity ^= 1, 0) : st + 1;
@@ -565,145 +650,188 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::W * 32, 1) decode_kernel(const 
     }
   }
 
-  if (joined) {
-    // ---- the CTA's warps, all on one item: joined in order through shared memory
-    if (!__syncthreads_and(ok)) return;
-    float* mo = reinterpret_cast<float*>(smem);                              // [W][rows][D]
-    float2* mml = reinterpret_cast<float2*>(smem + W * kRows * D * 4);       // [W][rows]
-    const bool has = x1 > x0;
+  // ---- the items that are in several warps, or go on in other CTAs: joined in order.  A warp's last
+  // item is in shared memory (the rings are idle now), one that ended in it in the workspace.
+  if (!__syncthreads_and(ok)) return;
+  float* mo = reinterpret_cast<float*>(smem);                         // [W][rows][D]
+  float2* mml = reinterpret_cast<float2*>(smem + W * kRows * D * 4);  // [W][rows]
+  if (waiting) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int row = warp * kRows + 8 * nt + 2 * c + k;
-        if (has) {
+        const int row = warp * kRows + row_of<kQuad>(nt, c, k);
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            mo[row * D + 16 * t + g] = o[t][nt][k];
-            mo[row * D + 16 * t + 8 + g] = o[t][nt][k + 2];
-          }
-        }
-        if (g == 0) mml[row] = has ? make_float2(m[nt][k], l[nt][k]) : make_float2(-INFINITY, 0.f);
+        for (int t = 0; t < kAcc; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) mo[row * D + channel_of<kQuad>(t, i, g, c)] = o[t][nt][2 * i + k];
+        if (g == 0) mml[row] = make_float2(m[nt][k], l[nt][k]);
       }
-    __syncthreads();
-    const Item it = find_item(pref, p.B, heads_rb, nrb, c0);
-    const bool whole = it.first == c0 && it.end == c1;
-    const int r0 = it.rb * kRows;
-    const float vsc = p.v_scale[it.h];
+  }
+  __syncthreads();
+  // the part of item sg that warps .. to of this CTA hold; here: whether the last of it is in the workspace
+  auto join = [&](const Seg& sg, int to, bool here) {
+    const int from = warps.of(max(sg.first, 0)), r0 = sg.rb * kRows;
+    const bool whole = sg.first >= 0 && sg.end <= cta_count;
+    const size_t wslot = (2 * kCtas + (size_t)blockIdx.x * W + to) * kRows;
+    const size_t cslot = (2 * (size_t)blockIdx.x + (sg.end <= cta_count ? 1 : 0)) * kRows;
     for (int i = tid; i < kRows * D; i += W * 32) {
       const int row = i / D, ch = i % D, r = r0 + row;
-      float M = -INFINITY, L = 0.f, acc = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, mml[w * kRows + row].x);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
+      const float2 tail = here ? p.part_ml[wslot + row] : mml[to * kRows + row];
+      float M = tail.x;
+      for (int w = from; w < to; ++w) M = fmaxf(M, mml[w * kRows + row].x);
+      float L = 0.f, acc = 0.f;
+      for (int w = from; w < to; ++w) {
         const float2 ml = mml[w * kRows + row];
         if (ml.y == 0.f) continue;
         const float f = ex2_approx(ml.x - M);
         L = fmaf(f, ml.y, L);
         acc = fmaf(f, mo[(w * kRows + row) * D + ch], acc);
       }
+      if (tail.y != 0.f) {
+        const float f = ex2_approx(tail.x - M);
+        L = fmaf(f, tail.y, L);
+        acc = fmaf(f, here ? p.part_o[(wslot + row) * D + ch] : mo[(to * kRows + row) * D + ch], acc);
+      }
       if (whole) {
         if (r >= R) continue;
-        write_row<F16>(p, D, it.b, it.h, r, ch, L == 0.f ? 0.f : acc * (vsc / L));
+        write_row<F16>(p, D, sg.b, sg.h, r, ch, L == 0.f ? 0.f : acc * (p.v_scale[sg.h] / L));
         if (ch == 0 && p.lse)
-          p.lse[((size_t)it.b * p.Hq + it.h * G + r % G) * p.Nq + r / G] =
+          p.lse[((size_t)sg.b * p.Hq + sg.h * G + r % G) * p.Nq + r / G] =
               L == 0.f ? -INFINITY : kLn2 * (M - kLift + log2f(L));
-      } else {  // in the slot of the CTA's first warp with units
-        const size_t prow = 2 * (((c0 + 1) * nwarps - 1) / total) * kRows + row;
-        p.part_o[prow * D + ch] = acc;
-        if (ch == 0) p.part_ml[prow] = make_float2(M, L);
+      } else {
+        p.part_o[(cslot + row) * D + ch] = acc;
+        if (ch == 0) p.part_ml[cslot + row] = make_float2(M, L);
       }
     }
+  };
+  for (int w = 0; w < W; ++w) {
+    const int a = (int)warps.first(w), e = (int)warps.first(w + 1);
+    if (e == a) break;
+    const Seg s0 = seg[w][0], s1 = seg[w][1];
+    if (s0.end <= e && s0.first < a) join(s0, w, s0.end < e);       // one that ends in warp w
+    if (e == cta_count && s1.end > e) join(s1, w, false);           // one that goes on behind the CTA
   }
 }
 
-// Joins the parts of the items that the first kernel left in more than one: one CTA per
-// query row, a thread per channel, the parts in list order.  Also writes the rows of
-// sequences without keys.
-constexpr int kPartChunk = 256;
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(D) join_kernel(const DecodeParams p) {
-  using C = DecCfg<D, NT>;
-  constexpr int W = C::W, kRows = C::kRows;
-  __shared__ int s_slot[kPartChunk];
-  __shared__ float s_f[kPartChunk], s_l[kPartChunk];
-  __shared__ float red[D / 32];
+// Joins the parts of the items that span several CTAs of the first kernel, in order;
+// also writes the rows of sequences without keys.  WPR warps per query row, a vector of
+// channels per lane, and each warp takes a share of the parts with many loads in flight.
+constexpr int kJoinThreads = 256;
+template <int D, int ROWS, bool F16, int WPR>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p) {
+  using C = DecCfg<D, ROWS>;
+  constexpr int kRows = C::kRows, kPer = kJoinThreads / 32 / WPR;
+  constexpr int kVec = D / 32 < 4 ? D / 32 : 4, kVecs = D / (32 * kVec);  // a lane's channels: kVecs vectors
+  __shared__ float s_m[WPR], s_l[WPR], s_o[WPR > 1 ? WPR : 1][WPR > 1 ? D : 1];
   const int G = p.Hq / p.Hkv, R = G * p.Nq, nrb = (R + kRows - 1) / kRows, heads_rb = p.Hkv * nrb;
-  const int r = blockIdx.x % R, bh = blockIdx.x / R, h = bh % p.Hkv, b = bh / p.Hkv;
-  const int rb = r / kRows, row = r % kRows, tid = threadIdx.x;
-  const size_t orow = ((size_t)b * p.Hq + h * G + r % G) * p.Nq + r / G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+  const int at = blockIdx.x * kPer + warp / WPR;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = p.pref[b + 1] - p.pref[b];
-  if (n == 0) {
-    p.out[orow * D + tid] = 0;
-    if (tid == 0 && p.lse) p.lse[orow] = -INFINITY;
-    return;
+  if (at >= p.B * p.Hkv * R) return;  // (with WPR > 1 the whole CTA)
+  const int r = at % R, bh = at / R, h = bh % p.Hkv, b = bh / p.Hkv, row = r % kRows;
+  const size_t orow = ((size_t)b * p.Hq + h * G + r % G) * p.Nq + r / G;
+  const int before = p.pref[b], n = p.pref[b + 1] - before;
+  int ca = 0, parts = 0;
+  long long u1 = 0;
+  const Cut ctas((long long)p.pref[p.B] * heads_rb, kCtas);
+  if (n > 0) {
+    const long long u0 = (long long)before * heads_rb + (long long)(h * nrb + r / kRows) * n;
+    u1 = u0 + n;
+    ca = ctas.of(u0);
+    parts = ctas.of(u1 - 1) - ca + 1;
+    if (parts == 1) return;  // that CTA wrote it
   }
-  const long long total = (long long)p.pref[p.B] * heads_rb;
-  const int nwarps = kCtas * W;
-  const long long u0 = (long long)p.pref[b] * heads_rb + (long long)(h * nrb + rb) * n, u1 = u0 + n;
-  auto warp_of = [&](long long x) { return (int)(((x + 1) * nwarps - 1) / total); };
-  const int w0 = warp_of(u0), w1 = warp_of(u1 - 1);
-  if (w0 == w1) return;  // one warp had all of it
-  const int ca = w0 / W, cb = w1 / W;
-  if (ca == cb && warp_first(total, ca * W, nwarps) == u0 && warp_first(total, (ca + 1) * W, nwarps) == u1)
-    return;  // one CTA had nothing else
-  // candidates: the slots of warps w0 .. w1 in order; the ones in use are kept
-  float M = -INFINITY, L = 0.f, acc = 0.f;
-  for (int wa = w0; wa <= w1;) {
-    // a chunk of the candidates: thread i looks at warp wa + i
-    const int count = min(w1 - wa + 1, kPartChunk);
-    __syncthreads();
-    float mx = -INFINITY;
-    for (int i = tid; i < count; i += D) {
-      const int w = wa + i, cta = w / W;
-      const long long a = warp_first(total, w, nwarps), e = warp_first(total, w + 1, nwarps);
-      const long long a0 = warp_first(total, cta * W, nwarps), e0 = warp_first(total, (cta + 1) * W, nwarps);
-      int slot = -1;
-      if (a0 >= u0 && e0 <= u1) {
-        // a CTA with this item alone: joined in the slot of its first warp with units
-        const int wf = e0 > a0 ? warp_of(a0) : -1;
-        if (w == wf) slot = 2 * w;
-      } else if (e > a) {
-        slot = 2 * w + (a >= u0 && e > u1 ? 1 : 0);
-      }
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (slot >= 0) ml = p.part_ml[(size_t)slot * kRows + row];
-      s_slot[i] = ml.y == 0.f ? -1 : slot;  // (a NaN sum goes on to the output)
-      s_f[i] = ml.x;
-      s_l[i] = ml.y;
-      mx = fmaxf(mx, ml.x);
+  float acc[kVecs][kVec], M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[v][k] = 0.f;
+  // 32 of this warp's parts at a time: parts sub, sub + WPR, ...
+  for (int i0 = sub; i0 < parts; i0 += 32 * WPR) {
+    const int mine = i0 + lane * WPR;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    size_t prow = 0;
+    if (mine < parts) {
+      const int cta = ca + mine;
+      prow = (2 * (size_t)cta + (u1 <= ctas.first(cta + 1) ? 1 : 0)) * kRows + row;
+      ml = p.part_ml[prow];
     }
-    // the chunk's maximum, then the weights
+    float mx = fmaxf(M, ml.x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    float m2 = M;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) m2 = fmaxf(m2, red[k]);
-    const float fo = M == -INFINITY ? 1.f : ex2_approx(M - m2);  // (nothing summed yet: 0, or NaN)
-    acc *= fo;
+    const float fo = M == mx ? 1.f : ex2_approx(M - mx);
+    const float f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);  // (a NaN sum goes on to the output)
+    M = mx;
     L *= fo;
-    M = m2;
-    for (int i = tid; i < count; i += D) s_f[i] = ex2_approx(s_f[i] - M);
-    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) acc[v][k] *= fo;
+    const int here = min(32, (parts - i0 + WPR - 1) / WPR);
 #pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-      if (s_slot[i] < 0) continue;
-      acc = fmaf(s_f[i], p.part_o[((size_t)s_slot[i] * kRows + row) * D + tid], acc);
-      L = fmaf(s_f[i], s_l[i], L);
+    for (int i = 0; i < here; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, ml.y, i);
+      const float* src = p.part_o + __shfl_sync(0xffffffffu, prow, i) * D;
+      L = fmaf(fi, li, L);
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        if constexpr (kVec == 4) {
+          const float4 y = reinterpret_cast<const float4*>(src)[32 * v + lane];
+          acc[v][0] = fmaf(fi, y.x, acc[v][0]);
+          acc[v][1] = fmaf(fi, y.y, acc[v][1]);
+          acc[v][2] = fmaf(fi, y.z, acc[v][2]);
+          acc[v][3] = fmaf(fi, y.w, acc[v][3]);
+        } else {
+          const float2 y = reinterpret_cast<const float2*>(src)[32 * v + lane];
+          acc[v][0] = fmaf(fi, y.x, acc[v][0]);
+          acc[v][1] = fmaf(fi, y.y, acc[v][1]);
+        }
+      }
     }
-    wa += count;
   }
-  p.out[orow * D + tid] = (uint16_t)pack2<F16>(L == 0.f ? 0.f : acc * (p.v_scale[h] / L), 0.f);
-  if (tid == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M - kLift + log2f(L));
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) s_o[sub][(32 * v + lane) * kVec + k] = acc[v][k];
+    if (lane == 0) {
+      s_m[sub] = M;
+      s_l[sub] = L;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    M = -INFINITY;
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) M = fmaxf(M, s_m[w]);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) acc[v][k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float f = s_l[w] == 0.f ? 0.f : ex2_approx(s_m[w] - M);
+      L = fmaf(f, s_l[w], L);
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) acc[v][k] = fmaf(f, s_o[w][(32 * v + lane) * kVec + k], acc[v][k]);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : p.v_scale[h] / L;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + (32 * v + lane) * kVec);
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) dst[k / 2] = pack2<F16>(acc[v][k] * inv, acc[v][k + 1] * inv);
+  }
+  if (lane == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M - kLift + log2f(L));
 }
 
-template <int D, int NT, bool F16>
+template <int D, int ROWS, bool F16>
 cudaError_t launch_decode(DecodeParams prm, void* ws, cudaStream_t stream) {
-  using C = DecCfg<D, NT>;
+  using C = DecCfg<D, ROWS>;
   uint8_t* w = static_cast<uint8_t*>(ws);
   prm.pref = (int*)w;
   w += C::align256((size_t)(prm.B + 1) * 4);
@@ -713,28 +841,51 @@ cudaError_t launch_decode(DecodeParams prm, void* ws, cudaStream_t stream) {
   prm.nstages = C::stages(prm.B);
   cudaError_t e;
   const int smem = C::smem(prm.B);
-  if ((e = cudaFuncSetAttribute(decode_kernel<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
-  decode_kernel<D, NT, F16><<<kCtas, C::W * 32, smem, stream>>>(prm);
+  if ((e = cudaFuncSetAttribute(decode_kernel<D, ROWS, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+    return e;
+  decode_kernel<D, ROWS, F16><<<kCtas, C::W * 32, smem, stream>>>(prm);
   if ((e = cudaGetLastError())) return e;
+  // few rows: all warps of a CTA on each, since an item may have up to kCtas parts; many: a
+  // warp each (there are few parts per item then)
+  const int rows = prm.B * prm.Hq * prm.Nq;
+  const bool wide = rows <= 8 * kCtas;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(prm.B * prm.Hq * prm.Nq);
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = dim3(wide ? rows : (rows + 7) / 8);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT, F16>, prm);
+  return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, ROWS, F16, 8>, prm)
+              : cudaLaunchKernelEx(&cfg, join_kernel<D, ROWS, F16, 1>, prm);
 }
 
-// Rows per block: as few n = 8 tiles as hold all G * Nq rows, up to what the registers
-// hold (32 rows at d <= 128, 16 at d = 256); more rows go in several blocks, each of
+// Rows per block: the fewest of 4, 8, 16, 32 that hold all G * Nq rows, up to what the
+// registers hold (32 at d <= 128, 16 at d = 256); more rows go in several blocks, each of
 // which reads the keys again (through L2).
-int row_tiles(int d, int rows) {
-  if (rows <= 8) return 1;
-  if (rows <= 16 || d == 256) return 2;
-  return 4;
+int block_rows(int d, int rows) {
+  if (rows <= 4) return 4;
+  if (rows <= 8) return 8;
+  if (rows <= 16 || d == 256) return 16;
+  return 32;
+}
+// f(D, ROWS) as constants
+template <typename F>
+auto with_config(int d, int rows, F f) {
+  using std::integral_constant;
+  auto with_d = [&](auto D) {
+    switch (rows) {
+      case 4: return f(D, integral_constant<int, 4>{});
+      case 8: return f(D, integral_constant<int, 8>{});
+      case 16: return f(D, integral_constant<int, 16>{});
+    }
+    return f(D, integral_constant<int, decltype(D)::value == 256 ? 16 : 32>{});
+  };
+  if (d == 64) return with_d(integral_constant<int, 64>{});
+  if (d == 128) return with_d(integral_constant<int, 128>{});
+  return with_d(integral_constant<int, 256>{});
 }
 
 bool bad_heads(int B, int Hq, int Hkv, int Nq) {
@@ -750,15 +901,9 @@ using namespace apa;
 extern "C" {
 
 size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
-  if (bad_heads(B, Hq, Hkv, Nq)) return 0;
-  const int nt = row_tiles(d, Hq / Hkv * Nq);
-  switch (d) {
-    case 64: return nt == 1 ? DecCfg<64, 1>::ws_bytes(B) : nt == 2 ? DecCfg<64, 2>::ws_bytes(B) : DecCfg<64, 4>::ws_bytes(B);
-    case 128:
-      return nt == 1 ? DecCfg<128, 1>::ws_bytes(B) : nt == 2 ? DecCfg<128, 2>::ws_bytes(B) : DecCfg<128, 4>::ws_bytes(B);
-    case 256: return nt == 1 ? DecCfg<256, 1>::ws_bytes(B) : DecCfg<256, 2>::ws_bytes(B);
-  }
-  return 0;
+  if (bad_heads(B, Hq, Hkv, Nq) || (d != 64 && d != 128 && d != 256)) return 0;
+  return with_config(d, block_rows(d, Hq / Hkv * Nq),
+                     [&](auto D, auto rows) { return DecCfg<decltype(D)::value, decltype(rows)::value>::ws_bytes(B); });
 }
 
 int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
@@ -804,24 +949,11 @@ int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long
   prm.out = (uint16_t*)out;
   prm.lse = lse;
   prm.err = device_error_word();
-  const bool f16 = dtype == APA_DTYPE_F16;
-  const int nt = row_tiles(d, Hq / Hkv * Nq);
-  auto go = [&](auto D_, auto NT_) {
-    constexpr int D = decltype(D_)::value, NT = decltype(NT_)::value;
-    return f16 ? launch_decode<D, NT, true>(prm, ws, stream) : launch_decode<D, NT, false>(prm, ws, stream);
-  };
-  using I64 = std::integral_constant<int, 64>;
-  using I128 = std::integral_constant<int, 128>;
-  using I256 = std::integral_constant<int, 256>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I4 = std::integral_constant<int, 4>;
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (d) {
-    case 64: e = nt == 1 ? go(I64{}, I1{}) : nt == 2 ? go(I64{}, I2{}) : go(I64{}, I4{}); break;
-    case 128: e = nt == 1 ? go(I128{}, I1{}) : nt == 2 ? go(I128{}, I2{}) : go(I128{}, I4{}); break;
-    case 256: e = nt == 1 ? go(I256{}, I1{}) : go(I256{}, I2{}); break;
-  }
+  const cudaError_t e = with_config(d, block_rows(d, Hq / Hkv * Nq), [&](auto D, auto rows) {
+    constexpr int kD = decltype(D)::value, kR = decltype(rows)::value;
+    return dtype == APA_DTYPE_F16 ? launch_decode<kD, kR, true>(prm, ws, stream)
+                                  : launch_decode<kD, kR, false>(prm, ws, stream);
+  });
   int st = e == cudaSuccess ? APA_OK : APA_ERR_CUDA;
   if (!workspace && cudaFreeAsync(ws, stream) != cudaSuccess && st == APA_OK) st = APA_ERR_CUDA;
   return st;
