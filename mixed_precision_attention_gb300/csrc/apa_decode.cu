@@ -212,6 +212,37 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, int D, int b, i
   p.out[row * D + ch] = (uint16_t)pack2<F16>(v, 0.f);
 }
 
+// acc += f * (kVec floats at src)
+template <int kVec>
+__device__ __forceinline__ void add_vec(float* acc, float f, const float* src) {
+  if constexpr (kVec == 4) {
+    const float4 y = *reinterpret_cast<const float4*>(src);
+    acc[0] = fmaf(f, y.x, acc[0]);
+    acc[1] = fmaf(f, y.y, acc[1]);
+    acc[2] = fmaf(f, y.z, acc[2]);
+    acc[3] = fmaf(f, y.w, acc[3]);
+  } else {
+    const float2 y = *reinterpret_cast<const float2*>(src);
+    acc[0] = fmaf(f, y.x, acc[0]);
+    acc[1] = fmaf(f, y.y, acc[1]);
+  }
+}
+// A joined row (a lane's channels in acc), written to out and lse.
+template <bool F16, int kVec, int kVecs>
+__device__ __forceinline__ void finish_row(const DecodeParams& p, int D, int b, int h, int r, int lane,
+                                           const float (*acc)[kVec], float M, float L) {
+  const int G = p.Hq / p.Hkv;
+  const size_t row = ((size_t)b * p.Hq + h * G + r % G) * p.Nq + r / G;
+  const float inv = L == 0.f ? 0.f : p.v_scale[h] / L;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D + (32 * v + lane) * kVec);
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) dst[k / 2] = pack2<F16>(acc[v][k] * inv, acc[v][k + 1] * inv);
+  }
+  if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : kLn2 * (M - kLift + log2f(L));
+}
+
 struct Seg {  // an item that a warp holds units of; counted from the CTA's first unit
   int first, end, b, h, rb;
 };
@@ -669,48 +700,62 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
       }
   }
   __syncthreads();
-  // the part of item sg that warps .. to of this CTA hold; here: whether the last of it is in the workspace
-  auto join = [&](const Seg& sg, int to, bool here) {
-    const int from = warps.of(max(sg.first, 0)), r0 = sg.rb * kRows;
-    const bool whole = sg.first >= 0 && sg.end <= cta_count;
-    const size_t wslot = (2 * kCtas + (size_t)blockIdx.x * W + to) * kRows;
-    const size_t cslot = (2 * (size_t)blockIdx.x + (sg.end <= cta_count ? 1 : 0)) * kRows;
-    for (int i = tid; i < kRows * D; i += W * 32) {
-      const int row = i / D, ch = i % D, r = r0 + row;
-      const float2 tail = here ? p.part_ml[wslot + row] : mml[to * kRows + row];
-      float M = tail.x;
-      for (int w = from; w < to; ++w) M = fmaxf(M, mml[w * kRows + row].x);
-      float L = 0.f, acc = 0.f;
-      for (int w = from; w < to; ++w) {
-        const float2 ml = mml[w * kRows + row];
-        if (ml.y == 0.f) continue;
-        const float f = ex2_approx(ml.x - M);
-        L = fmaf(f, ml.y, L);
-        acc = fmaf(f, mo[(w * kRows + row) * D + ch], acc);
-      }
-      if (tail.y != 0.f) {
-        const float f = ex2_approx(tail.x - M);
-        L = fmaf(f, tail.y, L);
-        acc = fmaf(f, here ? p.part_o[(wslot + row) * D + ch] : mo[(to * kRows + row) * D + ch], acc);
-      }
-      if (whole) {
-        if (r >= R) continue;
-        write_row<F16>(p, D, sg.b, sg.h, r, ch, L == 0.f ? 0.f : acc * (p.v_scale[sg.h] / L));
-        if (ch == 0 && p.lse)
-          p.lse[((size_t)sg.b * p.Hq + sg.h * G + r % G) * p.Nq + r / G] =
-              L == 0.f ? -INFINITY : kLn2 * (M - kLift + log2f(L));
-      } else {
-        p.part_o[(cslot + row) * D + ch] = acc;
-        if (ch == 0) p.part_ml[cslot + row] = make_float2(M, L);
-      }
+  // lane 2 w: the item that ends in warp w after beginning before it; lane 2 w + 1: the one that
+  // goes on behind the CTA from its last warp w.  Each (item, row) is one warp's to join.
+  const int jw = lane >> 1;
+  bool mine = false;
+  Seg sg{};
+  bool tail_in_ws = false;
+  if (jw < W) {
+    const int a = (int)warps.first(jw), e = (int)warps.first(jw + 1);
+    if (e > a) {
+      sg = seg[jw][lane & 1];
+      mine = lane & 1 ? e == cta_count && sg.end > e : sg.end <= e && sg.first < a;
+      tail_in_ws = !(lane & 1) && sg.end < e;
     }
-  };
-  for (int w = 0; w < W; ++w) {
-    const int a = (int)warps.first(w), e = (int)warps.first(w + 1);
-    if (e == a) break;
-    const Seg s0 = seg[w][0], s1 = seg[w][1];
-    if (s0.end <= e && s0.first < a) join(s0, w, s0.end < e);       // one that ends in warp w
-    if (e == cta_count && s1.end > e) join(s1, w, false);           // one that goes on behind the CTA
+  }
+  const int from_ = mine ? warps.of(max(sg.first, 0)) : 0;
+  const unsigned todo = __ballot_sync(0xffffffffu, mine);
+  constexpr int kVec = D / 32 < 4 ? D / 32 : 4, kVecs = D / (32 * kVec);  // a lane's channels: kVecs vectors
+  for (int task = warp; task < __popc(todo) * kRows; task += W) {
+    const int row = task % kRows, src = __fns(todo, 0, task / kRows + 1), to = src >> 1;
+    const int from = __shfl_sync(0xffffffffu, from_, src), first = __shfl_sync(0xffffffffu, sg.first, src);
+    const int end = __shfl_sync(0xffffffffu, sg.end, src), b = __shfl_sync(0xffffffffu, sg.b, src);
+    const int h = __shfl_sync(0xffffffffu, sg.h, src), r = __shfl_sync(0xffffffffu, sg.rb, src) * kRows + row;
+    const bool in_ws = __shfl_sync(0xffffffffu, tail_in_ws, src);
+    const size_t wrow = (2 * kCtas + (size_t)blockIdx.x * W + to) * kRows + row;
+    // lane i: the state of warp from + i
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (from + lane <= to) ml = from + lane == to && in_ws ? p.part_ml[wrow] : mml[(from + lane) * kRows + row];
+    float M = ml.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    const float f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);  // (a NaN sum goes on to the output)
+    float L = f * ml.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    float acc[kVecs][kVec];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) acc[v][k] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i <= to - from; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* src = from + i == to && in_ws ? p.part_o + wrow * D : mo + ((from + i) * kRows + row) * D;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) add_vec<kVec>(acc[v], fi, src + (32 * v + lane) * kVec);
+    }
+    if (first >= 0 && end <= cta_count) {
+      if (r < R) finish_row<F16, kVec, kVecs>(p, D, b, h, r, lane, acc, M, L);
+    } else {
+      const size_t crow = (2 * (size_t)blockIdx.x + (end <= cta_count ? 1 : 0)) * kRows + row;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) p.part_o[crow * D + (32 * v + lane) * kVec + k] = acc[v][k];
+      if (lane == 0) p.part_ml[crow] = make_float2(M, L);
+    }
   }
 }
 
@@ -730,7 +775,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (at >= p.B * p.Hkv * R) return;  // (with WPR > 1 the whole CTA)
   const int r = at % R, bh = at / R, h = bh % p.Hkv, b = bh / p.Hkv, row = r % kRows;
-  const size_t orow = ((size_t)b * p.Hq + h * G + r % G) * p.Nq + r / G;
   const int before = p.pref[b], n = p.pref[b + 1] - before;
   int ca = 0, parts = 0;
   long long u1 = 0;
@@ -775,19 +819,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
       const float* src = p.part_o + __shfl_sync(0xffffffffu, prow, i) * D;
       L = fmaf(fi, li, L);
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        if constexpr (kVec == 4) {
-          const float4 y = reinterpret_cast<const float4*>(src)[32 * v + lane];
-          acc[v][0] = fmaf(fi, y.x, acc[v][0]);
-          acc[v][1] = fmaf(fi, y.y, acc[v][1]);
-          acc[v][2] = fmaf(fi, y.z, acc[v][2]);
-          acc[v][3] = fmaf(fi, y.w, acc[v][3]);
-        } else {
-          const float2 y = reinterpret_cast<const float2*>(src)[32 * v + lane];
-          acc[v][0] = fmaf(fi, y.x, acc[v][0]);
-          acc[v][1] = fmaf(fi, y.y, acc[v][1]);
-        }
-      }
+      for (int v = 0; v < kVecs; ++v) add_vec<kVec>(acc[v], fi, src + (32 * v + lane) * kVec);
     }
   }
   if constexpr (WPR > 1) {
@@ -819,14 +851,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
         for (int k = 0; k < kVec; ++k) acc[v][k] = fmaf(f, s_o[w][(32 * v + lane) * kVec + k], acc[v][k]);
     }
   }
-  const float inv = L == 0.f ? 0.f : p.v_scale[h] / L;
-#pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + (32 * v + lane) * kVec);
-#pragma unroll
-    for (int k = 0; k < kVec; k += 2) dst[k / 2] = pack2<F16>(acc[v][k] * inv, acc[v][k + 1] * inv);
-  }
-  if (lane == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M - kLift + log2f(L));
+  finish_row<F16, kVec, kVecs>(p, D, b, h, r, lane, acc, M, L);
 }
 
 template <int D, int ROWS, bool F16>
