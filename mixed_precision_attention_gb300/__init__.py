@@ -183,17 +183,16 @@ def attention_window(q, k, v, window: int, sinks: int = 0, return_lse: bool = Tr
     position p = i + Nkv - Nq, sees the keys j <= p with j > p - window (window >= 1 keys, its own among
     them) or j < sinks.  Returns (out bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] or None)."""
     import torch
-    lib = _lib.load()
+
+    from .cache import _enqueue
     B, Hq, Hkv, Nq, Nkv, d = _check_qkv(q, k, v)
     dev = q.device
     if k.device != dev or v.device != dev:
         raise ValueError("q, k and v must be on the same device")
     out = torch.empty_like(q)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if return_lse else None
-    with torch.cuda.device(dev):
-        st = lib.apa_attention_window(_ptr(q), _ptr(k), _ptr(v), B, Hq, Hkv, Nq, Nkv, d, int(window), int(sinks),
-                                      _ptr(out), _ptr(lse), _stream(dev))
-    _lib.check(st, "apa_attention_window")
+    _enqueue(dev, "apa_attention_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, int(window),
+             int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
     return out, lse
 
 

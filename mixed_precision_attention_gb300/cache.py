@@ -15,26 +15,28 @@ can be captured into a CUDA graph.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib
 
 PAGE = 64  # keys per page
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # APA_DTYPE_*
-_NOTHING = contextlib.nullcontext()
 TABLES_STATUS = {0: "ok", 1: "a length is out of range", 2: "more tokens than max_tokens", 3: "too few free pages",
                  4: "the free list's count is out of range, or its capacity too small"}
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _on(dev):
-    """A context with `dev` current: kernels go to the device that holds the tensors."""
-    return _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _enqueue(dev, name, *args):
+    """Calls an entry point with the current stream of `dev`, which is made current for it (the raw stream: a decoding
+    step makes several of these calls, and a Stream object costs more than a launch)."""
+    fn = getattr(_lib.load(), name)
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, name)
 
 
 def _need(name, t, dtype, dim, dev=None, contiguous=True):
@@ -69,10 +71,6 @@ def _scales(Hkv, dev, k_scale, v_scale):
             raise ValueError(f"{name} must be [Hkv]")
 
 
-def _raw_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
 def cache_pages(num_pages: int, Hkv: int, d: int, device="cuda"):
     """An empty pool: uint8 zeros [num_pages, Hkv, 72 * d]."""
     if d not in (64, 128, 256):
@@ -105,16 +103,15 @@ def cache_tables(old_lens, new_lens, block_table, free_pages, free_count, max_to
         _need("free_count_out", free_count_out, torch.int32, 1, dev)
         if free_count_out.shape[0] != 1:
             raise ValueError("free_count_out must be [1]")
-    buf = torch.empty(2 * max_tokens + B + 3, dtype=torch.int32, device=dev)
-    slots, positions, starts, count, status = buf.split((max_tokens, max_tokens, B + 1, 1, 1))
-    if free_count_out is not None:
-        count = free_count_out
-    with _on(dev):
-        st = _lib.load().apa_cache_tables(
-            old_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), block_table.shape[1],
-            free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), max_tokens, slots.data_ptr(),
-            positions.data_ptr(), starts.data_ptr(), count.data_ptr(), status.data_ptr(), _raw_stream(dev))
-    _lib.check(st, "apa_cache_tables")
+    room = (max_tokens + 3) // 4 * 4  # (slots and positions on 16 bytes)
+    buf = torch.empty(2 * room + B + 3, dtype=torch.int32, device=dev)
+    one = (1,)
+    slots, positions = buf.as_strided((max_tokens,), one), buf.as_strided((max_tokens,), one, room)
+    starts, status = buf.as_strided((B + 1,), one, 2 * room), buf.as_strided(one, one, 2 * room + B + 1)
+    count = buf.as_strided(one, one, 2 * room + B + 2) if free_count_out is None else free_count_out
+    _enqueue(dev, "apa_cache_tables", old_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
+             block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), max_tokens,
+             slots.data_ptr(), positions.data_ptr(), starts.data_ptr(), count.data_ptr(), status.data_ptr())
     return {"slots": slots, "positions": positions, "starts": starts, "free_count": count, "status": status}
 
 
@@ -137,11 +134,10 @@ def cache_write(k, v, slots, pages, k_scale, v_scale):
     if _pool(pages, Hkv, d) != dev:
         raise ValueError("pages must be on k's device")
     _scales(Hkv, dev, k_scale, v_scale)
-    with _on(dev):
-        st = _lib.load().apa_cache_write(
-            k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], Hkv, T, d, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-            slots.data_ptr(), pages.data_ptr(), pages.shape[0], k_scale.data_ptr(), v_scale.data_ptr(), _raw_stream(dev))
-    _lib.check(st, "apa_cache_write")
+    kh, kt, _ = k.stride()
+    vh, vt, _ = v.stride()
+    _enqueue(dev, "apa_cache_write", k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], Hkv, T, d, kh, kt, vh, vt,
+             slots.data_ptr(), pages.data_ptr(), pages.shape[0], k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def cache_read(pages, slots, k_scale, v_scale, dtype=torch.bfloat16):
@@ -156,11 +152,8 @@ def cache_read(pages, slots, k_scale, v_scale, dtype=torch.bfloat16):
     T, d = slots.shape[0], n // 72
     k = torch.empty((Hkv, T, d), dtype=dtype, device=dev)
     v = torch.empty((Hkv, T, d), dtype=dtype, device=dev)
-    with _on(dev):
-        st = _lib.load().apa_cache_read(pages.data_ptr(), num_pages, _DTYPES[dtype], Hkv, T, d, slots.data_ptr(),
-                                        k_scale.data_ptr(), v_scale.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                        _raw_stream(dev))
-    _lib.check(st, "apa_cache_read")
+    _enqueue(dev, "apa_cache_read", pages.data_ptr(), num_pages, _DTYPES[dtype], Hkv, T, d, slots.data_ptr(),
+             k_scale.data_ptr(), v_scale.data_ptr(), k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -191,19 +184,15 @@ def attention_cache(q, pages, block_table, lens, k_scale, v_scale, window: int =
     if block_table.shape[0] != B or lens.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages] and lens [B]")
     _scales(Hkv, dev, k_scale, v_scale)
-    lib = _lib.load()
-    need = lib.apa_attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d), dtype=torch.uint8, device=dev)
     else:
         _need("workspace", workspace, torch.uint8, 1, dev)
     out = torch.empty((B, Hq, Nq, d), dtype=q.dtype, device=dev)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if return_lse else None
-    with _on(dev):
-        st = lib.apa_attention_cache(
-            q.data_ptr(), _DTYPES[q.dtype], q.stride(0), q.stride(1), q.stride(2), pages.data_ptr(), num_pages,
-            block_table.data_ptr(), block_table.shape[1], lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hq,
-            Hkv, Nq, d, int(window), int(sinks), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
-            _raw_stream(dev))
-    _lib.check(st, "apa_attention_cache")
+    qb, qh, qr, _ = q.stride()
+    _enqueue(dev, "apa_attention_cache", q.data_ptr(), _DTYPES[q.dtype], qb, qh, qr, pages.data_ptr(), num_pages,
+             block_table.data_ptr(), block_table.shape[1], lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hq,
+             Hkv, Nq, d, int(window), int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr(),
+             workspace.data_ptr(), workspace.numel())
     return out, lse

@@ -25,6 +25,7 @@
 // row block) that one warp holds entirely is written out at once; then the CTA joins its
 // warps' parts of the others in order, and a second kernel those that span CTAs, so
 // results do not depend on timing.
+#include <atomic>
 #include <cmath>
 
 #include "../../include/apa.h"
@@ -76,11 +77,12 @@ struct DecCfg {
   static constexpr int kUnitBytes = 36 * D;
   static constexpr int kScaleBytes = 8 * D;  // a unit's V scales as FP16 pairs, per warp
   static constexpr int kMaxStages = 6;
+  static constexpr int kStaticBytes = 1536;  // room for the kernel's static arrays
   static constexpr int kSlots = kCtas * (2 + W);
   static constexpr int kBarBytes = W * kMaxStages * 8 + 16;
   static constexpr int kMergeBytes = W * kRows * (D + 2) * 4;
   static int stages(int B) {
-    const int room = 232448 - W * kScaleBytes - kBarBytes - (B + 1) * 4 - 1536;  // (1536: the static arrays)
+    const int room = 232448 - W * kScaleBytes - kBarBytes - (B + 1) * 4 - kStaticBytes;
     const int n = room / (W * kUnitBytes);
     return n > kMaxStages ? kMaxStages : n;
   }
@@ -866,8 +868,17 @@ cudaError_t launch_decode(DecodeParams prm, void* ws, cudaStream_t stream) {
   prm.nstages = C::stages(prm.B);
   cudaError_t e;
   const int smem = C::smem(prm.B);
-  if ((e = cudaFuncSetAttribute(decode_kernel<D, ROWS, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-    return e;
+  // the largest size, once per device (a bit each)
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev))) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(ready.load() & bit)) {
+    if ((e = cudaFuncSetAttribute(decode_kernel<D, ROWS, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  232448 - C::kStaticBytes)))
+      return e;
+    if (dev <= 63) ready.fetch_or(bit);
+  }
   decode_kernel<D, ROWS, F16><<<kCtas, C::W * 32, smem, stream>>>(prm);
   if ((e = cudaGetLastError())) return e;
   // few rows: all warps of a CTA on each, since an item may have up to kCtas parts; many: a
