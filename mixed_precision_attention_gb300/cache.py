@@ -103,12 +103,11 @@ def cache_tables(old_lens, new_lens, block_table, free_pages, free_count, max_to
         _need("free_count_out", free_count_out, torch.int32, 1, dev)
         if free_count_out.shape[0] != 1:
             raise ValueError("free_count_out must be [1]")
-    room = (max_tokens + 3) // 4 * 4  # (slots and positions on 16 bytes)
-    buf = torch.empty(2 * room + B + 3, dtype=torch.int32, device=dev)
-    one = (1,)
-    slots, positions = buf.as_strided((max_tokens,), one), buf.as_strided((max_tokens,), one, room)
-    starts, status = buf.as_strided((B + 1,), one, 2 * room), buf.as_strided(one, one, 2 * room + B + 1)
-    count = buf.as_strided(one, one, 2 * room + B + 2) if free_count_out is None else free_count_out
+    slots = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    starts = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    status = torch.empty(1, dtype=torch.int32, device=dev)
+    count = torch.empty(1, dtype=torch.int32, device=dev) if free_count_out is None else free_count_out
     _enqueue(dev, "apa_cache_tables", old_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
              block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), max_tokens,
              slots.data_ptr(), positions.data_ptr(), starts.data_ptr(), count.data_ptr(), status.data_ptr())

@@ -82,11 +82,16 @@ struct P2Params {
   uint16_t* out16;            // [B,Hq,Nq,d] bf16
 };
 
-// The sliding-window form of the kernels (template parameter W; apa_attention_window):
+// The sliding-window form of pass2_kernel (template parameter W; apa_attention_window):
 // row position x (x = pos + off) sees the keys j <= x with j > x - window or j < sinks.
 // A block walks the tiles that hold sinks, then those its rows' windows reach, every
 // row group taking part; P and V go to the product in BF16, V straight from the
-// caller's array, so there is no copy of V and no workspace; out is bf16.
+// caller's array, so there is no copy of V and no workspace; out is bf16.  Walks are
+// short, so what a CTA does before its first and after its last product counts: at
+// d <= 128 two CTAs share an SM (256 TMEM columns each) and cover each other's.  On
+// 8192 rows with a window of 1024 the two-group kernel, one CTA per SM, took 180 us,
+// this one 133; on 16384 rows with a window of 4096, 797 and 670 us (1235 TFLOP/s, 0.65
+// of the measured BF16 rate; the matrix pipe and the softmax threads share what is left).
 struct WindowTiles {
   int n_sink, t_lo, n;  // entries 0 .. n_sink-1: tiles 0 ..; then tiles t_lo ..
   __device__ __forceinline__ WindowTiles(const P2Params& p, int p0, int t_hi) {
@@ -125,18 +130,26 @@ constexpr float kTau2 = 8.0f;  // pass-2 lazy rescale threshold (log2 units)
 // 122880 layer, two CTAs of that shape were no faster than one CTA with 3 stages.
 // P goes from the softmax threads into TMEM, over the S slot it came from, and the
 // PV product reads it there.
-template <int D>
+template <int D, bool W = false>
 struct P2Cfg {
-  static constexpr int kCtasPerSm = 1;
-  static constexpr int NS = kCtasPerSm == 2 ? 2 : (D >= 256 ? 2 : (D == 128 ? APA_P2_STAGES_D128 : 3));
+  static constexpr int kCtasPerSm = W && D <= 128 ? 2 : 1;
+  // K and V of a tile share a stage, or (kSplit) have rings of their own, so that the next
+  // tiles' K need not wait for a P.V product (16384 rows, window 4096: 885 us with two
+  // shared stages, 710 with rings of 3 and 2, 670 with 2 and 3)
+  static constexpr bool kSplit = kCtasPerSm == 2;
+  static constexpr int NS = kSplit ? (D == 128 ? 2 : 3) : (D >= 256 ? 2 : (D == 128 ? APA_P2_STAGES_D128 : 3));  // of K
+  static constexpr int NSV = kSplit ? 3 : NS;                                                 // of V
   static constexpr int kAtoms = D / 64;
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kKVBytes = 64 * D * 2;  // one of K or V per stage
   static constexpr int kQOff = 0;
   static constexpr int kStageOff = kQBytes;
-  static constexpr int kNumBars = 2 * NS + 10;
-  static constexpr int kBarOff = kStageOff + NS * 2 * kKVBytes;
-  static constexpr int kSlack = kCtasPerSm == 2 ? 0 : 1024;  // runtime alignment room
+  static constexpr int kStep = kSplit ? kKVBytes : 2 * kKVBytes;  // from a stage to the next
+  static constexpr int kVOff = kStageOff + (kSplit ? NS : 1) * kKVBytes;
+  static constexpr int kB0 = kSplit ? 2 * (NS + NSV) : 2 * NS;  // barriers of the stages
+  static constexpr int kNumBars = kB0 + 10;
+  static constexpr int kBarOff = kStageOff + (NS + NSV) * kKVBytes;
+  static constexpr int kSlack = kCtasPerSm == 2 && D == 128 ? 0 : 1024;  // runtime alignment room (none left for two CTAs)
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + kSlack;
   static constexpr uint32_t kTmemCols = D + 128 <= 256 ? 256 : 512;
   static constexpr uint32_t kOCol = 0, kSCol = D;
@@ -159,60 +172,54 @@ __device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, int*
 // run as packed FP32 pairs.
 template <bool W>
 __device__ __forceinline__ void p8(const float* x, float c2, float nb, uint32_t* h, float& s0, float& s1) {
-  if constexpr (W) {
-    float y[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = ex2_approx(fmaf(x[k], c2, nb));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(y[2 * k + 1]), "f"(y[2 * k]));
-      s0 += y[2 * k];
-      s1 += y[2 * k + 1];
-    }
-    return;
-  }
-  asm("{\n.reg .b64 a0, a1, a2, a3, c, n, s, one;\n"
-      ".reg .f32 y0, y1, y2, y3, y4, y5, y6, y7;\n"
-      "mov.b64 c, {%14, %14};\n"
-      "mov.b64 n, {%15, %15};\n"
-      "mov.b64 one, {%16, %16};\n"
-      "mov.b64 a0, {%6, %7};\n"
-      "mov.b64 a1, {%8, %9};\n"
-      "mov.b64 a2, {%10, %11};\n"
-      "mov.b64 a3, {%12, %13};\n"
-      "fma.rn.f32x2 a0, a0, c, n;\n"
-      "fma.rn.f32x2 a1, a1, c, n;\n"
-      "fma.rn.f32x2 a2, a2, c, n;\n"
-      "fma.rn.f32x2 a3, a3, c, n;\n"
-      "mov.b64 {y0, y1}, a0;\n"
-      "mov.b64 {y2, y3}, a1;\n"
-      "mov.b64 {y4, y5}, a2;\n"
-      "mov.b64 {y6, y7}, a3;\n"
-      "ex2.approx.ftz.f32 y0, y0;\n"
-      "ex2.approx.ftz.f32 y1, y1;\n"
-      "ex2.approx.ftz.f32 y2, y2;\n"
-      "ex2.approx.ftz.f32 y3, y3;\n"
-      "ex2.approx.ftz.f32 y4, y4;\n"
-      "ex2.approx.ftz.f32 y5, y5;\n"
-      "ex2.approx.ftz.f32 y6, y6;\n"
-      "ex2.approx.ftz.f32 y7, y7;\n"
-      "cvt.rn.f16x2.f32 %0, y1, y0;\n"
-      "cvt.rn.f16x2.f32 %1, y3, y2;\n"
-      "cvt.rn.f16x2.f32 %2, y5, y4;\n"
-      "cvt.rn.f16x2.f32 %3, y7, y6;\n"
-      "mov.b64 s, {%4, %5};\n"
-      "mov.b64 a0, {y0, y1};\n"
-      "mov.b64 a1, {y2, y3};\n"
-      "mov.b64 a2, {y4, y5};\n"
-      "mov.b64 a3, {y6, y7};\n"
-      "fma.rn.f32x2 s, a0, one, s;\n"
-      "fma.rn.f32x2 s, a1, one, s;\n"
-      "fma.rn.f32x2 s, a2, one, s;\n"
-      "fma.rn.f32x2 s, a3, one, s;\n"
-      "mov.b64 {%4, %5}, s;\n}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]), "+f"(s0), "+f"(s1)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(c2), "f"(nb),
-        "f"(1.f));
+#define APA_P8(CVT)                                                                                                  \
+  asm("{\n.reg .b64 a0, a1, a2, a3, c, n, s, one;\n"                                                                 \
+      ".reg .f32 y0, y1, y2, y3, y4, y5, y6, y7;\n"                                                                  \
+      "mov.b64 c, {%14, %14};\n"                                                                                     \
+      "mov.b64 n, {%15, %15};\n"                                                                                     \
+      "mov.b64 one, {%16, %16};\n"                                                                                   \
+      "mov.b64 a0, {%6, %7};\n"                                                                                      \
+      "mov.b64 a1, {%8, %9};\n"                                                                                      \
+      "mov.b64 a2, {%10, %11};\n"                                                                                    \
+      "mov.b64 a3, {%12, %13};\n"                                                                                    \
+      "fma.rn.f32x2 a0, a0, c, n;\n"                                                                                 \
+      "fma.rn.f32x2 a1, a1, c, n;\n"                                                                                 \
+      "fma.rn.f32x2 a2, a2, c, n;\n"                                                                                 \
+      "fma.rn.f32x2 a3, a3, c, n;\n"                                                                                 \
+      "mov.b64 {y0, y1}, a0;\n"                                                                                      \
+      "mov.b64 {y2, y3}, a1;\n"                                                                                      \
+      "mov.b64 {y4, y5}, a2;\n"                                                                                      \
+      "mov.b64 {y6, y7}, a3;\n"                                                                                      \
+      "ex2.approx.ftz.f32 y0, y0;\n"                                                                                 \
+      "ex2.approx.ftz.f32 y1, y1;\n"                                                                                 \
+      "ex2.approx.ftz.f32 y2, y2;\n"                                                                                 \
+      "ex2.approx.ftz.f32 y3, y3;\n"                                                                                 \
+      "ex2.approx.ftz.f32 y4, y4;\n"                                                                                 \
+      "ex2.approx.ftz.f32 y5, y5;\n"                                                                                 \
+      "ex2.approx.ftz.f32 y6, y6;\n"                                                                                 \
+      "ex2.approx.ftz.f32 y7, y7;\n"                                                                                 \
+      CVT " %0, y1, y0;\n"                                                                                           \
+      CVT " %1, y3, y2;\n"                                                                                           \
+      CVT " %2, y5, y4;\n"                                                                                           \
+      CVT " %3, y7, y6;\n"                                                                                           \
+      "mov.b64 s, {%4, %5};\n"                                                                                       \
+      "mov.b64 a0, {y0, y1};\n"                                                                                      \
+      "mov.b64 a1, {y2, y3};\n"                                                                                      \
+      "mov.b64 a2, {y4, y5};\n"                                                                                      \
+      "mov.b64 a3, {y6, y7};\n"                                                                                      \
+      "fma.rn.f32x2 s, a0, one, s;\n"                                                                                \
+      "fma.rn.f32x2 s, a1, one, s;\n"                                                                                \
+      "fma.rn.f32x2 s, a2, one, s;\n"                                                                                \
+      "fma.rn.f32x2 s, a3, one, s;\n"                                                                                \
+      "mov.b64 {%4, %5}, s;\n}"                                                                                      \
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]), "+f"(s0), "+f"(s1)                                           \
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(c2), "f"(nb),    \
+        "f"(1.f))
+  if constexpr (W)
+    APA_P8("cvt.rn.bf16x2.f32");
+  else
+    APA_P8("cvt.rn.f16x2.f32");
+#undef APA_P8
 }
 
 // 32 FP32 values of a row -> bf16, 64 bytes.
@@ -231,9 +238,9 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const uint32_t* o) 
 }
 
 template <int D, bool W = false>
-__global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
     pass2_kernel(const P2Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using C = P2Cfg<D>;
+  using C = P2Cfg<D, W>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (C::kSlack == 0 && smem != smem_raw) {  // no room to realign: refuse loudly
@@ -265,14 +272,19 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
 
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = smem_u32(bars);
-  auto kv_full = [&](int st) { return bar0 + 8u * st; };
-  auto kv_empty = [&](int st) { return bar0 + 8u * (C::NS + st); };
-  auto s_full = [&](int b2) { return bar0 + 8u * (2 * C::NS + b2); };
-  // (slots 2 NS + 2, 3 are unused: an S slot is free once the P.V that reads the P
+  // tile i's K and V: their stages' barriers (shared by both unless kSplit) and wait parities
+  auto k_full = [&](int i) { return bar0 + 8u * (i % C::NS); };
+  auto k_empty = [&](int i) { return bar0 + 8u * (C::NS + i % C::NS); };
+  auto v_full = [&](int i) { return C::kSplit ? bar0 + 8u * (2 * C::NS + i % C::NSV) : bar0 + 8u * (i % C::NS); };
+  auto v_empty = [&](int i) {
+    return C::kSplit ? bar0 + 8u * (2 * C::NS + C::NSV + i % C::NSV) : bar0 + 8u * (C::NS + i % C::NS);
+  };
+  auto s_full = [&](int b2) { return bar0 + 8u * (C::kB0 + b2); };
+  // (slots kB0 + 2, 3 are unused: an S slot is free once the P.V that reads the P
   // written over it has completed, so pv_done tells the S issuer)
-  auto p_full = [&](int b2) { return bar0 + 8u * (2 * C::NS + 4 + b2); };
-  auto pv_done = [&](int b2) { return bar0 + 8u * (2 * C::NS + 6 + b2); };
-  const uint32_t drain = bar0 + 8u * (2 * C::NS + 8), drain_pv = bar0 + 8u * (2 * C::NS + 9);
+  auto p_full = [&](int b2) { return bar0 + 8u * (C::kB0 + 4 + b2); };
+  auto pv_done = [&](int b2) { return bar0 + 8u * (C::kB0 + 6 + b2); };
+  const uint32_t drain = bar0 + 8u * (C::kB0 + 8), drain_pv = bar0 + 8u * (C::kB0 + 9);
   // every lane of a softmax warp waits; the warp proceeds only if all lanes succeeded
   auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;  // already complete
@@ -304,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < C::kNumBars; ++i) {
-      const bool per_warp = (i >= 2 * C::NS + 4 && i < 2 * C::NS + 6);  // p_full: one arrive per softmax warp
-      const bool kv_empty_bar = (i >= C::NS && i < 2 * C::NS);           // kv_empty: the S and the PV issuer
+      const bool per_warp = (i >= C::kB0 + 4 && i < C::kB0 + 6);         // p_full: one arrive per softmax warp
+      const bool kv_empty_bar = !C::kSplit && i >= C::NS && i < 2 * C::NS;  // empty: the S and the PV issuer
       mbar_init(bar0 + 8u * i, per_warp ? 4u : (kv_empty_bar ? 2u : 1u));
     }
     fence_mbar_init();
@@ -353,10 +365,9 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
   if (warp == 4) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int issued = 0;
+      int issued = 0, issued_v = 0;  // (issued_v: with rings of their own)
       for (int i = 0; i < n; ++i) {
-        const int st = i % C::NS;
-        if (i >= C::NS && !mbar_wait(kv_empty(st), ((i / C::NS) - 1) & 1, &abort_flag, p.err)) break;
+        if (i >= C::NS && !mbar_wait(k_empty(i), ((i / C::NS) - 1) & 1, &abort_flag, p.err)) break;
         uint32_t gm;
         const int t = tile_of(i, gm);
         // contiguous maps: (channel, key, b * Hkv + h); paged maps: (channel, key in
@@ -367,26 +378,38 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
           ky = 0;
           kz = kv_page(s, b, t, p.err) * s.Hkv + h;
         }
-        mbar_arrive_expect_tx(kv_full(st), 2 * C::kKVBytes);
-        const uint32_t kdst = sbase + C::kStageOff + st * 2 * C::kKVBytes;
+        mbar_arrive_expect_tx(k_full(i), C::kSplit ? C::kKVBytes : 2 * C::kKVBytes);
+        const uint32_t kdst = sbase + C::kStageOff + (i % C::NS) * C::kStep;
+        const uint32_t vdst = sbase + C::kVOff + (i % C::NSV) * C::kStep;
+        if constexpr (C::kSplit) {
 #pragma unroll
-        for (int a = 0; a < C::kAtoms; ++a) {
-          tma_load_3d(kdst + a * 8192, &kmap, a * 64, ky, kz, kv_full(st));
-          tma_load_3d(kdst + C::kKVBytes + a * 8192, &vmap, a * 64, vy, vz, kv_full(st));
+          for (int a = 0; a < C::kAtoms; ++a) tma_load_3d(kdst + a * 8192, &kmap, a * 64, ky, kz, k_full(i));
+          issued = i + 1;
+          if (i >= C::NSV && !mbar_wait(v_empty(i), ((i / C::NSV) - 1) & 1, &abort_flag, p.err)) break;
+          mbar_arrive_expect_tx(v_full(i), C::kKVBytes);
+#pragma unroll
+          for (int a = 0; a < C::kAtoms; ++a) tma_load_3d(vdst + a * 8192, &vmap, a * 64, vy, vz, v_full(i));
+          issued_v = i + 1;
+        } else {
+#pragma unroll
+          for (int a = 0; a < C::kAtoms; ++a) {
+            tma_load_3d(kdst + a * 8192, &kmap, a * 64, ky, kz, k_full(i));
+            tma_load_3d(vdst + a * 8192, &vmap, a * 64, vy, vz, k_full(i));
+          }
+          issued = i + 1;
         }
-        issued = i + 1;
       }
       // every copy issued lands before the CTA exits, also when another warp gave up
       // after this loop ended (normally they have all landed: the waits return at once)
-      for (int i = max(0, issued - C::NS); i < issued; ++i) wait_bounded(kv_full(i % C::NS), (i / C::NS) & 1, p.err);
+      for (int i = max(0, issued - C::NS); i < issued; ++i) wait_bounded(k_full(i), (i / C::NS) & 1, p.err);
+      for (int i = max(0, issued_v - C::NSV); i < issued_v; ++i) wait_bounded(v_full(i), (i / C::NSV) & 1, p.err);
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ S issuer
     if (lane == 0 && n > 0) {
       const uint32_t idS = idesc_bf16(128, 64, 0);
       auto issue_s = [&](int i) -> bool {
-        const int st = i % C::NS;
-        if (!mbar_wait(kv_full(st), (i / C::NS) & 1, &abort_flag, p.err)) return false;
+        if (!mbar_wait(k_full(i), (i / C::NS) & 1, &abort_flag, p.err)) return false;
         uint32_t gm_unused;
         if (s.pages && (s.Nkv % kTile) != 0 && tile_of(i, gm_unused) == T - 1) {
           // paged pool: the keys past Nkv in a sequence's last page hold whatever the
@@ -394,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
           // keep those out of an MMA, so the K rows are zeroed here, before any MMA
           // reads this stage (V comes from the contiguous FP16 copy).
           const int nk = s.Nkv - (T - 1) * kTile, rows = kTile - nk;
-          uint8_t* kst = smem + C::kStageOff + st * 2 * C::kKVBytes;
+          uint8_t* kst = smem + C::kStageOff + (i % C::NS) * C::kStep;
           for (int x = 0; x < rows * C::kAtoms * 8; ++x) {
             const int rest = x >> 3, rr = nk + rest % rows, atom = rest / rows;
             *reinterpret_cast<uint4*>(kst + atom * 8192 + rr * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -404,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
         // the slot holds P of entry i - 2 until its P.V has read it
         if (i >= 2 && !mbar_wait(pv_done(i & 1), ((i >> 1) - 1) & 1, &abort_flag, p.err)) return false;
         tc_fence_after();
-        const uint32_t kaddr = sbase + C::kStageOff + st * 2 * C::kKVBytes;
+        const uint32_t kaddr = sbase + C::kStageOff + (i % C::NS) * C::kStep;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t ad = smem_desc(sbase + C::kQOff + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, kSwizzle128B);
@@ -412,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
           mma_bf16(tmem + C::kSCol + 64 * (i & 1), ad, bd, idS, kk > 0);
         }
         mma_commit(s_full(i & 1));
-        mma_commit(kv_empty(st));  // this stage's K has been read
+        mma_commit(k_empty(i));  // this stage's K has been read
         return true;
       };
       for (int i = 0; i < n; ++i)
@@ -428,9 +451,9 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         if (!(ok = mbar_wait(p_full(i & 1), (i >> 1) & 1, &abort_flag, p.err))) break;
-        if (!(ok = mbar_wait(kv_full(i % C::NS), (i / C::NS) & 1, &abort_flag, p.err))) break;
+        if (!(ok = mbar_wait(v_full(i), (i / C::NSV) & 1, &abort_flag, p.err))) break;
         tc_fence_after();
-        const uint32_t vaddr = sbase + C::kStageOff + (i % C::NS) * 2 * C::kKVBytes + C::kKVBytes;
+        const uint32_t vaddr = sbase + C::kVOff + (i % C::NSV) * C::kStep;
         // P (FP16) sits in the first 32 columns of its S slot: 16 keys per MMA
         const uint32_t pcol = tmem + C::kSCol + 64u * (i & 1);
 #pragma unroll
@@ -439,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
           mma_f16_ts(tmem + C::kOCol, pcol + 8u * kk, bd, idO, (i > 0 || kk > 0) ? 1u : 0u);
         }
         mma_commit(pv_done(i & 1));
-        mma_commit(kv_empty(i % C::NS));  // this stage's V has been read
+        mma_commit(v_empty(i));  // this stage's V has been read
       }
       mma_commit(drain_pv);
       wait_bounded(drain_pv, 0, p.err);
@@ -729,7 +752,7 @@ struct P2DualCfg {
   static_assert(kSBase + 256 <= kTmemCols, "TMEM budget");
 };
 
-template <int D, bool W = false>
+template <int D>
 __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
     pass2_dual_kernel(const P2Params p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
@@ -783,11 +806,9 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
   const bool apa_mode = p.hot_list != nullptr;
   const int last_row = min(R, p0 + kBlockRows) - 1;
   const int t_hi = s.causal ? min(T - 1, (last_row / G + off) / kTile) : T - 1;
-  const WindowTiles wt(p, p0, t_hi);  // (used in the sliding-window form only)
-  const int n = W ? wt.n : apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
+  const int n = apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
   const uint32_t* list = apa_mode ? p.hot_list + ((size_t)bh * nblk + blk) * T : nullptr;
   auto entry = [&](int i) -> uint32_t {
-    if constexpr (W) return (uint32_t)wt.tile(i) | (0xFFu << 16);
     return apa_mode ? list[i] : ((uint32_t)(i == 0 ? 0 : t_hi + 1 - i) | (0xFFu << 16));
   };
 
@@ -922,7 +943,7 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
   } else if (warp == kMmaPV) {
     // ------------------------------------------------------------ PV issuer: tile i into group i % 2's O
     if (lane == 0 && n > 0) {
-      const uint32_t idO = W ? idesc_bf16(128, D, 1) : idesc_f16(128, D, 1);
+      const uint32_t idO = idesc_f16(128, D, 1);
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         const int st = i % C::NSV, v = i & 1, j = i >> 1, b2 = j & 1;
@@ -961,9 +982,7 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
       if (!(ok = warp_wait(s_full(u, j & 1), (j >> 1) & 1))) break;
       const bool row_hot = row_valid && ((gm >> (r >> 4)) & 1u);
       const int j0 = t * kTile;
-      const RowKeys rk(p, vis_last, j0, row_hot);  // (used in the sliding-window form only)
-      // keys j0 .. j0+nvis-1 visible (but for the gap behind the sinks)
-      const int nvis = W ? rk.nvis : row_hot ? min(kTile, vis_last + 1 - j0) : 0;
+      const int nvis = row_hot ? min(kTile, vis_last + 1 - j0) : 0;  // keys j0 .. j0+nvis-1 visible
       // P (FP16, two keys per column) goes over the first 32 columns of the S slot it
       // came from; the slot's previous P had been read before S was written into it
       const uint32_t pslot = tmem + lane_base + tS + 64u * (j & 1);
@@ -988,10 +1007,10 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
       float sv[64];
 #pragma unroll
       for (int x = 0; x < 64; ++x) sv[x] = __uint_as_float(raw[x]);
-      if (__any_sync(0xffffffffu, nvis > 0 && (W ? !rk.all() : nvis < 64))) {
+      if (__any_sync(0xffffffffu, nvis > 0 && nvis < 64)) {
 #pragma unroll
         for (int x = 0; x < 64; ++x)
-          if (W ? !rk.sees(x) : x >= nvis) sv[x] = -INFINITY;
+          if (x >= nvis) sv[x] = -INFINITY;
       }
       float g8[8];
 #pragma unroll
@@ -1017,7 +1036,7 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
           const int ch = 4 * hf + c4;
-          p8<W>(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
+          p8<false>(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
         }
         tmem_st_x16(pslot + 16u * hf, pk);
       }
@@ -1068,9 +1087,9 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
                   wB = eB == -INFINITY ? 0.f : exp2f(eB - M);
       const float L = (w1 * l1 + wA * lA) + wB * lB;
       const float invL = 1.f / L;
-      const float vsc = W ? 1.f : v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
+      const float vsc = v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
       const float wAo = wA * vsc, wBo = wB * vsc;
-      float* orow = W ? nullptr : p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
+      float* orow = p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t oa[32], ob[32];
@@ -1089,14 +1108,7 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) ob[x] = 0u;
         }
-        if constexpr (W) {
-          if (row_valid) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              oa[x] = __float_as_uint((wAo * __uint_as_float(oa[x]) + wBo * __uint_as_float(ob[x])) * invL);
-            store_bf16x32(p.out16 + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D + c0, oa);
-          }
-        } else if (row_valid) {
+        if (row_valid) {
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             float4 res;
@@ -1197,16 +1209,9 @@ template <int D>
 cudaError_t launch_window_d(const P2Params& prm, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   const int grid = prm.s.BH() * prm.s.nblk();
   cudaError_t e;
-  if constexpr (D <= 128) {
-    const int smem = P2DualCfg<D>::kSmem;
-    if ((e = cudaFuncSetAttribute(pass2_dual_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-      return e;
-    pass2_dual_kernel<D, true><<<grid, P2DualCfg<D>::kThreads, smem, st>>>(prm, km, vm);
-  } else {
-    const int smem = P2Cfg<D>::kSmem;
-    if ((e = cudaFuncSetAttribute(pass2_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
-    pass2_kernel<D, true><<<grid, kThreads, smem, st>>>(prm, km, vm);
-  }
+  const int smem = P2Cfg<D, true>::kSmem;
+  if ((e = cudaFuncSetAttribute(pass2_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+  pass2_kernel<D, true><<<grid, kThreads, smem, st>>>(prm, km, vm);
   return cudaGetLastError();
 }
 
