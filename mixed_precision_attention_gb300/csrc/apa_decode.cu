@@ -80,7 +80,8 @@ struct DecCfg {
   static constexpr int kStaticBytes = 1536;  // room for the kernel's static arrays
   static constexpr int kSlots = kCtas * (2 + W);
   static constexpr int kBarBytes = W * kMaxStages * 8 + 16;
-  static constexpr int kMergeBytes = W * kRows * (D + 2) * 4;
+  static constexpr int kPitch = D + (kQuad ? 8 : 4);  // floats per row of a state in shared memory: no bank twice
+  static constexpr int kMergeBytes = W * kRows * (kPitch + 2) * 4;
   static int stages(int B) {
     const int room = 232448 - W * kScaleBytes - kBarBytes - (B + 1) * 4 - kStaticBytes;
     const int n = room / (W * kUnitBytes);
@@ -328,30 +329,30 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
   if (count > 0) {
     // Units are counted from the warp's first one, x0, from here on.
     // ---- producer cursor: unit px, of an item [pfirst, pend), goes into stage ps next
-    int px = 0, pfirst, pend, pb, plo, psink, plast;
-    const uint8_t* head;  // the KV head's part of page 0
-    auto enter = [&]() {
-      const Item it = find_item(pref, p.B, heads_rb, nrb, x0 + px);
-      const SeqUnits su(p, p.lens[it.b]);
-      pb = it.b;
-      plo = su.lo - su.n_sink;
-      psink = su.n_sink;
-      plast = (su.len - 1) / kTile;
-      pfirst = (int)(it.first - x0);
-      pend = (int)(it.end - x0);
-      head = p.pages + (size_t)it.h * page_head_bytes(D);
+    struct Entered {
+      int b, h, rb, len, lo, sink, first, end;  // lo: from a unit behind the sinks to its half page
     };
-    enter();
+    int px = 0;
+    Entered pi;
+    const uint8_t* head;  // the KV head's part of page 0
+    auto enter = [&](int x) {
+      const Item it = find_item(pref, p.B, heads_rb, nrb, x0 + x);
+      const SeqUnits su(p, p.lens[it.b]);
+      return Entered{it.b, it.h, it.rb, su.len, su.lo - su.n_sink, su.n_sink, (int)(it.first - x0), (int)(it.end - x0)};
+    };
+    pi = enter(0);
+    head = p.pages + (size_t)pi.h * page_head_bytes(D);
     int ps = 0, tbase = -64, entry = 0;  // entry: this lane's of the 32 table entries from tbase
     auto issue = [&]() {
-      if (px == pend) {
-        enter();
+      if (px == pi.end) {
+        pi = enter(px);
+        head = p.pages + (size_t)pi.h * page_head_bytes(D);
         tbase = -64;
       }
-      const int u = px - pfirst, half = u < psink ? u : u + plo, e = half / 2;
+      const int u = px - pi.first, half = u < pi.sink ? u : u + pi.lo, e = half / 2;
       if ((unsigned)(e - tbase) >= 32u) {
         tbase = e;
-        entry = e + lane <= plast ? p.table[(size_t)pb * p.max_pages + e + lane] : 0;
+        entry = e + lane <= (pi.len - 1) / kTile ? p.table[(size_t)pi.b * p.max_pages + e + lane] : 0;
       }
       int page = __shfl_sync(0xffffffffu, entry, e - tbase);
       if (lane == 0) {
@@ -373,15 +374,14 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
     uint32_t parity = 0;
     while (x < count) {
       // ---- one segment: the units of one item that are this warp's
-      const Item it = find_item(pref, p.B, heads_rb, nrb, x0 + x);
-      const SeqUnits su(p, p.lens[it.b]);
-      const int len = su.len, sink = su.n_sink, lo = su.lo - su.n_sink, r0 = it.rb * kRows;
+      const Entered it = x >= pi.first && x < pi.end ? pi : enter(x);
+      const int len = it.len, sink = it.sink, lo = it.lo, r0 = it.rb * kRows, first = it.first;
+      const int seg_end = min(it.end, count);
       if (lane == 0) {
-        const Seg sg{(int)(it.first - c0), (int)(it.end - c0), it.b, it.h, it.rb};
+        const Seg sg{w0 + it.first, w0 + it.end, it.b, it.h, it.rb};
         if (x == 0) seg[warp][0] = sg;
         seg[warp][1] = sg;
       }
-      const int first = (int)(it.first - x0), seg_end = min((int)min(it.end - x0, (long long)count), count);
 
       // Q rows as the B operand: lane (g, c) has row 8 nt + g, channels 128 hf + (D/4 or 32) c + 4 s ..
       uint32_t qf[NT][kHalves][kSteps][2];
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], d);
       waiting = false;
-      if (first >= 0 && first + (int)(it.end - it.first) <= count) {
+      if (first >= 0 && it.end <= count) {
         // the whole item
         const float vsc = p.v_scale[it.h];
 #pragma unroll
@@ -686,8 +686,9 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
   // ---- the items that are in several warps, or go on in other CTAs: joined in order.  A warp's last
   // item is in shared memory (the rings are idle now), one that ended in it in the workspace.
   if (!__syncthreads_and(ok)) return;
-  float* mo = reinterpret_cast<float*>(smem);                         // [W][rows][D]
-  float2* mml = reinterpret_cast<float2*>(smem + W * kRows * D * 4);  // [W][rows]
+  constexpr int kPitch = C::kPitch;
+  float* mo = reinterpret_cast<float*>(smem);                              // [W][rows][pitch]
+  float2* mml = reinterpret_cast<float2*>(smem + W * kRows * kPitch * 4);  // [W][rows]
   if (waiting) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
 #pragma unroll
         for (int t = 0; t < kAcc; ++t)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) mo[row * D + channel_of<kQuad>(t, i, g, c)] = o[t][nt][2 * i + k];
+          for (int i = 0; i < 2; ++i) mo[row * kPitch + channel_of<kQuad>(t, i, g, c)] = o[t][nt][2 * i + k];
         if (g == 0) mml[row] = make_float2(m[nt][k], l[nt][k]);
       }
   }
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
 #pragma unroll 4
     for (int i = 0; i <= to - from; ++i) {
       const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float* src = from + i == to && in_ws ? p.part_o + wrow * D : mo + ((from + i) * kRows + row) * D;
+      const float* src = from + i == to && in_ws ? p.part_o + wrow * D : mo + ((from + i) * kRows + row) * kPitch;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) add_vec<kVec>(acc[v], fi, src + (32 * v + lane) * kVec);
     }
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
       for (int k = 0; k < kVec; ++k) acc[v][k] *= fo;
-    const int here = min(32, (parts - i0 + WPR - 1) / WPR);
+    const int here = min(32, (parts - i0 + WPR - 1) / WPR);  // (the loads below do not wait for the weights)
 #pragma unroll 8
     for (int i = 0; i < here; ++i) {
       const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, ml.y, i);
