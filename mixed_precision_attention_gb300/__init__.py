@@ -191,7 +191,7 @@ def attention_window(q, k, v, window: int, sinks: int = 0, return_lse: bool = Tr
         raise ValueError("q, k and v must be on the same device")
     out = torch.empty_like(q)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if return_lse else None
-    _enqueue(dev, "apa_attention_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, int(window),
+    _enqueue(dev.index, "apa_attention_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, int(window),
              int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
     return out, lse
 

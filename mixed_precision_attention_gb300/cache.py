@@ -25,50 +25,60 @@ TABLES_STATUS = {0: "ok", 1: "a length is out of range", 2: "more tokens than ma
                  4: "the free list's count is out of range, or its capacity too small"}
 
 
-def _enqueue(dev, name, *args):
-    """Calls an entry point with the current stream of `dev`, which is made current for it (the raw stream: a decoding
-    step makes several of these calls, and a Stream object costs more than a launch)."""
+_Tensor = torch.Tensor
+_empty = torch.empty
+_i32, _f32, _u8 = torch.int32, torch.float32, torch.uint8
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _enqueue(index, name, *args):
+    """Calls an entry point with the current stream of device `index`, which is made current for it (the raw stream: a
+    decoding step makes several of these calls, and a Stream object costs more than a launch)."""
     fn = getattr(_lib.load(), name)
-    index = dev.index
-    if torch._C._cuda_getDevice() == index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st:
         _lib.check(st, name)
 
 
-def _need(name, t, dtype, dim, dev=None, contiguous=True):
-    if not isinstance(t, torch.Tensor) or t.dim() != dim or (t.dtype is not dtype if dtype else t.dtype not in _DTYPES):
-        raise TypeError(f"{name} must be a {dim}-D tensor of {dtype or 'torch.bfloat16 or torch.float16'}")
+def _need(name, t, dtype, dim, index):
+    """t must be a contiguous `dim`-D tensor of `dtype` on CUDA device `index`."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.dim() == dim and t.get_device() == index and t.is_contiguous():
+        return
+    if not isinstance(t, _Tensor) or t.dim() != dim or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dim}-D tensor of {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be on cuda:{index}, not {t.device}")
+
+
+def _need_rows(name, t, dim):
+    """t must be a `dim`-D bf16 or fp16 CUDA tensor with contiguous channels, the other axes at any stride.  Returns
+    its device's index."""
+    if not isinstance(t, _Tensor) or t.dim() != dim or t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a {dim}-D tensor of torch.bfloat16 or torch.float16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, not {t.device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _need_rows(name, t, dim, dev=None):
-    """16-bit, channels contiguous and 16-byte aligned, the other axes at any stride."""
-    _need(name, t, None, dim, dev, contiguous=False)
     if t.stride(-1) != 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.get_device()
 
 
-def _pool(pages, Hkv=None, d=None):
-    _need("pages", pages, torch.uint8, 3)
-    if pages.shape[2] % 72 or (Hkv is not None and tuple(pages.shape[1:]) != (Hkv, 72 * d)):
+def _need_pool(pages, k_scale, v_scale, index):
+    """Checks a pool and its scales; returns (num_pages, Hkv, d)."""
+    _need("pages", pages, _u8, 3, index)
+    num_pages, Hkv, n = pages.shape
+    if n % 72:
         raise ValueError("pages must be [num_pages, Hkv, 72 * d]")
-    return pages.device
-
-
-def _scales(Hkv, dev, k_scale, v_scale):
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(name, t, torch.float32, 1, dev)
-        if t.shape[0] != Hkv:
-            raise ValueError(f"{name} must be [Hkv]")
+    _need("k_scale", k_scale, _f32, 1, index)
+    _need("v_scale", v_scale, _f32, 1, index)
+    if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
+        raise ValueError("k_scale and v_scale must be [Hkv]")
+    return num_pages, Hkv, n // 72
 
 
 def cache_pages(num_pages: int, Hkv: int, d: int, device="cuda"):
@@ -87,12 +97,14 @@ def cache_tables(old_lens, new_lens, block_table, free_pages, free_count, max_to
     tokens, packed by request (slot -1, position 0 behind the last), starts [B + 1], free_count [1] (in
     free_count_out if given, which may be free_count itself), and status [1] (TABLES_STATUS): where it is not
     0 nothing was changed and every slot is -1."""
-    _need("old_lens", old_lens, torch.int32, 1)
-    dev = old_lens.device
-    _need("new_lens", new_lens, torch.int32, 1, dev)
-    _need("block_table", block_table, torch.int32, 2, dev)
-    _need("free_pages", free_pages, torch.int32, 1, dev)
-    _need("free_count", free_count, torch.int32, 1, dev)
+    if not isinstance(old_lens, _Tensor) or not old_lens.is_cuda:
+        raise ValueError("old_lens must be on a CUDA device")
+    index = old_lens.get_device()
+    _need("old_lens", old_lens, _i32, 1, index)
+    _need("new_lens", new_lens, _i32, 1, index)
+    _need("block_table", block_table, _i32, 2, index)
+    _need("free_pages", free_pages, _i32, 1, index)
+    _need("free_count", free_count, _i32, 1, index)
     B = old_lens.shape[0]
     if new_lens.shape[0] != B or block_table.shape[0] != B or free_count.shape[0] != 1:
         raise ValueError("old_lens and new_lens must be [B], block_table [B, max_pages], free_count [1]")
@@ -100,15 +112,16 @@ def cache_tables(old_lens, new_lens, block_table, free_pages, free_count, max_to
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
     if free_count_out is not None:
-        _need("free_count_out", free_count_out, torch.int32, 1, dev)
+        _need("free_count_out", free_count_out, _i32, 1, index)
         if free_count_out.shape[0] != 1:
             raise ValueError("free_count_out must be [1]")
-    slots = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-    positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-    starts = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
-    count = torch.empty(1, dtype=torch.int32, device=dev) if free_count_out is None else free_count_out
-    _enqueue(dev, "apa_cache_tables", old_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
+    dev = old_lens.device
+    slots = _empty(max_tokens, dtype=_i32, device=dev)
+    positions = _empty(max_tokens, dtype=_i32, device=dev)
+    starts = _empty(B + 1, dtype=_i32, device=dev)
+    status = _empty(1, dtype=_i32, device=dev)
+    count = _empty(1, dtype=_i32, device=dev) if free_count_out is None else free_count_out
+    _enqueue(index, "apa_cache_tables", old_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
              block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), max_tokens,
              slots.data_ptr(), positions.data_ptr(), starts.data_ptr(), count.data_ptr(), status.data_ptr())
     return {"slots": slots, "positions": positions, "starts": starts, "free_count": count, "status": status}
@@ -121,37 +134,36 @@ def cache_write(k, v, slots, pages, k_scale, v_scale):
     8 elements (a projection's [T, Hkv, d] output goes in as ``k.transpose(0, 1)``).  slots: int32 [T], one
     for each token, no two alike; a token of a negative slot is skipped.  pages: the pool, written in place.
     k_scale, v_scale: fp32 [Hkv], positive (largest magnitude expected / 2688; larger values saturate)."""
-    _need_rows("k", k, 3)
-    dev = k.device
-    _need_rows("v", v, 3, dev)
+    index = _need_rows("k", k, 3)
     Hkv, T, d = k.shape
-    if v.shape != k.shape or v.dtype is not k.dtype:
+    if _need_rows("v", v, 3) != index or v.shape != k.shape or v.dtype is not k.dtype:
         raise ValueError("k and v must be alike")
-    _need("slots", slots, torch.int32, 1, dev)
+    _need("slots", slots, _i32, 1, index)
     if slots.shape[0] != T:
         raise ValueError("slots must be [T]")
-    if _pool(pages, Hkv, d) != dev:
-        raise ValueError("pages must be on k's device")
-    _scales(Hkv, dev, k_scale, v_scale)
+    num_pages, heads, dim = _need_pool(pages, k_scale, v_scale, index)
+    if heads != Hkv or dim != d:
+        raise ValueError("pages must be [num_pages, Hkv, 72 * d] with k's Hkv and d")
     kh, kt, _ = k.stride()
     vh, vt, _ = v.stride()
-    _enqueue(dev, "apa_cache_write", k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], Hkv, T, d, kh, kt, vh, vt,
-             slots.data_ptr(), pages.data_ptr(), pages.shape[0], k_scale.data_ptr(), v_scale.data_ptr())
+    _enqueue(index, "apa_cache_write", k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], Hkv, T, d, kh, kt, vh, vt,
+             slots.data_ptr(), pages.data_ptr(), num_pages, k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def cache_read(pages, slots, k_scale, v_scale, dtype=torch.bfloat16):
     """The values that cached tokens stand for (apa_cache_read): k, v [Hkv, T, d] of `dtype` (bf16 or fp16),
     contiguous, so that ``k[None]`` is what attention() takes.  Tokens of negative slots are zero."""
-    dev = _pool(pages)
-    _need("slots", slots, torch.int32, 1, dev)
-    num_pages, Hkv, n = pages.shape
-    _scales(Hkv, dev, k_scale, v_scale)
+    if not isinstance(pages, _Tensor) or not pages.is_cuda:
+        raise ValueError("pages must be on a CUDA device")
+    index = pages.get_device()
+    num_pages, Hkv, d = _need_pool(pages, k_scale, v_scale, index)
+    _need("slots", slots, _i32, 1, index)
     if dtype not in _DTYPES:
         raise TypeError("dtype must be torch.bfloat16 or torch.float16")
-    T, d = slots.shape[0], n // 72
-    k = torch.empty((Hkv, T, d), dtype=dtype, device=dev)
-    v = torch.empty((Hkv, T, d), dtype=dtype, device=dev)
-    _enqueue(dev, "apa_cache_read", pages.data_ptr(), num_pages, _DTYPES[dtype], Hkv, T, d, slots.data_ptr(),
+    T, dev = slots.shape[0], pages.device
+    k = _empty((Hkv, T, d), dtype=dtype, device=dev)
+    v = _empty((Hkv, T, d), dtype=dtype, device=dev)
+    _enqueue(index, "apa_cache_read", pages.data_ptr(), num_pages, _DTYPES[dtype], Hkv, T, d, slots.data_ptr(),
              k_scale.data_ptr(), v_scale.data_ptr(), k.data_ptr(), v.data_ptr())
     return k, v
 
@@ -172,25 +184,24 @@ def attention_cache(q, pages, block_table, lens, k_scale, v_scale, window: int =
     contiguous; lse fp32 [B, Hq, Nq] or None); a row that sees no key gives zeros and -inf.
     workspace: optional uint8 CUDA tensor of at least attention_cache_workspace_bytes(...) bytes; calls that
     can overlap on the GPU need one each."""
-    _need_rows("q", q, 4)
-    dev = q.device
+    index = _need_rows("q", q, 4)
     B, Hq, Nq, d = q.shape
-    if _pool(pages) != dev or pages.shape[2] != 72 * d:
-        raise ValueError("pages must be [num_pages, Hkv, 72 * d] with q's d, on q's device")
-    num_pages, Hkv, _ = pages.shape
-    _need("block_table", block_table, torch.int32, 2, dev)
-    _need("lens", lens, torch.int32, 1, dev)
+    num_pages, Hkv, dim = _need_pool(pages, k_scale, v_scale, index)
+    if dim != d:
+        raise ValueError("pages must be [num_pages, Hkv, 72 * d] with q's d")
+    _need("block_table", block_table, _i32, 2, index)
+    _need("lens", lens, _i32, 1, index)
     if block_table.shape[0] != B or lens.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages] and lens [B]")
-    _scales(Hkv, dev, k_scale, v_scale)
+    dev = q.device
     if workspace is None:
-        workspace = torch.empty(attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d), dtype=torch.uint8, device=dev)
+        workspace = _empty(attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d), dtype=_u8, device=dev)
     else:
-        _need("workspace", workspace, torch.uint8, 1, dev)
-    out = torch.empty((B, Hq, Nq, d), dtype=q.dtype, device=dev)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if return_lse else None
+        _need("workspace", workspace, _u8, 1, index)
+    out = _empty((B, Hq, Nq, d), dtype=q.dtype, device=dev)
+    lse = _empty((B, Hq, Nq), dtype=_f32, device=dev) if return_lse else None
     qb, qh, qr, _ = q.stride()
-    _enqueue(dev, "apa_attention_cache", q.data_ptr(), _DTYPES[q.dtype], qb, qh, qr, pages.data_ptr(), num_pages,
+    _enqueue(index, "apa_attention_cache", q.data_ptr(), _DTYPES[q.dtype], qb, qh, qr, pages.data_ptr(), num_pages,
              block_table.data_ptr(), block_table.shape[1], lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hq,
              Hkv, Nq, d, int(window), int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr(),
              workspace.data_ptr(), workspace.numel())
