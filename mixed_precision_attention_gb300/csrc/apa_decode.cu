@@ -64,18 +64,19 @@ struct DecodeParams {
                     // slot 2 kCtas + warp is a warp's part of an item that ends in it
 };
 
-// kRows rows share the keys: 8 per n = 8 tile, or 4, which then take a tile of V^T P^T
-// twice (see there).  Registers set the number of warps.
+// kRows rows share the keys: 8 per n = 8 tile, or 4 (kQuad), which then take a tile of
+// V^T P^T twice (see there).
 template <int D, int ROWS>
 struct DecCfg {
   static constexpr int kRows = ROWS;
   static constexpr int NT = ROWS < 8 ? 1 : ROWS / 8;
   static constexpr bool kQuad = ROWS == 4;
   static constexpr int kAcc = kQuad ? D / 32 : D / 16;   // product tiles of O^T per n tile
-  static constexpr int kRegs = (kAcc * 4 + D / 8) * NT;  // O and Q
-  static constexpr int W = D == 256 ? 8 : kRegs <= 48 ? 16 : kRegs <= 96 ? 12 : 8;  // (d = 256: two stages must fit)
+  // Warps: what the registers of O and Q leave room for (16 rows at d = 64: 12 warps 37 us,
+  // 16 warps 39; 8 rows at d = 128: 35 and 33); at d = 256 two stages must fit.
+  static constexpr int W = D == 256 ? 8 : ROWS <= 8 ? 16 : D * ROWS <= 2048 ? 12 : 8;
   static constexpr int kUnitBytes = 36 * D;
-  static constexpr int kScaleBytes = 8 * D;  // a unit's V scales as FP16 pairs, per warp
+  static constexpr int kScaleBytes = kQuad ? 8 * D : 4 * D;  // a unit's V scales as FP16 pairs, per warp
   static constexpr int kMaxStages = 6;
   static constexpr int kStaticBytes = 1536;  // room for the kernel's static arrays
   static constexpr int kSlots = kCtas * (2 + W);
@@ -201,7 +202,7 @@ __device__ __forceinline__ T lds(const uint8_t* p) {
 // The channel of o[t][.][2 i + k] in lane (g, c), and the row of the block (of n tile nt).
 template <bool QUAD>
 __device__ __forceinline__ int channel_of(int t, int i, int g, int c) {
-  return QUAD ? 32 * t + 16 * i + 8 * (c >> 1) + g : 16 * ((t & ~1) + i) + 8 * (t & 1) + g;
+  return QUAD ? 32 * t + 16 * i + 8 * (c >> 1) + g : 16 * t + 8 * i + g;
 }
 template <bool QUAD>
 __device__ __forceinline__ int row_of(int nt, int c, int k) {
@@ -552,15 +553,16 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
             pf[mb][nt][1] = transpose8(pack2<true>(p2, p3));
           }
         }
-        // ---- O^T += V^T P^T.  A code byte holds channels g and 8 + g of a tile for one key; its
-        // FP16 pair goes into the product as it is, as two steps of the summed axis, against P
-        // with zeros at every other step: (P, 0) gives the channels g, (0, P) the channels 8 + g.
-        // That spares the integer pipe the permutes that pairing two keys would take, for twice
-        // the products; with up to four rows both forms of P share one product's eight columns.
-        // Rows g and g + 8 of a product are tiles t and t + 1.
-        // The scales come as FP16 pairs (s, s), converted once per warp: word i of a block holds
-        // those of keys 4 (i / kTiles) .. + 3 for tile i % kTiles.  Keys past the end: whatever
-        // the page holds there (NaN too) counts as 0.
+        // ---- O^T += V^T P^T.  A code byte holds channels g and 8 + g of a tile for one key, a
+        // word four keys.  The products sum over pairs of keys: the FP16 pairs of two keys are
+        // permuted into rows g and 8 + g.  With up to four rows the pair goes in as it is, as two
+        // steps of the summed axis, against P with zeros at every other step: (P, 0) in columns
+        // 0 .. 3 gives the channels g, (0, P) in columns 4 .. 7 the channels 8 + g, and rows g and
+        // g + 8 are tiles t and t + 1: as many products, and no permutes, of which the integer
+        // pipe would be full.
+        // The scales come as FP16 pairs, converted once per warp: word i of a block holds those of
+        // keys 4 (i / kTiles) .. + 3 for tile i % kTiles.  Keys past the end: whatever the page
+        // holds there (NaN too) counts as 0.
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
@@ -569,55 +571,60 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
             uint32_t w = lds<uint32_t>(unit + mb * blk_bytes(D) + blk_vs(D) + 4 * i);
             if (left < 4) w &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
             const uint32_t f0 = e4m3x2(w & 0xFFFFu), f1 = e4m3x2(w >> 16);
-            *reinterpret_cast<uint4*>(scales + 4 * D * mb + 16 * (4 * (i % kTiles) + kc)) =
-                make_uint4(__byte_perm(f0, 0, 0x1010), __byte_perm(f0, 0, 0x3232), __byte_perm(f1, 0, 0x1010),
-                           __byte_perm(f1, 0, 0x3232));
+            uint8_t* dst = scales + mb * (C::kScaleBytes / 2) + (kQuad ? 16 : 8) * (4 * (i % kTiles) + kc);
+            if constexpr (kQuad)  // (s, s) of each key
+              *reinterpret_cast<uint4*>(dst) =
+                  make_uint4(__byte_perm(f0, 0, 0x1010), __byte_perm(f0, 0, 0x3232), __byte_perm(f1, 0, 0x1010),
+                             __byte_perm(f1, 0, 0x3232));
+            else  // of two keys
+              *reinterpret_cast<uint2*>(dst) = make_uint2(f0, f1);
           }
         __syncwarp();
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
           const uint8_t* blk = unit + mb * blk_bytes(D);
-          // [keys 4c, 4c + 1 | 4c + 2, 4c + 3][(P, 0) of both, (0, P) of both]; with four rows lanes
-          // g < 4 take (P, 0) and the others (0, P)
-          uint32_t pz[NT][2][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          const uint8_t* sc_mb = scales + mb * (C::kScaleBytes / 2);
+          // (four rows) lanes g < 4 take (P, 0), the others (0, P), of keys 4c, 4c + 1 and 4c + 2, 4c + 3
+          uint32_t pz[2][2];
+          if constexpr (kQuad) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t w = pf[mb][nt][i];
-              if constexpr (kQuad) {
-                pz[nt][i][0] = __byte_perm(w, 0, g < 4 ? 0x4410 : 0x1044);
-                pz[nt][i][1] = __byte_perm(w, 0, g < 4 ? 0x4432 : 0x3244);
-              } else {
-                pz[nt][i][0] = w & 0xFFFFu;
-                pz[nt][i][1] = w >> 16;
-                pz[nt][i][2] = w << 16;
-                pz[nt][i][3] = w & 0xFFFF0000u;
-              }
+              pz[i][0] = __byte_perm(pf[mb][0][i], 0, g < 4 ? 0x4410 : 0x1044);
+              pz[i][1] = __byte_perm(pf[mb][0][i], 0, g < 4 ? 0x4432 : 0x3244);
             }
+          }
 #pragma unroll
           for (int tq = 0; tq < kTiles / 4; ++tq) {
             const uint4 vw = lds<uint4>(blk + blk_v(D) + 512 * tq + 16 * lane);
             const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
+            if constexpr (kQuad) {
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const int t = 4 * tq + k;
-              const uint4 sa = lds<uint4>(scales + 4 * D * mb + 16 * (4 * t + c));
-              const uint4 sb = lds<uint4>(scales + 4 * D * mb + 16 * (4 * t + 4 + c));
-              uint32_t ha[4], hb[4];
-              e2m1x8(w4[k], ha);  // [key 4c + i]
-              e2m1x8(w4[k + 1], hb);
-              ha[0] = hmul2(ha[0], sa.x), ha[1] = hmul2(ha[1], sa.y), ha[2] = hmul2(ha[2], sa.z), ha[3] = hmul2(ha[3], sa.w);
-              hb[0] = hmul2(hb[0], sb.x), hb[1] = hmul2(hb[1], sb.y), hb[2] = hmul2(hb[2], sb.z), hb[3] = hmul2(hb[3], sb.w);
+              for (int k = 0; k < 4; k += 2) {
+                const int t = 4 * tq + k;
+                const uint4 sa = lds<uint4>(sc_mb + 16 * (4 * t + c)), sb = lds<uint4>(sc_mb + 16 * (4 * t + 4 + c));
+                uint32_t ha[4], hb[4];
+                e2m1x8(w4[k], ha);  // [key 4c + i]
+                e2m1x8(w4[k + 1], hb);
+                ha[0] = hmul2(ha[0], sa.x), ha[1] = hmul2(ha[1], sa.y), ha[2] = hmul2(ha[2], sa.z), ha[3] = hmul2(ha[3], sa.w);
+                hb[0] = hmul2(hb[0], sb.x), hb[1] = hmul2(hb[1], sb.y), hb[2] = hmul2(hb[2], sb.z), hb[3] = hmul2(hb[3], sb.w);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < 2; ++i)
+                  mma_f16(o[t / 2][0], ha[2 * i], hb[2 * i], ha[2 * i + 1], hb[2 * i + 1], pz[i][0], pz[i][1]);
+              }
+            } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  float* od = o[kQuad ? t / 2 : t][nt];
-                  mma_f16(od, ha[2 * i], hb[2 * i], ha[2 * i + 1], hb[2 * i + 1], pz[nt][i][0], pz[nt][i][1]);
-                  if constexpr (!kQuad)
-                    mma_f16(o[t + 1][nt], ha[2 * i], hb[2 * i], ha[2 * i + 1], hb[2 * i + 1], pz[nt][i][2], pz[nt][i][3]);
-                }
+              for (int k = 0; k < 4; ++k) {
+                const int t = 4 * tq + k;
+                const uint2 f = lds<uint2>(sc_mb + 8 * (4 * t + c));
+                uint32_t h[4];
+                e2m1x8(w4[k], h);  // [key 4c + i]
+                const uint32_t a0 = hmul2(__byte_perm(h[0], h[1], 0x5410), f.x);
+                const uint32_t a1 = hmul2(__byte_perm(h[0], h[1], 0x7632), f.x);
+                const uint32_t a2 = hmul2(__byte_perm(h[2], h[3], 0x5410), f.y);
+                const uint32_t a3 = hmul2(__byte_perm(h[2], h[3], 0x7632), f.y);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, pf[mb][nt][0], pf[mb][nt][1]);
+              }
             }
           }
         }
