@@ -56,7 +56,7 @@ struct DecodeParams {
   uint16_t* out;
   float* lse;
   int* err;
-  int nstages;
+  int nstages, ring_off;
   // workspace
   int* pref;        // [B + 1] units before each sequence (of one head and row block)
   float2* part_ml;  // [slots][rows] (m, l): slots 2 cta + 1 and 2 cta are the CTA's part of the item
@@ -77,22 +77,30 @@ struct DecCfg {
   static constexpr int W = D == 256 ? 8 : ROWS <= 8 ? 16 : D * ROWS <= 2048 ? 12 : 8;
   static constexpr int kUnitBytes = 36 * D;
   static constexpr int kScaleBytes = kQuad ? 8 * D : 4 * D;  // a unit's V scales as FP16 pairs, per warp
+  // Q's fragments in shared memory, where registers are short (32 rows at d = 128: 93 us with
+  // them in registers, spilling, and 70 so)
+  static constexpr bool kQShared = D * ROWS >= 2048;
+  static constexpr int kQBytes = kQShared ? NT * D * 16 : 0;  // per warp
   static constexpr int kMaxStages = 6;
   static constexpr int kStaticBytes = 1536;  // room for the kernel's static arrays
   static constexpr int kSlots = kCtas * (2 + W);
   static constexpr int kBarBytes = W * kMaxStages * 8 + 16;
   static constexpr int kPitch = D + (kQuad ? 8 : 4);  // floats per row of a state in shared memory: no bank twice
   static constexpr int kMergeBytes = W * kRows * (kPitch + 2) * 4;
-  static int stages(int B) {
-    const int room = 232448 - W * kScaleBytes - kBarBytes - (B + 1) * 4 - kStaticBytes;
-    const int n = room / (W * kUnitBytes);
+  // Shared memory: the barriers, the warps' scales and Q, the units before each sequence, the
+  // rings (the joined states take the place of all but the barriers at the end).
+  static constexpr int kScaleOff = kBarBytes, kQOff = kScaleOff + W * kScaleBytes, kPrefOff = kQOff + W * kQBytes;
+  static constexpr int ring_off(int B) { return kPrefOff + ((B + 1) * 4 + 15) / 16 * 16; }
+  static constexpr int stages(int B) {
+    const int n = (232448 - kStaticBytes - ring_off(B)) / (W * kUnitBytes);
     return n > kMaxStages ? kMaxStages : n;
   }
-  static int ring_bytes(int B) {
-    const int r = stages(B) * W * kUnitBytes;
-    return r > kMergeBytes ? r : kMergeBytes;
+  static constexpr int smem(int B) {
+    const int r = ring_off(B) + W * stages(B) * kUnitBytes, m = kBarBytes + kMergeBytes;
+    return r > m ? r : m;
   }
-  static int smem(int B) { return ring_bytes(B) + W * kScaleBytes + kBarBytes + (B + 1) * 4; }
+  // (two stages or more, but for 16 rows at d = 256 from 2600 sequences on: one, without overlap)
+  static constexpr bool kFits = stages(kMaxSeqs) >= 1 && smem(kMaxSeqs) <= 232448 - kStaticBytes;
   static size_t ws_bytes(int B) {
     return align256((size_t)(B + 1) * 4) + align256((size_t)kSlots * kRows * 8) + (size_t)kSlots * kRows * D * 4;
   }
@@ -254,6 +262,7 @@ struct Seg {  // an item that a warp holds units of; counted from the CTA's firs
 template <int D, int ROWS, bool F16>
 __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(const DecodeParams p) {
   using C = DecCfg<D, ROWS>;
+  static_assert(C::kFits, "shared memory");
   constexpr int W = C::W, kRows = C::kRows, NT = C::NT, kAcc = C::kAcc;
   constexpr bool kQuad = C::kQuad;
   constexpr int kHalves = D == 256 ? 2 : 1;      // 128-channel halves of a K row
@@ -261,13 +270,13 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
   constexpr int kTiles = D / 16;                 // 16-channel tiles of V
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int ring = p.nstages * W * C::kUnitBytes > C::kMergeBytes ? p.nstages * W * C::kUnitBytes : C::kMergeBytes;
-  uint8_t* scales = smem + ring + warp * C::kScaleBytes;
-  uint8_t* behind = smem + ring + W * C::kScaleBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(behind) + warp * C::kMaxStages;
-  int* abort_flag = reinterpret_cast<int*>(behind + W * C::kMaxStages * 8);
-  int* pref = reinterpret_cast<int*>(behind + C::kBarBytes);
-  const uint32_t bar0 = smem_u32(bars), stage0 = smem_u32(smem) + warp * p.nstages * C::kUnitBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem) + warp * C::kMaxStages;
+  int* abort_flag = reinterpret_cast<int*>(smem + W * C::kMaxStages * 8);
+  uint8_t* scales = smem + C::kScaleOff + warp * C::kScaleBytes;
+  uint8_t* qsh = smem + C::kQOff + warp * C::kQBytes + 8 * lane;
+  int* pref = reinterpret_cast<int*>(smem + C::kPrefOff);
+  const int ring = p.ring_off + warp * p.nstages * C::kUnitBytes;
+  const uint32_t bar0 = smem_u32(bars), stage0 = smem_u32(smem) + ring;
 
   if (lane < C::kMaxStages) mbar_init(bar0 + 8 * lane, 1);
   if (tid == 0) *abort_flag = 0;
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
       }
 
       // Q rows as the B operand: lane (g, c) has row 8 nt + g, channels 128 hf + (D/4 or 32) c + 4 s ..
-      uint32_t qf[NT][kHalves][kSteps][2];
+      uint32_t qf[C::kQShared ? 1 : NT][kHalves][kSteps][2];
       float rf[NT][2];  // score factor of rows 2c, 2c + 1: the power of two back, and k_scale log2(e) / sqrt(d)
       const float sc = p.k_scale[it.h] * kLog2e * rsqrtf((float)D);
 #pragma unroll
@@ -416,8 +425,13 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
             const float2 u = unpack2<F16>(raw[hf][s].x), v = unpack2<F16>(raw[hf][s].y);
-            qf[nt][hf][s][0] = pack2<true>(u.x * up, u.y * up);
-            qf[nt][hf][s][1] = pack2<true>(v.x * up, v.y * up);
+            const uint32_t q0 = pack2<true>(u.x * up, u.y * up), q1 = pack2<true>(v.x * up, v.y * up);
+            if constexpr (C::kQShared) {
+              *reinterpret_cast<uint2*>(qsh + 256 * ((nt * kHalves + hf) * kSteps + s)) = make_uint2(q0, q1);
+            } else {
+              qf[nt][hf][s][0] = q0;
+              qf[nt][hf][s][1] = q1;
+            }
           }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -438,7 +452,7 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
           ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, parity, abort_flag, p.err));
           if (!ok) break;
         }
-        const uint8_t* unit = smem + (warp * p.nstages + st) * C::kUnitBytes;
+        const uint8_t* unit = smem + ring + st * C::kUnitBytes;
         const int u = x - first, j0 = (u < sink ? u : u + lo) * kUnit;
         // ---- S^T = K Q^T.  Rows g and g + 8 of the product are keys 4 (g/2) + g%2 and that + 2, so
         // that a lane's four keys of V^T below are neighbours.  Both blocks go side by side.
@@ -471,7 +485,11 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
               }
             }
 #pragma unroll
-          for (int w = 0; w < kSteps / 2; ++w)
+          for (int w = 0; w < kSteps / 2; ++w) {
+            auto q_at = [&](int nt, int i) -> uint2 {  // of product 2 w + i
+              if constexpr (C::kQShared) return lds<uint2>(qsh + 256 * ((nt * kHalves + hf) * kSteps + 2 * w + i));
+              return make_uint2(qf[C::kQShared ? 0 : nt][hf][2 * w + i][0], qf[C::kQShared ? 0 : nt][hf][2 * w + i][1]);
+            };
 #pragma unroll
             for (int mb = 0; mb < 2; ++mb) {
               // a lane's words 0, 1 (16 codes) share its first scale, words 2, 3 the second
@@ -487,10 +505,12 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
               }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma_f16(s[mb][nt], ha[0], hb[0], ha[1], hb[1], qf[nt][hf][2 * w][0], qf[nt][hf][2 * w][1]);
-                mma_f16(s[mb][nt], ha[2], hb[2], ha[3], hb[3], qf[nt][hf][2 * w + 1][0], qf[nt][hf][2 * w + 1][1]);
+                const uint2 q0 = q_at(nt, 0), q1 = q_at(nt, 1);
+                mma_f16(s[mb][nt], ha[0], hb[0], ha[1], hb[1], q0.x, q0.y);
+                mma_f16(s[mb][nt], ha[2], hb[2], ha[3], hb[3], q1.x, q1.y);
               }
             }
+          }
         }
         // ---- softmax: s[mb][nt] = keys kg (0, 1) and kg + 2 (2, 3) of block mb, rows 2c and 2c + 1,
         // still without the row's factor rf
@@ -694,8 +714,8 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
   // item is in shared memory (the rings are idle now), one that ended in it in the workspace.
   if (!__syncthreads_and(ok)) return;
   constexpr int kPitch = C::kPitch;
-  float* mo = reinterpret_cast<float*>(smem);                              // [W][rows][pitch]
-  float2* mml = reinterpret_cast<float2*>(smem + W * kRows * kPitch * 4);  // [W][rows]
+  float* mo = reinterpret_cast<float*>(smem + C::kBarBytes);                 // [W][rows][pitch]
+  float2* mml = reinterpret_cast<float2*>(mo + W * kRows * kPitch);          // [W][rows]
   if (waiting) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -874,6 +894,7 @@ cudaError_t launch_decode(DecodeParams prm, void* ws, cudaStream_t stream) {
   w += C::align256((size_t)C::kSlots * C::kRows * 8);
   prm.part_o = (float*)w;
   prm.nstages = C::stages(prm.B);
+  prm.ring_off = C::ring_off(prm.B);
   cudaError_t e;
   const int smem = C::smem(prm.B);
   // the largest size, once per device (a bit each)

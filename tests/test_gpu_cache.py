@@ -479,3 +479,25 @@ def test_a_cached_prefix_feeds_prefill():
     out, _, _ = apa.attention(q, k[None], v[None], eps=0.0)
     ref, _, _ = _attend(q.double().cpu().numpy(), [[x.double().cpu().numpy() for x in (k, v)]], [n], 0, 0)
     assert np.abs(out.cpu().numpy() - ref).max() <= 4e-3  # attention()'s own bound at eps = 0
+
+
+@pytest.mark.parametrize("B,Hq,H,Nq,d", [(8192, 1, 1, 1, 64), (3000, 4, 1, 4, 256), (8192, 8, 1, 4, 128)])
+def test_attention_cache_many_sequences(B, Hq, H, Nq, d):
+    # as many sequences as the calls allow, most of them empty; the rest share their pages
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(B + d)
+    n0 = 40
+    pages, table, ks, vs, kv = _cache(rng, 1, H, d, [n0], 1)
+    lens = np.where(rng.integers(0, 8, B) == 0, rng.integers(1, n0 + 1, B), 0)
+    lens[-1] = n0
+    q = _torch(rng.standard_normal((B, Hq, Nq, d)), torch.bfloat16)
+    out, lse = apa.attention_cache(q, pages, table.expand(B, 1).contiguous(), _torch(lens.astype(np.int32)), _torch(ks),
+                                   _torch(vs))
+    apa.check_error()
+    some = np.concatenate([np.flatnonzero(lens)[:20], np.flatnonzero(lens == 0)[:5], [B - 1]])
+    ref = _attend(q[some].double().cpu().numpy(), [[x[:, :lens[b]] for x in kv[0]] for b in some], lens[some], 0, 0)
+    _near(out[some], lse[some], ref, "bf16")
+    empty = _torch(lens == 0)
+    assert not out[empty].any() and torch.isneginf(lse[empty]).all()
