@@ -454,6 +454,26 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
         }
         const uint8_t* unit = smem + ring + st * C::kUnitBytes;
         const int u = x - first, j0 = (u < sink ? u : u + lo) * kUnit;
+        // ---- V's scales as FP16 pairs, converted once per warp (here, so that nothing below waits):
+        // word i of a block holds those of keys 4 (i / kTiles) .. + 3 for tile i % kTiles.  Keys past
+        // the end: whatever the page holds there (NaN too) counts as 0.
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int i = lane; i < 4 * kTiles; i += 32) {
+            const int kc = i / kTiles, left = len - (j0 + 16 * mb + 4 * kc);
+            uint32_t w = lds<uint32_t>(unit + mb * blk_bytes(D) + blk_vs(D) + 4 * i);
+            if (left < 4) w &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            const uint32_t f0 = e4m3x2(w & 0xFFFFu), f1 = e4m3x2(w >> 16);
+            uint8_t* dst = scales + mb * (C::kScaleBytes / 2) + (kQuad ? 16 : 8) * (4 * (i % kTiles) + kc);
+            if constexpr (kQuad)  // (s, s) of each key
+              *reinterpret_cast<uint4*>(dst) =
+                  make_uint4(__byte_perm(f0, 0, 0x1010), __byte_perm(f0, 0, 0x3232), __byte_perm(f1, 0, 0x1010),
+                             __byte_perm(f1, 0, 0x3232));
+            else  // of two keys
+              *reinterpret_cast<uint2*>(dst) = make_uint2(f0, f1);
+          }
+        __syncwarp();
         // ---- S^T = K Q^T.  Rows g and g + 8 of the product are keys 4 (g/2) + g%2 and that + 2, so
         // that a lane's four keys of V^T below are neighbours.  Both blocks go side by side.
         float s[2][NT][4];
@@ -580,26 +600,6 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
         // 0 .. 3 gives the channels g, (0, P) in columns 4 .. 7 the channels 8 + g, and rows g and
         // g + 8 are tiles t and t + 1: as many products, and no permutes, of which the integer
         // pipe would be full.
-        // The scales come as FP16 pairs, converted once per warp: word i of a block holds those of
-        // keys 4 (i / kTiles) .. + 3 for tile i % kTiles.  Keys past the end: whatever the page
-        // holds there (NaN too) counts as 0.
-#pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-          for (int i = lane; i < 4 * kTiles; i += 32) {
-            const int kc = i / kTiles, left = len - (j0 + 16 * mb + 4 * kc);
-            uint32_t w = lds<uint32_t>(unit + mb * blk_bytes(D) + blk_vs(D) + 4 * i);
-            if (left < 4) w &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-            const uint32_t f0 = e4m3x2(w & 0xFFFFu), f1 = e4m3x2(w >> 16);
-            uint8_t* dst = scales + mb * (C::kScaleBytes / 2) + (kQuad ? 16 : 8) * (4 * (i % kTiles) + kc);
-            if constexpr (kQuad)  // (s, s) of each key
-              *reinterpret_cast<uint4*>(dst) =
-                  make_uint4(__byte_perm(f0, 0, 0x1010), __byte_perm(f0, 0, 0x3232), __byte_perm(f1, 0, 0x1010),
-                             __byte_perm(f1, 0, 0x3232));
-            else  // of two keys
-              *reinterpret_cast<uint2*>(dst) = make_uint2(f0, f1);
-          }
-        __syncwarp();
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
           const uint8_t* blk = unit + mb * blk_bytes(D);
