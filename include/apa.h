@@ -355,8 +355,8 @@ int apa_cache_read(const uint8_t* pages, int num_pages, int dtype, int Hkv, int 
  *            on the GPU must not share one.
  * K, V and Q enter the products exactly (E2M1 * UE4M3 and a row of Q divided by a
  * power of two are FP16 values), with FP32 accumulation; the softmax weights are
- * rounded to FP16 for the product with V.  B <= 8192.  The work is split over the GPU
- * by the lengths alone, so reruns are bitwise equal. */
+ * rounded to FP16 for the product with V.  B <= 8192, B * max_pages < 2^29.  The work is
+ * split over the GPU by the lengths alone, so reruns are bitwise equal. */
 int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
                         long long q_row_stride, const uint8_t* pages, int num_pages, const int32_t* block_table,
                         int max_pages, const int32_t* lens, const float* k_scale, const float* v_scale, int B, int Hq,

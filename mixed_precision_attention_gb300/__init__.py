@@ -25,18 +25,18 @@ __all__ = ["attention", "attention_paged", "attention_host", "quantize", "quanti
            "cache_tables", "cache_write", "cache_read", "attention_cache", "attention_cache_workspace_bytes",
            "TABLES_STATUS"]
 
-_CACHE = frozenset(("cache_pages", "cache_tables", "cache_write", "cache_read", "attention_cache",
-                    "attention_cache_workspace_bytes", "TABLES_STATUS"))
+_LATER = {n: "cache" for n in ("cache_pages", "cache_tables", "cache_write", "cache_read", "attention_cache",
+                               "attention_cache_workspace_bytes", "TABLES_STATUS")}
+_LATER["attention_window"] = "window"
 
 
 def __getattr__(name):
-    """The cache operators, from the module that holds them (imported with their first use, as torch is)."""
-    if name in _CACHE:
-        from . import cache
-        for n in _CACHE:
-            globals()[n] = getattr(cache, n)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    """The operators that have modules of their own, imported with their first use (as torch is)."""
+    if name not in _LATER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    value = globals()[name] = getattr(importlib.import_module("." + _LATER[name], __name__), name)
+    return value
 
 
 FLAG_Q_RESIDUAL = 1  # APA_FLAG_Q_RESIDUAL: Q as two FP4 terms in pass 1
@@ -174,26 +174,6 @@ def attention_paged(q, k_pages, v_pages, block_table, Nkv: int, causal: bool = T
                                  _ptr(out), _ptr(lse), _ptr(mask), _stream(dev))
     _lib.check(st, "apa_attention_paged")
     return out, lse, mask
-
-
-def attention_window(q, k, v, window: int, sinks: int = 0, return_lse: bool = True):
-    """apa_attention_window: exact causal attention with a sliding window and sinks.
-
-    q: [B, Hq, Nq, d] bf16; k, v: [B, Hkv, Nkv, d] bf16 (CUDA, contiguous, Nkv >= Nq).  Query row i, at
-    position p = i + Nkv - Nq, sees the keys j <= p with j > p - window (window >= 1 keys, its own among
-    them) or j < sinks.  Returns (out bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] or None)."""
-    import torch
-
-    from .cache import _enqueue
-    B, Hq, Hkv, Nq, Nkv, d = _check_qkv(q, k, v)
-    dev = q.device
-    if k.device != dev or v.device != dev:
-        raise ValueError("q, k and v must be on the same device")
-    out = torch.empty_like(q)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if return_lse else None
-    _enqueue(dev.index, "apa_attention_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, int(window),
-             int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
-    return out, lse
 
 
 def attention_host(q, k, v, causal: bool = True, eps: float = 0.005, return_hot_mask: bool = False, stream=None,

@@ -605,7 +605,7 @@ int apa_cache_tables(const int32_t* old_lens, const int32_t* new_lens, int B, in
   int ncta = 1;
   while (ncta < 8 && ncta * 4096 < max_tokens) ncta *= 2;
   const int smem = 5 * B * (int)sizeof(int);
-  if (smem > 48 * 1024 &&
+  if (smem > 40 * 1024 &&  // (48 KB with the static arrays need no leave)
       cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 5 * kMaxRequests * 4))
     return APA_ERR_CUDA;
   if (ncta == 1) {  // (a plain launch takes the host less time)

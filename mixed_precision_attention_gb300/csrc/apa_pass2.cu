@@ -45,6 +45,7 @@
 // 1's, in that order.  The per-row work is
 // the same as the one-group kernel's; only the tile-to-accumulator assignment
 // (and so the rounding order of the merge) differs.
+#include <atomic>
 #include <cstring>
 #include <cuda_fp16.h>
 
@@ -1210,7 +1211,14 @@ cudaError_t launch_window_d(const P2Params& prm, const CUtensorMap& km, const CU
   const int grid = prm.s.BH() * prm.s.nblk();
   cudaError_t e;
   const int smem = P2Cfg<D, true>::kSmem;
-  if ((e = cudaFuncSetAttribute(pass2_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+  static std::atomic<uint64_t> ready{0};  // once per device (a bit each)
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev))) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(ready.load() & bit)) {
+    if ((e = cudaFuncSetAttribute(pass2_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    if (dev <= 63) ready.fetch_or(bit);
+  }
   pass2_kernel<D, true><<<grid, kThreads, smem, st>>>(prm, km, vm);
   return cudaGetLastError();
 }

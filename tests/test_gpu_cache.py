@@ -112,7 +112,8 @@ def _batch(rng, B, longest, spare):
 
 
 @pytest.mark.parametrize("B,longest,spare", [(1, 1, 0), (1, 64, 0), (3, 65, 1), (40, 1000, 0), (1024, 200, 7),
-                                             (1025, 130, 3), (8192, 70, 0), (5, 30000, 2)])
+                                             (1025, 130, 3), (2048, 70, 1), (2456, 70, 0),
+                                             (8192, 70, 0), (5, 30000, 2)])
 def test_tables(B, longest, spare):
     import torch
 
@@ -501,3 +502,81 @@ def test_attention_cache_many_sequences(B, Hq, H, Nq, d):
     _near(out[some], lse[some], ref, "bf16")
     empty = _torch(lens == 0)
     assert not out[empty].any() and torch.isneginf(lse[empty]).all()
+
+
+def test_bindings_refuse_what_does_not_fit():
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    dev = "cuda"
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+    f32 = torch.ones(2, device=dev)
+    k = torch.zeros(2, 3, 64, dtype=torch.bfloat16, device=dev)
+    pages, q = apa.cache_pages(3, 2, 64), torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=dev)
+    refused = [
+        lambda: apa.cache_tables(i32(2), i32(3), i32(2, 4), i32(5), i32(1), 4),
+        lambda: apa.cache_tables(i32(2), i32(2), i32(3, 4), i32(5), i32(1), 4),
+        lambda: apa.cache_tables(i32(2), i32(2), i32(2, 4), i32(5), i32(2), 4),
+        lambda: apa.cache_tables(i32(2), i32(2), i32(4, 2).t(), i32(5), i32(1), 4),
+        lambda: apa.cache_tables(i32(2), i32(2), i32(2, 4), i32(5), i32(1), -1),
+        lambda: apa.cache_write(k, k[:, :2], i32(3), pages, f32, f32),
+        lambda: apa.cache_write(k, k.half(), i32(3), pages, f32, f32),
+        lambda: apa.cache_write(k, k, i32(2), pages, f32, f32),
+        lambda: apa.cache_write(k, k, i32(3), apa.cache_pages(3, 1, 64), f32[:1], f32[:1]),
+        lambda: apa.cache_write(k, k, i32(3), apa.cache_pages(3, 2, 128), f32, f32),
+        lambda: apa.cache_write(k, k, i32(3), pages, f32[:1], f32),
+        lambda: apa.cache_write(k.transpose(1, 2), k.transpose(1, 2), i32(64), pages, f32, f32),
+        lambda: apa.cache_read(pages[:, :, :100].contiguous(), i32(3), f32, f32),
+        lambda: apa.attention_cache(q, pages, i32(3, 4), i32(2), f32, f32),
+        lambda: apa.attention_cache(q, pages, i32(2, 4), i32(3), f32, f32),
+        lambda: apa.attention_cache(q, apa.cache_pages(3, 2, 128), i32(2, 4), i32(2), f32, f32),
+        lambda: apa.attention_window(q, k[None], k[None], 4),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was taken")
+    with pytest.raises(TypeError):
+        apa.attention_cache(q.float(), pages, i32(2, 4), i32(2), f32, f32)
+    with pytest.raises(TypeError):
+        apa.attention_cache(q, pages, i32(2, 4).long(), i32(2), f32, f32)
+    with pytest.raises(TypeError):
+        apa.cache_read(pages, i32(3), f32, f32, dtype=torch.float32)
+    for window, sinks in ((-1, 0), (4, -1)):
+        with pytest.raises(apa.ApaError):
+            apa.attention_cache(q, pages, i32(2, 4), i32(2), f32, f32, window=window, sinks=sinks)
+    with pytest.raises(apa.ApaError):  # rows that do not start on 16 bytes
+        wide = torch.zeros(2, 4, 1, 68, dtype=torch.bfloat16, device=dev)
+        apa.attention_cache(wide[..., :64], pages, i32(2, 4), i32(2), f32, f32)
+    need = apa.attention_cache_workspace_bytes(2, 4, 2, 1, 64)
+    with pytest.raises(apa.ApaError):
+        apa.attention_cache(q, pages, i32(2, 4), i32(2), f32, f32, workspace=torch.zeros(need - 1, dtype=torch.uint8, device=dev))
+    ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+    out, lse = apa.attention_cache(q, pages, i32(2, 4), i32(2), f32, f32, workspace=ws)
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_two_streams_at_once():
+    """Two sequences' writes and attention on two streams, interleaved: each has its own workspace and pages."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(12)
+    args, want = [], []
+    for d in (64, 128):
+        pages, table, ks, vs, _ = _cache(rng, 3, 2, d, [700, 64, 1], 12)
+        q = _torch(rng.standard_normal((3, 6, 2, d)), torch.bfloat16)
+        args.append((q, pages, table, _torch(np.array([700, 64, 1], np.int32)), _torch(ks), _torch(vs)))
+        want.append(apa.attention_cache(*args[-1]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(apa.attention_cache(*args[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+    apa.check_error()
