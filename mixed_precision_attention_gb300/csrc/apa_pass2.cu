@@ -45,7 +45,6 @@
 // 1's, in that order.  The per-row work is
 // the same as the one-group kernel's; only the tile-to-accumulator assignment
 // (and so the rounding order of the merge) differs.
-#include <atomic>
 #include <cstring>
 #include <cuda_fp16.h>
 
@@ -78,43 +77,6 @@ struct P2Params {
   float* part_o;              // [BH*nblk*nsplit][128][d]
   float2* part_ml;            // [BH*nblk*nsplit][128]
   float* part_qmu;            // [BH*nblk][128], APA mode only
-  // the sliding-window form: see WindowTiles
-  int window, sinks;
-  uint16_t* out16;            // [B,Hq,Nq,d] bf16
-};
-
-// The sliding-window form of pass2_kernel (template parameter W; apa_attention_window):
-// row position x (x = pos + off) sees the keys j <= x with j > x - window or j < sinks.
-// A block walks the tiles that hold sinks, then those its rows' windows reach, every
-// row group taking part; P and V go to the product in BF16, V straight from the
-// caller's array, so there is no copy of V and no workspace; out is bf16.  Walks are
-// short, so what a CTA does before its first and after its last product counts: at
-// d <= 128 two CTAs share an SM (256 TMEM columns each) and cover each other's.  On
-// 8192 rows with a window of 1024 the two-group kernel, one CTA per SM, took 180 us,
-// this one 133; on 16384 rows with a window of 4096, 797 and 670 us (1235 TFLOP/s, 0.65
-// of the measured BF16 rate; the matrix pipe and the softmax threads share what is left).
-struct WindowTiles {
-  int n_sink, t_lo, n;  // entries 0 .. n_sink-1: tiles 0 ..; then tiles t_lo ..
-  __device__ __forceinline__ WindowTiles(const P2Params& p, int p0, int t_hi) {
-    const int first = p0 / p.s.G() + p.s.off();  // position of the block's first row
-    t_lo = max(0, first - p.window + 1) / kTile;
-    n_sink = min((int)(((long long)p.sinks + kTile - 1) / kTile), t_lo);
-    n = n_sink + t_hi - t_lo + 1;
-  }
-  __device__ __forceinline__ int tile(int i) const { return i < n_sink ? i : t_lo + i - n_sink; }
-};
-// The keys of tile j0 .. j0+63 that a row at position x sees: indices 0 .. nvis-1 but
-// for gap_lo .. gap_hi-1.  nvis = 0 if there is none.
-struct RowKeys {
-  int nvis, gap_lo, gap_hi;
-  __device__ __forceinline__ RowKeys(const P2Params& p, int x, int j0, bool valid) {
-    nvis = valid ? min(kTile, x + 1 - j0) : 0;
-    gap_hi = min(kTile, x - p.window + 1 - j0);  // first key of the window
-    gap_lo = max(0, min(kTile, p.sinks - j0));   // first key that is no sink
-    if (gap_lo == 0 && gap_hi >= nvis) nvis = 0;
-  }
-  __device__ __forceinline__ bool all() const { return nvis == kTile && gap_lo >= gap_hi; }
-  __device__ __forceinline__ bool sees(int i) const { return i < nvis && (i < gap_lo || i >= gap_hi); }
 };
 
 constexpr int kThreads = 224;
@@ -131,26 +93,18 @@ constexpr float kTau2 = 8.0f;  // pass-2 lazy rescale threshold (log2 units)
 // 122880 layer, two CTAs of that shape were no faster than one CTA with 3 stages.
 // P goes from the softmax threads into TMEM, over the S slot it came from, and the
 // PV product reads it there.
-template <int D, bool W = false>
+template <int D>
 struct P2Cfg {
-  static constexpr int kCtasPerSm = W && D <= 128 ? 2 : 1;
-  // K and V of a tile share a stage, or (kSplit) have rings of their own, so that the next
-  // tiles' K need not wait for a P.V product (16384 rows, window 4096: 885 us with two
-  // shared stages, 710 with rings of 3 and 2, 670 with 2 and 3)
-  static constexpr bool kSplit = kCtasPerSm == 2;
-  static constexpr int NS = kSplit ? (D == 128 ? 2 : 3) : (D >= 256 ? 2 : (D == 128 ? APA_P2_STAGES_D128 : 3));  // of K
-  static constexpr int NSV = kSplit ? 3 : NS;                                                 // of V
+  static constexpr int kCtasPerSm = 1;
+  static constexpr int NS = kCtasPerSm == 2 ? 2 : (D >= 256 ? 2 : (D == 128 ? APA_P2_STAGES_D128 : 3));
   static constexpr int kAtoms = D / 64;
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kKVBytes = 64 * D * 2;  // one of K or V per stage
   static constexpr int kQOff = 0;
   static constexpr int kStageOff = kQBytes;
-  static constexpr int kStep = kSplit ? kKVBytes : 2 * kKVBytes;  // from a stage to the next
-  static constexpr int kVOff = kStageOff + (kSplit ? NS : 1) * kKVBytes;
-  static constexpr int kB0 = kSplit ? 2 * (NS + NSV) : 2 * NS;  // barriers of the stages
-  static constexpr int kNumBars = kB0 + 10;
-  static constexpr int kBarOff = kStageOff + (NS + NSV) * kKVBytes;
-  static constexpr int kSlack = kCtasPerSm == 2 && D == 128 ? 0 : 1024;  // runtime alignment room (none left for two CTAs)
+  static constexpr int kNumBars = 2 * NS + 10;
+  static constexpr int kBarOff = kStageOff + NS * 2 * kKVBytes;
+  static constexpr int kSlack = kCtasPerSm == 2 ? 0 : 1024;  // runtime alignment room
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + kSlack;
   static constexpr uint32_t kTmemCols = D + 128 <= 256 ? 256 : 512;
   static constexpr uint32_t kOCol = 0, kSCol = D;
@@ -168,80 +122,57 @@ __device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, int*
 }
 
 // P of eight consecutive keys, 2^(x*c2 + nb), as four FP16x2 words (key 2k in the
-// low half of word k; BF16x2 in the sliding-window form); the FP32 values are added
-// into (s0, s1): even keys into s0, odd keys into s1.  The affine step and the sums
-// run as packed FP32 pairs.
-template <bool W>
-__device__ __forceinline__ void p8(const float* x, float c2, float nb, uint32_t* h, float& s0, float& s1) {
-#define APA_P8(CVT)                                                                                                  \
-  asm("{\n.reg .b64 a0, a1, a2, a3, c, n, s, one;\n"                                                                 \
-      ".reg .f32 y0, y1, y2, y3, y4, y5, y6, y7;\n"                                                                  \
-      "mov.b64 c, {%14, %14};\n"                                                                                     \
-      "mov.b64 n, {%15, %15};\n"                                                                                     \
-      "mov.b64 one, {%16, %16};\n"                                                                                   \
-      "mov.b64 a0, {%6, %7};\n"                                                                                      \
-      "mov.b64 a1, {%8, %9};\n"                                                                                      \
-      "mov.b64 a2, {%10, %11};\n"                                                                                    \
-      "mov.b64 a3, {%12, %13};\n"                                                                                    \
-      "fma.rn.f32x2 a0, a0, c, n;\n"                                                                                 \
-      "fma.rn.f32x2 a1, a1, c, n;\n"                                                                                 \
-      "fma.rn.f32x2 a2, a2, c, n;\n"                                                                                 \
-      "fma.rn.f32x2 a3, a3, c, n;\n"                                                                                 \
-      "mov.b64 {y0, y1}, a0;\n"                                                                                      \
-      "mov.b64 {y2, y3}, a1;\n"                                                                                      \
-      "mov.b64 {y4, y5}, a2;\n"                                                                                      \
-      "mov.b64 {y6, y7}, a3;\n"                                                                                      \
-      "ex2.approx.ftz.f32 y0, y0;\n"                                                                                 \
-      "ex2.approx.ftz.f32 y1, y1;\n"                                                                                 \
-      "ex2.approx.ftz.f32 y2, y2;\n"                                                                                 \
-      "ex2.approx.ftz.f32 y3, y3;\n"                                                                                 \
-      "ex2.approx.ftz.f32 y4, y4;\n"                                                                                 \
-      "ex2.approx.ftz.f32 y5, y5;\n"                                                                                 \
-      "ex2.approx.ftz.f32 y6, y6;\n"                                                                                 \
-      "ex2.approx.ftz.f32 y7, y7;\n"                                                                                 \
-      CVT " %0, y1, y0;\n"                                                                                           \
-      CVT " %1, y3, y2;\n"                                                                                           \
-      CVT " %2, y5, y4;\n"                                                                                           \
-      CVT " %3, y7, y6;\n"                                                                                           \
-      "mov.b64 s, {%4, %5};\n"                                                                                       \
-      "mov.b64 a0, {y0, y1};\n"                                                                                      \
-      "mov.b64 a1, {y2, y3};\n"                                                                                      \
-      "mov.b64 a2, {y4, y5};\n"                                                                                      \
-      "mov.b64 a3, {y6, y7};\n"                                                                                      \
-      "fma.rn.f32x2 s, a0, one, s;\n"                                                                                \
-      "fma.rn.f32x2 s, a1, one, s;\n"                                                                                \
-      "fma.rn.f32x2 s, a2, one, s;\n"                                                                                \
-      "fma.rn.f32x2 s, a3, one, s;\n"                                                                                \
-      "mov.b64 {%4, %5}, s;\n}"                                                                                      \
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]), "+f"(s0), "+f"(s1)                                           \
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(c2), "f"(nb),    \
-        "f"(1.f))
-  if constexpr (W)
-    APA_P8("cvt.rn.bf16x2.f32");
-  else
-    APA_P8("cvt.rn.f16x2.f32");
-#undef APA_P8
+// low half of word k); the FP32 values are added into (s0, s1): even keys into s0,
+// odd keys into s1.  The affine step and the sums run as packed FP32 pairs.
+__device__ __forceinline__ void p8_f16(const float* x, float c2, float nb, uint32_t* h, float& s0, float& s1) {
+  asm("{\n.reg .b64 a0, a1, a2, a3, c, n, s, one;\n"
+      ".reg .f32 y0, y1, y2, y3, y4, y5, y6, y7;\n"
+      "mov.b64 c, {%14, %14};\n"
+      "mov.b64 n, {%15, %15};\n"
+      "mov.b64 one, {%16, %16};\n"
+      "mov.b64 a0, {%6, %7};\n"
+      "mov.b64 a1, {%8, %9};\n"
+      "mov.b64 a2, {%10, %11};\n"
+      "mov.b64 a3, {%12, %13};\n"
+      "fma.rn.f32x2 a0, a0, c, n;\n"
+      "fma.rn.f32x2 a1, a1, c, n;\n"
+      "fma.rn.f32x2 a2, a2, c, n;\n"
+      "fma.rn.f32x2 a3, a3, c, n;\n"
+      "mov.b64 {y0, y1}, a0;\n"
+      "mov.b64 {y2, y3}, a1;\n"
+      "mov.b64 {y4, y5}, a2;\n"
+      "mov.b64 {y6, y7}, a3;\n"
+      "ex2.approx.ftz.f32 y0, y0;\n"
+      "ex2.approx.ftz.f32 y1, y1;\n"
+      "ex2.approx.ftz.f32 y2, y2;\n"
+      "ex2.approx.ftz.f32 y3, y3;\n"
+      "ex2.approx.ftz.f32 y4, y4;\n"
+      "ex2.approx.ftz.f32 y5, y5;\n"
+      "ex2.approx.ftz.f32 y6, y6;\n"
+      "ex2.approx.ftz.f32 y7, y7;\n"
+      "cvt.rn.f16x2.f32 %0, y1, y0;\n"
+      "cvt.rn.f16x2.f32 %1, y3, y2;\n"
+      "cvt.rn.f16x2.f32 %2, y5, y4;\n"
+      "cvt.rn.f16x2.f32 %3, y7, y6;\n"
+      "mov.b64 s, {%4, %5};\n"
+      "mov.b64 a0, {y0, y1};\n"
+      "mov.b64 a1, {y2, y3};\n"
+      "mov.b64 a2, {y4, y5};\n"
+      "mov.b64 a3, {y6, y7};\n"
+      "fma.rn.f32x2 s, a0, one, s;\n"
+      "fma.rn.f32x2 s, a1, one, s;\n"
+      "fma.rn.f32x2 s, a2, one, s;\n"
+      "fma.rn.f32x2 s, a3, one, s;\n"
+      "mov.b64 {%4, %5}, s;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]), "+f"(s0), "+f"(s1)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(c2), "f"(nb),
+        "f"(1.f));
 }
 
-// 32 FP32 values of a row -> bf16, 64 bytes.
-__device__ __forceinline__ void store_bf16x32(uint16_t* dst, const uint32_t* o) {
-#pragma unroll
-  for (int j = 0; j < 32; j += 8) {
-    uint4 w;
-    uint32_t* r = &w.x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-          : "=r"(r[e])
-          : "f"(__uint_as_float(o[j + 2 * e + 1])), "f"(__uint_as_float(o[j + 2 * e])));
-    *reinterpret_cast<uint4*>(dst + j) = w;
-  }
-}
-
-template <int D, bool W = false>
-__global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
+template <int D>
+__global__ void __launch_bounds__(kThreads, P2Cfg<D>::kCtasPerSm)
     pass2_kernel(const P2Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using C = P2Cfg<D, W>;
+  using C = P2Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (C::kSlack == 0 && smem != smem_raw) {  // no room to realign: refuse loudly
@@ -273,19 +204,14 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
 
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = smem_u32(bars);
-  // tile i's K and V: their stages' barriers (shared by both unless kSplit) and wait parities
-  auto k_full = [&](int i) { return bar0 + 8u * (i % C::NS); };
-  auto k_empty = [&](int i) { return bar0 + 8u * (C::NS + i % C::NS); };
-  auto v_full = [&](int i) { return C::kSplit ? bar0 + 8u * (2 * C::NS + i % C::NSV) : bar0 + 8u * (i % C::NS); };
-  auto v_empty = [&](int i) {
-    return C::kSplit ? bar0 + 8u * (2 * C::NS + C::NSV + i % C::NSV) : bar0 + 8u * (C::NS + i % C::NS);
-  };
-  auto s_full = [&](int b2) { return bar0 + 8u * (C::kB0 + b2); };
-  // (slots kB0 + 2, 3 are unused: an S slot is free once the P.V that reads the P
+  auto kv_full = [&](int st) { return bar0 + 8u * st; };
+  auto kv_empty = [&](int st) { return bar0 + 8u * (C::NS + st); };
+  auto s_full = [&](int b2) { return bar0 + 8u * (2 * C::NS + b2); };
+  // (slots 2 NS + 2, 3 are unused: an S slot is free once the P.V that reads the P
   // written over it has completed, so pv_done tells the S issuer)
-  auto p_full = [&](int b2) { return bar0 + 8u * (C::kB0 + 4 + b2); };
-  auto pv_done = [&](int b2) { return bar0 + 8u * (C::kB0 + 6 + b2); };
-  const uint32_t drain = bar0 + 8u * (C::kB0 + 8), drain_pv = bar0 + 8u * (C::kB0 + 9);
+  auto p_full = [&](int b2) { return bar0 + 8u * (2 * C::NS + 4 + b2); };
+  auto pv_done = [&](int b2) { return bar0 + 8u * (2 * C::NS + 6 + b2); };
+  const uint32_t drain = bar0 + 8u * (2 * C::NS + 8), drain_pv = bar0 + 8u * (2 * C::NS + 9);
   // every lane of a softmax warp waits; the warp proceeds only if all lanes succeeded
   auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;  // already complete
@@ -297,8 +223,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
   const bool apa_mode = p.hot_list != nullptr;
   const int last_row = min(R, p0 + kBlockRows) - 1;
   const int t_hi = s.causal ? min(T - 1, (last_row / G + off) / kTile) : T - 1;
-  const WindowTiles wt(p, p0, t_hi);  // (used in the sliding-window form only)
-  const int n_all = W ? wt.n : apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
+  const int n_all = apa_mode ? (int)p.hot_count[(size_t)bh * nblk + blk] : t_hi + 1;
   const int i0 = p.nsplit > 1 ? (int)((long long)n_all * part / p.nsplit) : 0;
   const int n = p.nsplit > 1 ? (int)((long long)n_all * (part + 1) / p.nsplit) - i0 : n_all;
   const uint32_t* list = apa_mode ? p.hot_list + ((size_t)bh * nblk + blk) * T : nullptr;
@@ -309,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
       return (int)(e & 0xFFFFu);
     }
     gmask = 0xFFu;
-    if constexpr (W) return wt.tile(i0 + i);
     const int g = i0 + i;
     return g == 0 ? 0 : t_hi + 1 - g;
   };
@@ -317,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < C::kNumBars; ++i) {
-      const bool per_warp = (i >= C::kB0 + 4 && i < C::kB0 + 6);         // p_full: one arrive per softmax warp
-      const bool kv_empty_bar = !C::kSplit && i >= C::NS && i < 2 * C::NS;  // empty: the S and the PV issuer
+      const bool per_warp = (i >= 2 * C::NS + 4 && i < 2 * C::NS + 6);  // p_full: one arrive per softmax warp
+      const bool kv_empty_bar = (i >= C::NS && i < 2 * C::NS);           // kv_empty: the S and the PV issuer
       mbar_init(bar0 + 8u * i, per_warp ? 4u : (kv_empty_bar ? 2u : 1u));
     }
     fence_mbar_init();
@@ -366,9 +290,10 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
   if (warp == 4) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int issued = 0, issued_v = 0;  // (issued_v: with rings of their own)
+      int issued = 0;
       for (int i = 0; i < n; ++i) {
-        if (i >= C::NS && !mbar_wait(k_empty(i), ((i / C::NS) - 1) & 1, &abort_flag, p.err)) break;
+        const int st = i % C::NS;
+        if (i >= C::NS && !mbar_wait(kv_empty(st), ((i / C::NS) - 1) & 1, &abort_flag, p.err)) break;
         uint32_t gm;
         const int t = tile_of(i, gm);
         // contiguous maps: (channel, key, b * Hkv + h); paged maps: (channel, key in
@@ -379,38 +304,26 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
           ky = 0;
           kz = kv_page(s, b, t, p.err) * s.Hkv + h;
         }
-        mbar_arrive_expect_tx(k_full(i), C::kSplit ? C::kKVBytes : 2 * C::kKVBytes);
-        const uint32_t kdst = sbase + C::kStageOff + (i % C::NS) * C::kStep;
-        const uint32_t vdst = sbase + C::kVOff + (i % C::NSV) * C::kStep;
-        if constexpr (C::kSplit) {
+        mbar_arrive_expect_tx(kv_full(st), 2 * C::kKVBytes);
+        const uint32_t kdst = sbase + C::kStageOff + st * 2 * C::kKVBytes;
 #pragma unroll
-          for (int a = 0; a < C::kAtoms; ++a) tma_load_3d(kdst + a * 8192, &kmap, a * 64, ky, kz, k_full(i));
-          issued = i + 1;
-          if (i >= C::NSV && !mbar_wait(v_empty(i), ((i / C::NSV) - 1) & 1, &abort_flag, p.err)) break;
-          mbar_arrive_expect_tx(v_full(i), C::kKVBytes);
-#pragma unroll
-          for (int a = 0; a < C::kAtoms; ++a) tma_load_3d(vdst + a * 8192, &vmap, a * 64, vy, vz, v_full(i));
-          issued_v = i + 1;
-        } else {
-#pragma unroll
-          for (int a = 0; a < C::kAtoms; ++a) {
-            tma_load_3d(kdst + a * 8192, &kmap, a * 64, ky, kz, k_full(i));
-            tma_load_3d(vdst + a * 8192, &vmap, a * 64, vy, vz, k_full(i));
-          }
-          issued = i + 1;
+        for (int a = 0; a < C::kAtoms; ++a) {
+          tma_load_3d(kdst + a * 8192, &kmap, a * 64, ky, kz, kv_full(st));
+          tma_load_3d(kdst + C::kKVBytes + a * 8192, &vmap, a * 64, vy, vz, kv_full(st));
         }
+        issued = i + 1;
       }
       // every copy issued lands before the CTA exits, also when another warp gave up
       // after this loop ended (normally they have all landed: the waits return at once)
-      for (int i = max(0, issued - C::NS); i < issued; ++i) wait_bounded(k_full(i), (i / C::NS) & 1, p.err);
-      for (int i = max(0, issued_v - C::NSV); i < issued_v; ++i) wait_bounded(v_full(i), (i / C::NSV) & 1, p.err);
+      for (int i = max(0, issued - C::NS); i < issued; ++i) wait_bounded(kv_full(i % C::NS), (i / C::NS) & 1, p.err);
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ S issuer
     if (lane == 0 && n > 0) {
       const uint32_t idS = idesc_bf16(128, 64, 0);
       auto issue_s = [&](int i) -> bool {
-        if (!mbar_wait(k_full(i), (i / C::NS) & 1, &abort_flag, p.err)) return false;
+        const int st = i % C::NS;
+        if (!mbar_wait(kv_full(st), (i / C::NS) & 1, &abort_flag, p.err)) return false;
         uint32_t gm_unused;
         if (s.pages && (s.Nkv % kTile) != 0 && tile_of(i, gm_unused) == T - 1) {
           // paged pool: the keys past Nkv in a sequence's last page hold whatever the
@@ -418,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
           // keep those out of an MMA, so the K rows are zeroed here, before any MMA
           // reads this stage (V comes from the contiguous FP16 copy).
           const int nk = s.Nkv - (T - 1) * kTile, rows = kTile - nk;
-          uint8_t* kst = smem + C::kStageOff + (i % C::NS) * C::kStep;
+          uint8_t* kst = smem + C::kStageOff + st * 2 * C::kKVBytes;
           for (int x = 0; x < rows * C::kAtoms * 8; ++x) {
             const int rest = x >> 3, rr = nk + rest % rows, atom = rest / rows;
             *reinterpret_cast<uint4*>(kst + atom * 8192 + rr * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -428,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
         // the slot holds P of entry i - 2 until its P.V has read it
         if (i >= 2 && !mbar_wait(pv_done(i & 1), ((i >> 1) - 1) & 1, &abort_flag, p.err)) return false;
         tc_fence_after();
-        const uint32_t kaddr = sbase + C::kStageOff + (i % C::NS) * C::kStep;
+        const uint32_t kaddr = sbase + C::kStageOff + st * 2 * C::kKVBytes;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t ad = smem_desc(sbase + C::kQOff + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, kSwizzle128B);
@@ -436,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
           mma_bf16(tmem + C::kSCol + 64 * (i & 1), ad, bd, idS, kk > 0);
         }
         mma_commit(s_full(i & 1));
-        mma_commit(k_empty(i));  // this stage's K has been read
+        mma_commit(kv_empty(st));  // this stage's K has been read
         return true;
       };
       for (int i = 0; i < n; ++i)
@@ -448,13 +361,13 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
   } else if (warp == 6) {
     // ------------------------------------------------------------ PV issuer
     if (lane == 0 && n > 0) {
-      const uint32_t idO = W ? idesc_bf16(128, D, 1) : idesc_f16(128, D, 1);
+      const uint32_t idO = idesc_f16(128, D, 1);
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         if (!(ok = mbar_wait(p_full(i & 1), (i >> 1) & 1, &abort_flag, p.err))) break;
-        if (!(ok = mbar_wait(v_full(i), (i / C::NSV) & 1, &abort_flag, p.err))) break;
+        if (!(ok = mbar_wait(kv_full(i % C::NS), (i / C::NS) & 1, &abort_flag, p.err))) break;
         tc_fence_after();
-        const uint32_t vaddr = sbase + C::kVOff + (i % C::NSV) * C::kStep;
+        const uint32_t vaddr = sbase + C::kStageOff + (i % C::NS) * 2 * C::kKVBytes + C::kKVBytes;
         // P (FP16) sits in the first 32 columns of its S slot: 16 keys per MMA
         const uint32_t pcol = tmem + C::kSCol + 64u * (i & 1);
 #pragma unroll
@@ -463,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
           mma_f16_ts(tmem + C::kOCol, pcol + 8u * kk, bd, idO, (i > 0 || kk > 0) ? 1u : 0u);
         }
         mma_commit(pv_done(i & 1));
-        mma_commit(v_empty(i));  // this stage's V has been read
+        mma_commit(kv_empty(i % C::NS));  // this stage's V has been read
       }
       mma_commit(drain_pv);
       wait_bounded(drain_pv, 0, p.err);
@@ -486,9 +399,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
       if (!(ok = warp_wait(s_full(i & 1), (i >> 1) & 1))) break;
       const bool row_hot = row_valid && ((gm >> (r >> 4)) & 1u);
       const int j0 = t * kTile;
-      const RowKeys rk(p, vis_last, j0, row_hot);  // (used in the sliding-window form only)
-      // keys j0 .. j0+nvis-1 visible (but for the gap behind the sinks)
-      const int nvis = W ? rk.nvis : row_hot ? min(kTile, vis_last + 1 - j0) : 0;
+      const int nvis = row_hot ? min(kTile, vis_last + 1 - j0) : 0;  // keys j0 .. j0+nvis-1 visible
       // P (FP16, two keys per column) goes over the first 32 columns of the S slot it
       // came from; the slot's previous P had been read before S was written into it
       const uint32_t pslot = tmem + lane_base + C::kSCol + 64u * (i & 1);
@@ -517,10 +428,10 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
       float sv[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) sv[j] = __uint_as_float(raw[j]);
-      if (__any_sync(0xffffffffu, nvis > 0 && (W ? !rk.all() : nvis < 64))) {
+      if (__any_sync(0xffffffffu, nvis > 0 && nvis < 64)) {
 #pragma unroll
         for (int j = 0; j < 64; ++j)
-          if (W ? !rk.sees(j) : j >= nvis) sv[j] = -INFINITY;
+          if (j >= nvis) sv[j] = -INFINITY;
       }
       // row maximum as a tree of 3-input maxima; the logit map x*c2 - shift is monotone
       // (c2 > 0), so its maximum is the map of the raw maximum, rounded the same way
@@ -552,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
           const int ch = 4 * hf + c4;
-          p8<W>(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
+          p8_f16(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
         }
         tmem_st_x16(pslot + 16u * hf, pk);
       }
@@ -642,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
       const float w1 = e1 == -INFINITY ? 0.f : exp2f(e1 - M), w2 = e2 == -INFINITY ? 0.f : exp2f(e2 - M);
       const float L = w1 * l1 + w2 * l2;
       const float invL = 1.f / L;
-      const float w2o = W ? w2 : w2 * v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
-      float* orow = W ? nullptr : p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
+      const float w2o = w2 * v16_scale(__uint_as_float(p.vamax[bh]));  // O carries V / scale
+      float* orow = p.out + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t o[32];
@@ -654,13 +565,7 @@ __global__ void __launch_bounds__(kThreads, (P2Cfg<D, W>::kCtasPerSm))
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
-        if constexpr (W) {
-          if (row_valid) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * (w2o * invL));
-            store_bf16x32(p.out16 + (((size_t)b * s.Hq + hq) * s.Nq + pos) * D + c0, o);
-          }
-        } else if (row_valid) {
+        if (row_valid) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             float4 res;
@@ -1037,7 +942,7 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
           const int ch = 4 * hf + c4;
-          p8<false>(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
+          p8_f16(sv + 8 * ch, c2, nb, pk + 4 * c4, ps[ch & 1], ps[2 + (ch & 1)]);
         }
         tmem_st_x16(pslot + 16u * hf, pk);
       }
@@ -1138,6 +1043,8 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
   }
 }
 
+}  // namespace
+
 // paged: the pool [num_pages][Hkv][64][d] as (channel, key in page, page * Hkv + h)
 bool make_kv_map(CUtensorMap* map, const void* base, const Shape& s, CUtensorMapDataType dtype, bool paged) {
   using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1162,6 +1069,8 @@ bool make_kv_map(CUtensorMap* map, const void* base, const Shape& s, CUtensorMap
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // Two softmax groups per block at d <= 128; at d = 256 their two O accumulators
 // would take all 512 TMEM columns, so one group.
@@ -1207,23 +1116,6 @@ __global__ void __launch_bounds__(D) combine_kernel(const P2Params p) {
 }
 
 template <int D>
-cudaError_t launch_window_d(const P2Params& prm, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
-  const int grid = prm.s.BH() * prm.s.nblk();
-  cudaError_t e;
-  const int smem = P2Cfg<D, true>::kSmem;
-  static std::atomic<uint64_t> ready{0};  // once per device (a bit each)
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev))) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev > 63 || !(ready.load() & bit)) {
-    if ((e = cudaFuncSetAttribute(pass2_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
-    if (dev <= 63) ready.fetch_or(bit);
-  }
-  pass2_kernel<D, true><<<grid, kThreads, smem, st>>>(prm, km, vm);
-  return cudaGetLastError();
-}
-
-template <int D>
 cudaError_t launch_d(const P2Params& prm, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   const int grid = prm.s.BH() * prm.s.nblk();
   cudaError_t e;
@@ -1266,29 +1158,6 @@ cudaError_t launch_pass2_order(const Shape& s, const Workspace& ws, cudaStream_t
   if (n > (size_t)kMaxRanked) return cudaSuccess;  // pass 2 keeps the position order
   rank_kernel<<<1, 1024, 0, st>>>(ws.hot_count, (int)n, ws.p2_order);
   return cudaGetLastError();
-}
-
-cudaError_t launch_window(const Shape& s, const void* q, const void* k, const void* v, int window, int sinks, void* out,
-                          float* lse, cudaStream_t st) {
-  CUtensorMap km, vm;
-  if (!make_kv_map(&km, k, s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false) ||
-      !make_kv_map(&vm, v, s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false))
-    return cudaErrorInvalidValue;
-  P2Params prm{};
-  prm.s = s;
-  prm.q = (const uint16_t*)q;
-  prm.lse = lse;
-  prm.err = device_error_word();
-  prm.nsplit = 1;
-  prm.window = window;
-  prm.sinks = sinks;
-  prm.out16 = (uint16_t*)out;
-  switch (s.d) {
-    case 64: return launch_window_d<64>(prm, km, vm, st);
-    case 128: return launch_window_d<128>(prm, km, vm, st);
-    case 256: return launch_window_d<256>(prm, km, vm, st);
-  }
-  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_pass2(const Shape& s, const void* q, const void* k, const void* v, const Workspace* ws, float* out,

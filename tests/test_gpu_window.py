@@ -103,3 +103,36 @@ def test_window_on_a_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d,B,Hq,H,Nq,N,window,sinks", [
+    (64, 1, 24, 8, 5001, 5001, 70, 3), (128, 2, 24, 8, 2500, 6000, 333, 130), (256, 1, 16, 4, 3333, 3333, 64, 0),
+    (128, 1, 8, 8, 40000, 40000, 1, 1)])
+def test_more_row_blocks_than_ctas(d, B, Hq, H, Nq, N, window, sinks):
+    # each CTA takes several row blocks in turn; against 64-bit attention over each row's own keys
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    g = torch.Generator(device="cuda").manual_seed(d + Nq)
+    q = (2 * torch.randn(B, Hq, Nq, d, device="cuda", generator=g)).bfloat16()
+    k, v = (torch.randn(B, H, N, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    out, lse = apa.attention_window(q, k, v, window, sinks=sinks)
+    apa.check_error()
+    at = torch.arange(N - Nq, N, device="cuda")
+    for b in range(B):
+        for h in range(0, Hq, 5):
+            for r in range(0, Nq, 2048):
+                p = at[r:r + 2048, None]
+                j = torch.cat([torch.arange(sinks, device="cuda").expand(len(p), -1),
+                               p - window + 1 + torch.arange(window, device="cuda")], 1)
+                see = torch.cat([j[:, :sinks] <= p - window, j[:, sinks:] >= 0], 1)
+                j = j.clamp(0, N - 1)
+                kj, vj = k[b, h * H // Hq].double()[j], v[b, h * H // Hq].double()[j]
+                s = torch.einsum("rd,rjd->rj", q[b, h, r:r + 2048].double(), kj) / math.sqrt(d)
+                s = s.masked_fill(~see, -math.inf)
+                w = torch.softmax(s, 1)
+                ref, mag = torch.einsum("rj,rjd->rd", w, vj), torch.einsum("rj,rjd->rd", w, vj.abs())
+                err = (out[b, h, r:r + 2048].double() - ref).abs()
+                assert (err <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -14) * mag).all()
+                rl = torch.logsumexp(s, 1)
+                assert ((lse[b, h, r:r + 2048].double() - rl).abs() <= 1e-5 * rl.abs().clamp_min(1)).all()
