@@ -11,11 +11,15 @@
 // turn, the longest walks first.  7 warps:
 //   warps 0-3  softmax, one thread per row (TMEM lane = row), and the epilogue;
 //   warp 4     TMA producer: K and V tiles (64 keys x d, 128-byte swizzle), a ring each;
-//   warp 5     TMEM owner and S issuer: S = Q K^T (kind::f16), two S slots;
-//   warp 6     PV issuer: O += P V, P read from TMEM over the first half of its S slot.
+//   warp 5     TMEM owner and S issuer: S = Q K^T (kind::f16);
+//   warp 6     PV issuer: O += P V, P read from TMEM.
+// TMEM: O, one S and two P.  S is free again as soon as the softmax threads hold its
+// scores in registers, so the next tile's is computed while they work on this one, and
+// P.V of a tile has a tile's time.  (Two S with P over them, so that S waits for a P.V,
+// takes the same columns: 8192 rows 117 us, 16384 rows 650 us, against XX and YY.)
 // Everything runs on over the end of an item: the producer is already loading the next
 // item's tiles; the softmax threads store the next Q as soon as the last S is done and
-// before they wait for the last P.V, so the next item's first two S are computed under
+// before they wait for the last P.V, so the next item's first S is computed under
 // the epilogue; the first P.V of an item waits until the epilogue has read O.
 // P goes to the product in BF16 (2^-8 relative, the rounding of the output) against V
 // itself, so there is no copy of V and no workspace; l adds the FP32 values.  The
@@ -57,7 +61,7 @@ struct WinCfg {
   static constexpr int kSlack = D == 128 ? 0 : 1024;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + kSlack;
   static constexpr uint32_t kTmemCols = D + 128 <= 256 ? 256 : 512;
-  static constexpr uint32_t kOCol = 0, kSCol = D;
+  static constexpr uint32_t kOCol = 0, kSCol = D, kPCol = D + 64;  // O, S, and P twice (32 columns each)
   static_assert(kCtasPerSm * (kSmem + 1024) <= 233472, "shared memory");
   static_assert(kCtasPerSm * kTmemCols <= 512, "TMEM");
 };
@@ -152,9 +156,9 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
   auto v_full = [&](int T) { return bar0 + 8u * (2 * C::NS + T % C::NSV); };
   auto v_empty = [&](int T) { return bar0 + 8u * (2 * C::NS + C::NSV + T % C::NSV); };
   constexpr int kB0 = 2 * C::NS + 2 * C::NSV;
-  auto s_full = [&](int T) { return bar0 + 8u * (kB0 + (T & 1)); };
-  auto p_full = [&](int T) { return bar0 + 8u * (kB0 + 2 + (T & 1)); };   // one arrive per softmax warp
-  auto pv_done = [&](int T) { return bar0 + 8u * (kB0 + 4 + (T & 1)); };  // also: the S slot is free
+  const uint32_t s_full = bar0 + 8u * kB0, s_free = bar0 + 8u * (kB0 + 1);  // s_free: one arrive per softmax warp
+  auto p_full = [&](int T) { return bar0 + 8u * (kB0 + 2 + (T & 1)); };     // one arrive per softmax warp
+  auto pv_done = [&](int T) { return bar0 + 8u * (kB0 + 4 + (T & 1)); };
   const uint32_t q_full = bar0 + 8u * (kB0 + 6), o_free = bar0 + 8u * (kB0 + 7);  // one arrive per softmax warp
   const uint32_t drain_s = bar0 + 8u * (kB0 + 8), drain_pv = bar0 + 8u * (kB0 + 9);
   // every lane of a softmax warp waits; the warp proceeds only if all lanes succeeded
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
     abort_flag = 0;
     for (int i = 0; i < C::kNumBars; ++i) {
       const int x = i - kB0;
-      mbar_init(bar0 + 8u * i, x == 2 || x == 3 || x == 6 || x == 7 ? 4u : 1u);
+      mbar_init(bar0 + 8u * i, x == 1 || x == 2 || x == 3 || x == 6 || x == 7 ? 4u : 1u);
     }
     fence_mbar_init();
   }
@@ -224,17 +228,17 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
         if (!(ok = mbar_wait(q_full, j & 1, &abort_flag, p.err))) break;
         for (int i = 0; i < n; ++i, ++T) {
           if (!(ok = mbar_wait(k_full(T), (T / C::NS) & 1, &abort_flag, p.err))) break;
-          // the slot holds P of tile T - 2 until its P.V has read it
-          if (T >= 2 && !(ok = mbar_wait(pv_done(T), ((T >> 1) - 1) & 1, &abort_flag, p.err))) break;
+          // the softmax threads have taken the scores of the tile before
+          if (T >= 1 && !(ok = mbar_wait(s_free, (T - 1) & 1, &abort_flag, p.err))) break;
           tc_fence_after();
           const uint32_t kaddr = sbase + C::kKOff + (T % C::NS) * C::kKVBytes;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t ad = smem_desc(sbase + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, kSwizzle128B);
             const uint64_t bd = smem_desc(kaddr + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, kSwizzle128B);
-            mma_bf16(tmem + C::kSCol + 64 * (T & 1), ad, bd, idS, kk > 0);
+            mma_bf16(tmem + C::kSCol, ad, bd, idS, kk > 0);
           }
-          mma_commit(s_full(T));
+          mma_commit(s_full);
           mma_commit(k_empty(T));  // this stage's K has been read
         }
       }
@@ -257,8 +261,7 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
           if (!(ok = mbar_wait(v_full(T), (T / C::NSV) & 1, &abort_flag, p.err))) break;
           tc_fence_after();
           const uint32_t vaddr = sbase + C::kVOff + (T % C::NSV) * C::kKVBytes;
-          // P (BF16) sits in the first 32 columns of its S slot: 16 keys per MMA
-          const uint32_t pcol = tmem + C::kSCol + 64u * (T & 1);
+          const uint32_t pcol = tmem + C::kPCol + 32u * (T & 1);  // P (BF16): 16 keys per MMA
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t bd = smem_desc(vaddr + kk * 2048, 8192, 1024, kSwizzle128B);
@@ -311,14 +314,18 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
       }
       float m2 = -INFINITY, l2 = 0.f;
       for (int i = 0; i < it.n; ++i, ++T) {
-        if (!(ok = warp_wait(s_full(T), (T >> 1) & 1))) break;
+        if (!(ok = warp_wait(s_full, T & 1))) break;
         const RowKeys rk(p, x, it.tile(i) * kTile, row >= 0);
-        // P (two keys per column) goes over the first 32 columns of the S slot it came
-        // from; the slot's previous P had been read before S was written into it
-        const uint32_t pslot = tmem + lane_base + C::kSCol + 64u * (T & 1);
+        const uint32_t pslot = tmem + lane_base + C::kPCol + 32u * (T & 1);  // P, two keys per column
         tc_fence_after();
         if (!__any_sync(0xffffffffu, rk.nvis > 0)) {
-          uint32_t z[16];  // no row of this warp takes part in this tile: its P rows are zero
+          // no row of this warp takes part in this tile: its P rows are zero
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+          if (T >= 2 && !(ok = warp_wait(pv_done(T), ((T >> 1) - 1) & 1))) break;
+          tc_fence_after();
+          uint32_t z[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) z[c] = 0u;
           tmem_st_x16(pslot, z);
@@ -330,9 +337,12 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
           continue;
         }
         uint32_t raw[64];
-        tmem_ld_x32(pslot, raw);
-        tmem_ld_x32(pslot + 32, raw + 32);
+        tmem_ld_x32(tmem + lane_base + C::kSCol, raw);
+        tmem_ld_x32(tmem + lane_base + C::kSCol + 32, raw + 32);
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
         float sv[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(raw[c]);
@@ -360,6 +370,9 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
           m2 = top;
         }
         const float nb = (rk.nvis <= 0 || m2 == -INFINITY) ? -INFINITY : -m2;
+        // the P.V of tile T - 2 has read what this P goes over
+        if (T >= 2 && !(ok = warp_wait(pv_done(T), ((T >> 1) - 1) & 1))) break;
+        tc_fence_after();
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
