@@ -21,7 +21,7 @@
 // Everything runs on over the end of an item: the producer is already loading the next
 // item's tiles; the softmax threads store the next Q as soon as the last S is done and
 // before they wait for the last P.V, so the next item's first S is computed under
-// the epilogue; the first P.V of an item waits until the epilogue has read O.
+// the epilogue; the first P.V of an item comes after it anyway, as its P does.
 // P goes to the product in BF16 (2^-8 relative, the rounding of the output) against V
 // itself, so there is no copy of V and no workspace; l adds the FP32 values.  The
 // running maximum moves only when a score exceeds it by 8 (log2 units).
@@ -56,7 +56,7 @@ struct WinCfg {
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kKVBytes = 64 * D * 2;  // one of K or V per stage
   static constexpr int kKOff = kQBytes, kVOff = kKOff + NS * kKVBytes;
-  static constexpr int kNumBars = 2 * NS + 2 * NSV + 10;
+  static constexpr int kNumBars = 2 * NS + 2 * NSV + 9;
   static constexpr int kBarOff = kVOff + NSV * kKVBytes;
   // two CTAs of d = 128 leave no room to align the window: it must start on 1024 bytes
   static constexpr int kSlack = D == 128 ? 0 : 1024;
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
   const uint32_t s_full = bar0 + 8u * kB0, s_free = bar0 + 8u * (kB0 + 1);  // s_free: one arrive per softmax warp
   auto p_full = [&](int T) { return bar0 + 8u * (kB0 + 2 + (T & 1)); };     // one arrive per softmax warp
   auto pv_done = [&](int T) { return bar0 + 8u * (kB0 + 4 + (T & 1)); };
-  const uint32_t q_full = bar0 + 8u * (kB0 + 6), o_free = bar0 + 8u * (kB0 + 7);  // one arrive per softmax warp
-  const uint32_t drain_s = bar0 + 8u * (kB0 + 8), drain_pv = bar0 + 8u * (kB0 + 9);
+  const uint32_t q_full = bar0 + 8u * (kB0 + 6);  // one arrive per softmax warp
+  const uint32_t drain_s = bar0 + 8u * (kB0 + 7), drain_pv = bar0 + 8u * (kB0 + 8);
   // every lane of a softmax warp waits; the warp proceeds only if all lanes succeeded
   auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;  // already complete
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
     abort_flag = 0;
     for (int i = 0; i < C::kNumBars; ++i) {
       const int x = i - kB0;
-      mbar_init(bar0 + 8u * i, x == 1 || x == 2 || x == 3 || x == 6 || x == 7 ? 4u : 1u);
+      mbar_init(bar0 + 8u * i, x == 1 || x == 2 || x == 3 || x == 6 ? 4u : 1u);
     }
     fence_mbar_init();
   }
@@ -251,12 +251,11 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
     // ------------------------------------------------------------ PV issuer
     if (lane == 0) {
       const uint32_t idO = idesc_bf16(128, D, 1);
-      int T = 0, j = 0;
+      int T = 0;
       bool ok = true;
-      for (int k = blockIdx.x; ok && k < items; k += gridDim.x, ++j) {
+      for (int k = blockIdx.x; ok && k < items; k += gridDim.x) {
         const int n = WinItem(p, k).n;
-        // the epilogue of the item before has read O
-        if (j > 0 && !(ok = mbar_wait(o_free, (j - 1) & 1, &abort_flag, p.err))) break;
+        // (the P of an item's first tile comes after the epilogue that read the last item's O)
         for (int i = 0; i < n; ++i, ++T) {
           if (!(ok = mbar_wait(p_full(T), (T >> 1) & 1, &abort_flag, p.err))) break;
           if (!(ok = mbar_wait(v_full(T), (T / C::NSV) & 1, &abort_flag, p.err))) break;
@@ -422,11 +421,6 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
         tmem_ld_x32(tmem + lane_base + C::kOCol + c0, o);
         tmem_ld_x32(tmem + lane_base + C::kOCol + c0 + 32, o + 32);
         tmem_wait_ld();
-        if (c0 + 64 == D) {  // O has been read: the next item's P.V may write it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_free);
-        }
         if (row0 >= 0) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * D + c0);
 #pragma unroll
