@@ -7,6 +7,7 @@
 
 #include "../../include/apa.h"
 #include "apa_internal.h"
+#include "apa_window.h"
 
 #ifndef APA_HOST_LANE_PRIORITY
 #define APA_HOST_LANE_PRIORITY 1  // later compute lanes of apa_attention_host at higher stream priority

@@ -191,11 +191,6 @@ cudaError_t launch_pass1(const Shape& s, const Workspace& ws, float eps, uint32_
                          cudaStream_t st, const KvSource* kv = nullptr, bool rowsum_mma = false);
 cudaError_t launch_pass2(const Shape& s, const void* q, const void* k, const void* v, const Workspace* ws,
                          float* out, float* lse, cudaStream_t st);
-// Tensor map of K or V for 64-channel x 64-key boxes with the 128-byte swizzle.
-bool make_kv_map(CUtensorMap* map, const void* base, const Shape& s, CUtensorMapDataType dtype, bool paged);
-// Exact causal attention with a sliding window and sinks (apa_attention_window).
-cudaError_t launch_window(const Shape& s, const void* q, const void* k, const void* v, int window, int sinks,
-                          void* out, float* lse, cudaStream_t st);
 // The all-exact path's FP16 copy of V (ws.v16, with the head maxima in ws.vamax):
 // V divided by v16_scale(max |v|) per head, the copy the quantizer writes in APA mode.
 cudaError_t launch_v16(const Shape& s, const void* v, const Workspace& ws, cudaStream_t st);

@@ -1043,8 +1043,6 @@ __global__ void __launch_bounds__(P2DualCfg<D>::kThreads, 1)
   }
 }
 
-}  // namespace
-
 // paged: the pool [num_pages][Hkv][64][d] as (channel, key in page, page * Hkv + h)
 bool make_kv_map(CUtensorMap* map, const void* base, const Shape& s, CUtensorMapDataType dtype, bool paged) {
   using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1069,8 +1067,6 @@ bool make_kv_map(CUtensorMap* map, const void* base, const Shape& s, CUtensorMap
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-namespace {
 
 // Two softmax groups per block at d <= 128; at d = 256 their two O accumulators
 // would take all 512 TMEM columns, so one group.

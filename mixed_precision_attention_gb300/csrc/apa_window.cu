@@ -28,6 +28,7 @@
 #include <atomic>
 
 #include "apa_internal.h"
+#include "apa_window.h"
 #include "tc.cuh"
 
 namespace apa {
@@ -448,6 +449,30 @@ __global__ void __launch_bounds__(kThreads, WinCfg<D>::kCtasPerSm)
   }
 }
 
+// Tensor map of a contiguous K or V [B*Hkv][Nkv][d] for boxes of 64 channels x 64 keys with the
+// 128-byte swizzle; keys past Nkv come as zeros.
+bool tile_map(CUtensorMap* map, const void* base, const Shape& s) {
+  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn encode = known.load();
+  if (!encode) {
+    cudaDriverEntryPointQueryResult found;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || !fn)
+      return false;
+    known.store(encode = reinterpret_cast<EncodeFn>(fn));
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)s.d, (cuuint64_t)s.Nkv, (cuuint64_t)s.BH()};
+  const cuuint64_t strides[2] = {(cuuint64_t)s.d * 2, (cuuint64_t)s.Nkv * s.d * 2};
+  const cuuint32_t box[3] = {64, 64, 1}, steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch_d(const WinParams& prm, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   using C = WinCfg<D>;
@@ -472,9 +497,7 @@ cudaError_t launch_d(const WinParams& prm, const CUtensorMap& km, const CUtensor
 cudaError_t launch_window(const Shape& s, const void* q, const void* k, const void* v, int window, int sinks, void* out,
                           float* lse, cudaStream_t st) {
   CUtensorMap km, vm;
-  if (!make_kv_map(&km, k, s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false) ||
-      !make_kv_map(&vm, v, s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, false))
-    return cudaErrorInvalidValue;
+  if (!tile_map(&km, k, s) || !tile_map(&vm, v, s)) return cudaErrorInvalidValue;
   const WinParams prm{s, (const uint16_t*)q, window, sinks, (uint16_t*)out, lse, device_error_word()};
   switch (s.d) {
     case 64: return launch_d<64>(prm, km, vm, st);
