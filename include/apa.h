@@ -49,7 +49,7 @@ extern "C" {
 #define APA_ERR_HEAD_DIM (-4)  /* d not in {64, 128, 256} */
 #define APA_ERR_CUDA (-5)      /* a CUDA call or launch failed; cudaGetLastError() holds the cause */
 #define APA_ERR_NOMEM (-6)     /* the workspace could not be allocated, or the given one is too small */
-#define APA_ERR_DEVICE (-7)    /* a kernel recorded a device-side error: a timeout, or a bad block-table entry (apa_check_error) */
+#define APA_ERR_DEVICE (-7)    /* a kernel recorded a device-side error: a timeout, or a page, slot or length in device memory that is out of range (apa_check_error) */
 #define APA_ERR_ALIGN (-8)     /* q, k or v not 16-byte aligned */
 #define APA_ERR_SCRATCH (-9)   /* too large for the fixed scratch of apa_quantize_noalloc */
 #define APA_ERR_FLAGS (-10)    /* an unknown bit in `flags` */
@@ -306,7 +306,8 @@ size_t apa_cache_page_bytes(int Hkv, int d); /* bytes of one page: Hkv * 72 * d 
  *              length out of range, APA_TABLES_TOKENS more tokens than max_tokens,
  *              APA_TABLES_PAGES too few free pages, APA_TABLES_FREE the stack's
  *              count out of range, or too many pages given back for its capacity
- * One launch, no workspace; the results do not depend on the launch's shape. */
+ * No workspace; the results do not depend on the launch's shape.  One launch for up
+ * to 8192 tokens; for more, a second one fills slots and positions. */
 #define APA_TABLES_LENGTH 1
 #define APA_TABLES_TOKENS 2
 #define APA_TABLES_PAGES 3
@@ -353,8 +354,9 @@ int apa_cache_read(const uint8_t* pages, int num_pages, int dtype, int Hkv, int 
  *   workspace  apa_attention_cache_workspace_bytes() bytes, 256-byte aligned, or null
  *            to have it allocated stream-ordered for the call.  Two calls that overlap
  *            on the GPU must not share one.
- * K, V and Q enter the products exactly (E2M1 * UE4M3 and a row of Q divided by a
- * power of two are FP16 values), with FP32 accumulation; the softmax weights are
+ * K, V and Q enter the products exactly (E2M1 * UE4M3 and a row of Q times a power of
+ * two are FP16 values, but for values of Q below 2^-31 of their row's largest, which are
+ * rounded at 2^-39 of it), with FP32 accumulation; the softmax weights are
  * rounded to FP16 for the product with V.  B <= 8192, B * max_pages < 2^29.  The work is
  * split over the GPU by the lengths alone, so reruns are bitwise equal. */
 int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,

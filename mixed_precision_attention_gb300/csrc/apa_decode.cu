@@ -13,7 +13,8 @@
 //   S^T = K Q^T: A = 16 keys x 16 channels of K, B = Q^T, 8 rows; O^T = V^T P^T: A = 16
 //   channels x 16 keys of V, B = P^T.  E2M1 * UE4M3 has 6 significant bits and lies in
 //   2^-10 .. 2688, so K and V are exact in FP16; a row of Q is scaled by a power of two
-//   into FP16's range.  P is rounded to FP16 (2^-11), lifted by 2^6 so that weights
+//   to 2^14 .. 2^16: its BF16 values are exact down to 2^-31 of the largest, those below
+//   are off by 2^-39 of it at most.  P is rounded to FP16 (2^-11), lifted by 2^6 so that weights
 //   down to 2^-30 of the row's largest keep a value; l sums the FP32 weights.
 //
 // Split: the units (32 keys of one KV head, one contiguous half page) of all sequences,
