@@ -32,6 +32,13 @@ _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+def _int(x):
+    """x as a C int that the entry points read as it is meant: ctypes would drop the upper bits of a larger one.  Window
+    and sinks beyond every position mean any such number; negative ones, and counts past 2^31, are refused there."""
+    x = int(x)
+    return x if -1 <= x <= 0x7FFFFFFF else 0x7FFFFFFF if x > 0 else -1
+
+
 def _enqueue(index, name, *args):
     """Calls an entry point with the current stream of device `index`, which is made current for it (the raw stream: a
     decoding step makes several of these calls, and a Stream object costs more than a launch)."""
@@ -109,8 +116,8 @@ def cache_tables(old_lens, new_lens, block_table, free_pages, free_count, max_to
     if new_lens.shape[0] != B or block_table.shape[0] != B or free_count.shape[0] != 1:
         raise ValueError("old_lens and new_lens must be [B], block_table [B, max_pages], free_count [1]")
     max_tokens = int(max_tokens)
-    if max_tokens < 0:
-        raise ValueError("max_tokens must not be negative")
+    if not 0 <= max_tokens <= 1 << 30:
+        raise ValueError("max_tokens must be in [0, 2^30]")
     if free_count_out is not None:
         _need("free_count_out", free_count_out, _i32, 1, index)
         if free_count_out.shape[0] != 1:
@@ -122,7 +129,7 @@ def cache_tables(old_lens, new_lens, block_table, free_pages, free_count, max_to
     status = _empty(1, dtype=_i32, device=dev)
     count = _empty(1, dtype=_i32, device=dev) if free_count_out is None else free_count_out
     _enqueue(index, "apa_cache_tables", old_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
-             block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), max_tokens,
+             _int(block_table.shape[1]), free_pages.data_ptr(), _int(free_pages.shape[0]), free_count.data_ptr(), max_tokens,
              slots.data_ptr(), positions.data_ptr(), starts.data_ptr(), count.data_ptr(), status.data_ptr())
     return {"slots": slots, "positions": positions, "starts": starts, "free_count": count, "status": status}
 
@@ -139,8 +146,8 @@ def cache_write(k, v, slots, pages, k_scale, v_scale):
     if _need_rows("v", v, 3) != index or v.shape != k.shape or v.dtype is not k.dtype:
         raise ValueError("k and v must be alike")
     _need("slots", slots, _i32, 1, index)
-    if slots.shape[0] != T:
-        raise ValueError("slots must be [T]")
+    if slots.shape[0] != T or T > 0x7FFFFFFF:
+        raise ValueError("slots must be [T], T < 2^31")
     num_pages, heads, dim = _need_pool(pages, k_scale, v_scale, index)
     if heads != Hkv or dim != d:
         raise ValueError("pages must be [num_pages, Hkv, 72 * d] with k's Hkv and d")
@@ -161,6 +168,8 @@ def cache_read(pages, slots, k_scale, v_scale, dtype=torch.bfloat16):
     if dtype not in _DTYPES:
         raise TypeError("dtype must be torch.bfloat16 or torch.float16")
     T, dev = slots.shape[0], pages.device
+    if T > 0x7FFFFFFF:
+        raise ValueError("slots must be [T], T < 2^31")
     k = _empty((Hkv, T, d), dtype=dtype, device=dev)
     v = _empty((Hkv, T, d), dtype=dtype, device=dev)
     _enqueue(index, "apa_cache_read", pages.data_ptr(), num_pages, _DTYPES[dtype], Hkv, T, d, slots.data_ptr(),
@@ -202,7 +211,7 @@ def attention_cache(q, pages, block_table, lens, k_scale, v_scale, window: int =
     lse = _empty((B, Hq, Nq), dtype=_f32, device=dev) if return_lse else None
     qb, qh, qr, _ = q.stride()
     _enqueue(index, "apa_attention_cache", q.data_ptr(), _DTYPES[q.dtype], qb, qh, qr, pages.data_ptr(), num_pages,
-             block_table.data_ptr(), block_table.shape[1], lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hq,
-             Hkv, Nq, d, int(window), int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr(),
+             block_table.data_ptr(), _int(block_table.shape[1]), lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, Hq,
+             Hkv, Nq, d, _int(window), _int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr(),
              workspace.data_ptr(), workspace.numel())
     return out, lse

@@ -2,7 +2,7 @@
 ``apa_attention_window`` (``include/apa.h``)."""
 from __future__ import annotations
 
-from .cache import _Tensor, _empty, _enqueue, _f32, _need, torch
+from .cache import _Tensor, _empty, _enqueue, _f32, _int, _need, torch
 
 _bf16 = torch.bfloat16
 
@@ -26,6 +26,6 @@ def attention_window(q, k, v, window: int, sinks: int = 0, return_lse: bool = Tr
     dev = q.device
     out = _empty((B, Hq, Nq, d), dtype=_bf16, device=dev)
     lse = _empty((B, Hq, Nq), dtype=_f32, device=dev) if return_lse else None
-    _enqueue(index, "apa_attention_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, int(window),
-             int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
+    _enqueue(index, "apa_attention_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, _int(window),
+             _int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
     return out, lse

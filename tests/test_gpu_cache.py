@@ -580,3 +580,28 @@ def test_two_streams_at_once():
         for out, lse in got[i]:
             assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
     apa.check_error()
+
+
+def test_numbers_past_32_bits_keep_their_meaning():
+    """A window or sinks past 2^32 reach over every key (and are not their low 32 bits); a negative one is refused."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(13)
+    pages, table, ks, vs, _ = _cache(rng, 1, 2, 64, [300], 6)
+    q = _torch(rng.standard_normal((1, 4, 2, 64)), torch.bfloat16)
+    args = (q, pages, table, _torch(np.array([300], np.int32)), _torch(ks), _torch(vs))
+    want = apa.attention_cache(*args)
+    kv = [_torch(rng.standard_normal((1, 2, 300, 64)), torch.bfloat16) for _ in range(2)]
+    full = apa.attention_window(q, *kv, 300)
+    for window, sinks in ((2**32 + 1, 0), (2**31, 0), (1, 2**32), (1, 2**31 + 5)):
+        assert all(torch.equal(a, b) for a, b in zip(apa.attention_cache(*args, window=window, sinks=sinks), want))
+        assert all(torch.equal(a, b) for a, b in zip(apa.attention_window(q, *kv, window, sinks), full))
+    for window, sinks in ((-2**32 + 5, 0), (4, -2**32)):
+        with pytest.raises(apa.ApaError):
+            apa.attention_cache(*args, window=window, sinks=sinks)
+        with pytest.raises(apa.ApaError):
+            apa.attention_window(q, *kv, window, sinks)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError):
+        apa.cache_tables(i32(1), i32(1), i32(1, 1), i32(1), i32(1), 2**32 + 1)
