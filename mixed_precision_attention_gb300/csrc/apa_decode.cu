@@ -956,7 +956,7 @@ auto with_config(int d, int rows, F f) {
 
 bool bad_heads(int B, int Hq, int Hkv, int Nq) {
   return B < 1 || B > kMaxSeqs || Hq < 1 || Hkv < 1 || Hq % Hkv || Hkv > (1 << 16) || Nq < 1 ||
-         (long long)(Hq / Hkv) * Nq > (1 << 20) || (long long)B * Hq * Nq > 0x7FFFFFFF;
+         (long long)(Hq / Hkv) * Nq > (1 << 20) || (long long)B * Hq * Nq > 0x7FFFFFF0;  // (rounded up to 8 it is an int)
 }
 
 }  // namespace
