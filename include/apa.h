@@ -276,7 +276,7 @@ int apa_attention_window(const void* q, const void* k, const void* v, int B, int
  * (the V order is the one the attention's matrix products read in place, and every
  * key owns whole bytes, so tokens are appended independently of each other).
  * A value is E2M1 * UE4M3 * the head's FP32 scale.  Quantization is apa_quantize's,
- * bit for bit, with the caller's head scales (positive and finite; the largest
+ * bit for bit, with the caller's head scales (2^-100 .. 2^100; the largest
  * magnitude expected divided by 2688; larger values saturate): scale code
  * b = UE4M3(fp32(max|x| / fp32(6 s))); codes 0 if b is 0, else
  * E2M1(fp32(x * fp32(1 / fp32(b s)))).  Keys are not mean-centred (the mean would

@@ -27,6 +27,7 @@
 // warps' parts of the others in order, and a second kernel those that span CTAs, so
 // results do not depend on timing.
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/apa.h"
@@ -436,7 +437,11 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
           }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          rf[nt][k] = __shfl_sync(0xffffffffu, down, (kQuad ? (2 * c + k) & 3 : 2 * c + k) * 4) * sc;
+          // a positive finite number: a masked score is -inf times it, a key of zeros 0 times it (without a
+          // value above 2^-100 in the row the product is 0 for k_scale < 1e-10; scores are below 2^35
+          // here, so that at the smallest normal number they are all 0 to FP32)
+          const float f = __shfl_sync(0xffffffffu, down, (kQuad ? (2 * c + k) & 3 : 2 * c + k) * 4) * sc;
+          rf[nt][k] = f < FLT_MIN ? FLT_MIN : f > FLT_MAX ? FLT_MAX : f;
           m[nt][k] = -INFINITY;
           l[nt][k] = 0.f;
         }
