@@ -279,7 +279,8 @@ int apa_attention_window(const void* q, const void* k, const void* v, int B, int
  * bit for bit, with the caller's head scales (2^-100 .. 2^100; the largest
  * magnitude expected divided by 2688; larger values saturate): scale code
  * b = UE4M3(fp32(max|x| / fp32(6 s))); codes 0 if b is 0, else
- * E2M1(fp32(x * fp32(1 / fp32(b s)))).  Keys are not mean-centred (the mean would
+ * E2M1(fp32(x * fp32(1 / fp32(b s)))).  Infinities saturate too; a NaN makes its
+ * group of 16 NaN (b = 0x7F, codes 0).  Keys are not mean-centred (the mean would
  * change with every appended key).
  * A slot names a key's place in the pool: page * 64 + key within the page. */
 size_t apa_cache_page_bytes(int Hkv, int d); /* bytes of one page: Hkv * 72 * d */

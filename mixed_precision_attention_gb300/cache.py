@@ -140,7 +140,8 @@ def cache_write(k, v, slots, pages, k_scale, v_scale):
     k, v: [Hkv, T, d] bf16 or fp16; channels contiguous, heads and tokens at any stride that is a multiple of
     8 elements (a projection's [T, Hkv, d] output goes in as ``k.transpose(0, 1)``).  slots: int32 [T], one
     for each token, no two alike; a token of a negative slot is skipped.  pages: the pool, written in place.
-    k_scale, v_scale: fp32 [Hkv], 2^-100 .. 2^100 (largest magnitude expected / 2688; larger values saturate)."""
+    k_scale, v_scale: fp32 [Hkv], 2^-100 .. 2^100 (largest magnitude expected / 2688; larger values, and
+    infinities, saturate).  A NaN makes its group of 16 channels NaN."""
     index = _need_rows("k", k, 3)
     Hkv, T, d = k.shape
     if _need_rows("v", v, 3) != index or v.shape != k.shape or v.dtype is not k.dtype:

@@ -378,8 +378,15 @@ __device__ __forceinline__ uint32_t e2m1_word(const float* x) {
       : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return w;
 }
+// The largest of three, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 // quant16's steps on 16 values in memory.  s6 = fp32(6 s); inv[b] = fp32(1 / fp32(b s)), 0 for
-// b = 0: 127 reciprocals per CTA and head instead of one per 16 values.
+// b = 0: 127 reciprocals per CTA and head instead of one per 16 values.  A group with a NaN gets
+// the scale code 0x7F, which is NaN, and codes of 0, so that it reads back as NaN.
 template <bool F16>
 __device__ __forceinline__ uint32_t quant_row(const uint16_t* src, bool wide, float s6, const float* inv, uint2* codes) {
   uint32_t w[8];
@@ -391,15 +398,17 @@ __device__ __forceinline__ uint32_t quant_row(const uint16_t* src, bool wide, fl
     x[2 * e] = f.x;
     x[2 * e + 1] = f.y;
   }
-  float a = fmaxf(fabsf(x[0]), fabsf(x[1]));
+  float a = max3_nan(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
 #pragma unroll
-  for (int e = 2; e < 16; e += 2) a = max3(a, fabsf(x[e]), fabsf(x[e + 1]));
+  for (int e = 3; e < 15; e += 2) a = max3_nan(a, fabsf(x[e]), fabsf(x[e + 1]));
+  a = max3_nan(a, fabsf(x[15]), 0.f);
   const uint32_t sb = cvt_ue4m3(__fdiv_rn(a, s6)) & 127u;  // (no sign, whatever the scale)
   const float f = inv[sb];
 #pragma unroll
   for (int e = 0; e < 16; ++e) x[e] = __fmul_rn(x[e], f);
-  codes->x = sb ? e2m1_word(x) : 0u;
-  codes->y = sb ? e2m1_word(x + 8) : 0u;
+  const bool some = sb - 1u < 126u;  // neither 0 nor NaN
+  codes->x = some ? e2m1_word(x) : 0u;
+  codes->y = some ? e2m1_word(x + 8) : 0u;
   return sb;
 }
 

@@ -44,3 +44,53 @@ def test_rows_of_zeros_under_any_key_scale(d, Hq, Nq, lens, window, sinks, k_sca
                                    sinks=sinks)
     apa.check_error()
     _near(out, lse, _attend(qt.double().cpu().numpy(), kv, lens, window, sinks), "bf16")
+
+
+# ------------------------------------------------------------------ values that are no numbers
+def _with_nonfinite(rng, H, T, d, dtype):
+    """k, v [H, T, d] of which some groups of 16 hold a NaN (one, or all 16), some infinities, some both."""
+    import torch
+    x = rng.standard_normal((2, H, T, d))
+    x[0, 0, 1, 3] = x[1, 0, 2, 17] = np.nan
+    x[0, H - 1, 3, 16:32] = x[1, H - 1, 3, 48:64] = np.nan
+    x[0, 0, 5, 40], x[1, 0, 5, 41] = np.inf, -np.inf
+    x[0, 0, T - 1, :2], x[1, 0, T - 1, :2] = (np.nan, np.inf), (-np.inf, np.nan)
+    return [_torch(a, dtype) for a in x]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("order", ["run", "any"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_a_nan_stays_one_and_infinities_saturate(d, order, dtype):
+    """A NaN makes its group of 16 NaN (scale code 0x7F, codes 0) and no other; an infinity is the largest value."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(d)
+    H, T, P, dt = 2, 23, 4, _types()[dtype]
+    slots = 64 + 4 + np.arange(T) if order == "run" else rng.permutation(P * 64)[:T]
+    k, v = _with_nonfinite(rng, H, T, d, dt)
+    ks, vs = rng.uniform(0.3, 2, (2, H)).astype(np.float32) / 448
+    want = rng.integers(0, 256, (P, H, 72 * d), dtype=np.uint8)
+    pages = _torch(want.copy())
+    values = []
+    quantized = []
+    for x, s in ((k, ks), (v, vs)):
+        a = x.double().cpu().numpy()
+        nan = np.isnan(a).reshape(H, T, d // 16, 16).any(-1)
+        code, sb = _quantize(np.where(nan.repeat(16, -1), 0, a), s[:, None, None])
+        assert (sb[np.isinf(a).reshape(H, T, d // 16, 16).any(-1) & ~nan] == 126).all()
+        sb[nan] = 0x7F
+        quantized.append((code, sb))
+        # (_value takes the code 0x7F for the largest scale)
+        values.append(np.where(nan.repeat(16, -1), np.nan, _value(code, sb).astype(np.float32) * s[:, None, None]))
+    for t in range(T):
+        for h in range(H):
+            _set(want, slots[t], h, *[(c[h, t], sb[h, t]) for c, sb in quantized])
+    s32 = _torch(slots.astype(np.int32))
+    apa.cache_write(k, v, s32, pages, _torch(ks), _torch(vs))
+    apa.check_error()
+    assert np.array_equal(pages.cpu().numpy(), want)
+    for got, ref in zip(apa.cache_read(pages, s32, _torch(ks), _torch(vs), dtype=dt), values):
+        ref = _torch(ref.astype(np.float32)).to(dt)
+        assert torch.equal(got.isnan(), ref.isnan()) and torch.equal(got.nan_to_num(0), ref.nan_to_num(0))
