@@ -349,7 +349,9 @@ int apa_cache_read(const uint8_t* pages, int num_pages, int dtype, int Hkv, int 
  *            apa_check_error (only entries of visible keys are read)
  *   lens     int32 [B]: keys per sequence, the rows' own among them, in
  *            [0, 64 * max_pages] (others are clamped to it and reported).  Keys past
- *            lens[b], and whatever a page holds there, are never used.
+ *            lens[b] or between the sinks and the first row's window, and whatever a
+ *            page holds there, are never used.  (With Nq > 1, a NaN in V at a key that
+ *            some of the sequence's rows see may reach the others' outputs too.)
  *   out      dtype [B][Hq][Nq][d], contiguous; a row that sees no key is zero
  *   lse      fp32 [B][Hq][Nq], natural log (nullable); -inf for such a row
  *   workspace  apa_attention_cache_workspace_bytes() bytes, 256-byte aligned, or null

@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
       }
       const int pmin = len - p.Nq + r0 / G;                             // positions of the block's first row
       const int pmax = len - p.Nq + min(r0 + kRows - 1, R - 1) / G;  // and of its last
+      const int gap_end = p.window ? pmin - p.window + 1 : 0;  // no row sees the keys from sinks to here
 
       for (; x < seg_end; ++x) {
         if (!__all_sync(0xffffffffu, mbar_test_wait(bar0 + 8 * st, parity))) {
@@ -479,6 +480,24 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
             else  // of two keys
               *reinterpret_cast<uint2*>(dst) = make_uint2(f0, f1);
           }
+        // nor do keys between the sinks and the first row's window (a weight of 0 does not hide a NaN):
+        // this lane's scales of them, once more
+        if (j0 < gap_end && j0 + kUnit > p.sinks) {
+#pragma unroll 1
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll 1
+            for (int i = lane; i < 4 * kTiles; i += 32) {
+              const int kc = i / kTiles, j = j0 + 16 * mb + 4 * kc;
+              uint8_t* dst = scales + mb * (C::kScaleBytes / 2) + (kQuad ? 16 : 8) * (4 * (i % kTiles) + kc);
+              for (int k = 0; k < 4; ++k)
+                if (j + k >= p.sinks && j + k < gap_end) {
+                  if constexpr (kQuad)
+                    reinterpret_cast<uint32_t*>(dst)[k] = 0u;
+                  else
+                    reinterpret_cast<uint16_t*>(dst)[k] = 0;
+                }
+            }
+        }
         __syncwarp();
         // ---- S^T = K Q^T.  Rows g and g + 8 of the product are keys 4 (g/2) + g%2 and that + 2, so
         // that a lane's four keys of V^T below are neighbours.  Both blocks go side by side.

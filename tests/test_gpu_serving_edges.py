@@ -94,3 +94,32 @@ def test_a_nan_stays_one_and_infinities_saturate(d, order, dtype):
     for got, ref in zip(apa.cache_read(pages, s32, _torch(ks), _torch(vs), dtype=dt), values):
         ref = _torch(ref.astype(np.float32)).to(dt)
         assert torch.equal(got.isnan(), ref.isnan()) and torch.equal(got.nan_to_num(0), ref.nan_to_num(0))
+
+
+@pytest.mark.parametrize("d,Hq,Nq,n,window,sinks,bad", [
+    (64, 2, 1, 130, 20, 0, [96, 109]),       # in the half page in which the window starts
+    (128, 6, 1, 200, 70, 5, [5, 31, 129]),   # behind the sinks; before the window
+    (256, 2, 1, 190, 29, 2, [2, 160]),
+    (128, 4, 3, 310, 40, 33, [33, 63, 267]),
+    (64, 40, 1, 100, 3, 1, [1, 96]),         # more than one row block
+    (64, 1, 1, 40, 1, 0, [32, 38])])
+def test_a_nan_that_no_row_sees(d, Hq, Nq, n, window, sinks, bad):
+    """Keys between the sinks and the window, NaN in every channel of K and V, in units that the rows do read."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(n)
+    pages, table, ks, vs, kv = _cache(rng, 1, 1, d, [n], n // 64 + 2)
+    first = n - Nq
+    assert all(sinks <= j <= first - window for j in bad)
+    slots = (table[0, torch.tensor(bad, device="cuda") // 64] * 64 + torch.tensor(bad, device="cuda", dtype=torch.int32) % 64)
+    x = torch.full((1, len(bad), d), math.nan, dtype=torch.bfloat16, device="cuda")
+    apa.cache_write(x, x, slots.to(torch.int32), pages, _torch(ks), _torch(vs))
+    q = _torch(rng.standard_normal((1, Hq, Nq, d)) * 2, torch.bfloat16)
+    out, lse = apa.attention_cache(q, pages, table, _torch(np.array([n], np.int32)), _torch(ks), _torch(vs), window=window,
+                                   sinks=sinks)
+    apa.check_error()
+    _near(out, lse, _attend(q.double().cpu().numpy(), kv, [n], window, sinks), "bf16")
+    # with the window open it is seen, by every row
+    out, lse = apa.attention_cache(q, pages, table, _torch(np.array([n], np.int32)), _torch(ks), _torch(vs))
+    assert out.isnan().all() and lse.isnan().all()
