@@ -320,7 +320,8 @@ int apa_cache_tables(const int32_t* old_lens, const int32_t* new_lens, int B, in
 
 /* Quantizes T tokens' keys and values into their slots of the cache.
  *   k, v     dtype (APA_DTYPE_*) [Hkv][T][d]; channels contiguous, heads and tokens
- *            at the given strides (in elements, multiples of 8); 16-byte aligned.
+ *            at the given strides (in elements, multiples of 8; of an axis of length 1
+ *            any); 16-byte aligned.
  *            (A projection's [T][Hkv][d] output is such an array.)
  *   slots    int32 [T]; a negative slot's token is skipped (padding), one outside the
  *            pool is skipped and reported by apa_check_error.  Slots of one call differ
@@ -343,7 +344,7 @@ int apa_cache_read(const uint8_t* pages, int num_pages, int dtype, int Hkv, int 
  * position p = lens[b] - Nq + i, sees key j iff j <= p and, with window >= 1,
  * (j > p - window or j < sinks); window = 0: every key up to p.
  *   q        dtype [B][Hq][Nq][d]; channels contiguous, the rest at the given strides
- *            (in elements, multiples of 8); 16-byte aligned
+ *            (in elements, multiples of 8; of an axis of length 1 any); 16-byte aligned
  *   block_table  int32 [B][max_pages]: entry t of sequence b is the page of its keys
  *            64t .. 64t+63; an entry outside the pool reads page 0 and is reported by
  *            apa_check_error (only entries of visible keys are read)

@@ -655,6 +655,9 @@ int apa_cache_write(const void* k, const void* v, int dtype, int Hkv, int T, int
   if (st) return st;
   if (T == 0) return APA_OK;
   if (!k || !v || !slots || !pages || !k_scale || !v_scale) return APA_ERR_NULL;
+  // (the stride of an axis of length 1 is never used: any value will do)
+  if (Hkv == 1) k_head_stride = v_head_stride = 0;
+  if (T == 1) k_token_stride = v_token_stride = 0;
   if ((((uintptr_t)k | (uintptr_t)v | (uintptr_t)pages) & 15) ||
       ((k_head_stride | k_token_stride | v_head_stride | v_token_stride) & 7))
     return APA_ERR_ALIGN;

@@ -1008,6 +1008,10 @@ int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long
   if (d != 64 && d != 128 && d != 256) return APA_ERR_HEAD_DIM;
   if (dtype != APA_DTYPE_BF16 && dtype != APA_DTYPE_F16) return APA_ERR_DTYPE;
   if (window < 0 || sinks < 0) return APA_ERR_WINDOW;
+  // (the stride of an axis of length 1 is never used: any value will do)
+  if (B == 1) q_batch_stride = 0;
+  if (Hq == 1) q_head_stride = 0;
+  if (Nq == 1) q_row_stride = 0;
   if ((((uintptr_t)q | (uintptr_t)pages | (uintptr_t)out) & 15) || ((q_batch_stride | q_head_stride | q_row_stride) & 7))
     return APA_ERR_ALIGN;
   const size_t need = apa_attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d);

@@ -123,3 +123,40 @@ def test_a_nan_that_no_row_sees(d, Hq, Nq, n, window, sinks, bad):
     # with the window open it is seen, by every row
     out, lse = apa.attention_cache(q, pages, table, _torch(np.array([n], np.int32)), _torch(ks), _torch(vs))
     assert out.isnan().all() and lse.isnan().all()
+
+
+# ------------------------------------------------------------------ axes of one element
+def test_strides_of_axes_of_length_one_do_not_matter():
+    """They are never used, so any value of theirs is taken: here 1, 3 and 5 elements."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(2)
+    d = 64
+    pages, table, ks, vs, _ = _cache(rng, 1, 1, d, [70], 3)
+    s = (_torch(ks), _torch(vs))
+    n = _torch(np.array([70], np.int32))
+    q = _torch(rng.standard_normal((1, 1, 1, d)), torch.bfloat16)
+    want = apa.attention_cache(q, pages, table, n, *s)
+    got = apa.attention_cache(q.as_strided(q.shape, (1, 3, 5, 1)), pages, table, n, *s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # one row of many heads, as a view that puts the row's axis last makes it
+    q = _torch(rng.standard_normal((1, 3, 1, d)), torch.bfloat16)
+    want = apa.attention_cache(q, pages, table, n, *s)
+    got = apa.attention_cache(q.reshape(1, 3, d, 1).transpose(2, 3), pages, table, n, *s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    k, v = (_torch(rng.standard_normal((1, 1, d)), torch.bfloat16) for _ in range(2))
+    slot = _torch(np.array([77], np.int32))
+    a, b = pages.clone(), pages.clone()
+    apa.cache_write(k, v, slot, a, *s)
+    apa.cache_write(k.as_strided(k.shape, (1, 5, 1)), v.as_strided(v.shape, (3, 1, 1)), slot, b, *s)
+    assert torch.equal(a, b) and not torch.equal(a, pages)
+    apa.check_error()
+    # those of longer axes do
+    two = torch.zeros(200, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(apa.ApaError):
+        apa.attention_cache(two.as_strided((1, 2, 1, d), (1, 68, 3, 1)), pages, table, n, *s)
+    with pytest.raises(apa.ApaError):
+        apa.cache_write(two.as_strided((1, 2, d), (1, 68, 1)), two.as_strided((1, 2, d), (1, 68, 1)),
+                        _torch(np.array([3, 4], np.int32)), pages, *s)
