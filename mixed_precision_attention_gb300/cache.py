@@ -179,8 +179,8 @@ def cache_read(pages, slots, k_scale, v_scale, dtype=torch.bfloat16):
 
 
 def attention_cache_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int) -> int:
-    """Bytes of workspace that attention_cache() needs for these sizes."""
-    return int(_lib.load().apa_attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d))
+    """Bytes of workspace that attention_cache() needs for these sizes; 0 if it does not take them."""
+    return _lib.load().apa_attention_cache_workspace_bytes(_int(B), _int(Hq), _int(Hkv), _int(Nq), _int(d))
 
 
 def attention_cache(q, pages, block_table, lens, k_scale, v_scale, window: int = 0, sinks: int = 0,
@@ -205,7 +205,7 @@ def attention_cache(q, pages, block_table, lens, k_scale, v_scale, window: int =
         raise ValueError("block_table must be [B, max_pages] and lens [B]")
     dev = q.device
     if workspace is None:
-        workspace = _empty(attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d), dtype=_u8, device=dev)
+        workspace = _empty(_lib.load().apa_attention_cache_workspace_bytes(B, Hq, Hkv, Nq, d), dtype=_u8, device=dev)
     else:
         _need("workspace", workspace, _u8, 1, index)
     out = _empty((B, Hq, Nq, d), dtype=q.dtype, device=dev)
