@@ -24,8 +24,9 @@
  *     aligned.
  *   - Calls are asynchronous: they enqueue work on `stream` and return.
  *     Asynchronous kernel errors surface at the caller's next synchronisation;
- *     a device-side wait that timed out is recorded in a library-wide device
- *     error word that apa_check_error() reports.
+ *     a device-side wait that timed out, or a page, slot or length in device
+ *     memory that is out of range, is recorded in a library-wide device error
+ *     word that apa_check_error() reports.
  *   - Results are deterministic: reruns with the same inputs are bitwise equal.
  *   - On a negative status nothing has been enqueued.  No C++ exception crosses
  *     the ABI.
@@ -48,9 +49,9 @@ extern "C" {
 #define APA_ERR_EPS (-3)       /* eps < 0 or NaN */
 #define APA_ERR_HEAD_DIM (-4)  /* d not in {64, 128, 256} */
 #define APA_ERR_CUDA (-5)      /* a CUDA call or launch failed; cudaGetLastError() holds the cause */
-#define APA_ERR_NOMEM (-6)     /* the workspace could not be allocated, or the given one is too small */
+#define APA_ERR_NOMEM (-6)     /* the workspace could not be allocated, or the given one is too small or misaligned */
 #define APA_ERR_DEVICE (-7)    /* a kernel recorded a device-side error: a timeout, or a page, slot or length in device memory that is out of range (apa_check_error) */
-#define APA_ERR_ALIGN (-8)     /* q, k or v not 16-byte aligned */
+#define APA_ERR_ALIGN (-8)     /* a tensor not 16-byte aligned, or a stride no multiple of 8 elements */
 #define APA_ERR_SCRATCH (-9)   /* too large for the fixed scratch of apa_quantize_noalloc */
 #define APA_ERR_FLAGS (-10)    /* an unknown bit in `flags` */
 #define APA_ERR_DTYPE (-11)    /* an unknown element type */

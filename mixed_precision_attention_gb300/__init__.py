@@ -257,5 +257,6 @@ def quantize_noalloc(q, k, v, out=None):
 
 
 def check_error(device=None):
-    """Synchronizes the current stream and raises if a kernel recorded a device-side timeout."""
+    """Synchronizes the current stream and raises if a kernel recorded a device-side error: a wait that timed out, or a
+    page, slot or length in device memory that is out of range."""
     _lib.check(_lib.load().apa_check_error(_stream(device)), "apa_check_error")

@@ -192,8 +192,8 @@ def attention_cache(q, pages, block_table, lens, k_scale, v_scale, window: int =
     each sequence's keys with the rows' own.  Row i, at position p = lens - Nq + i, sees the keys j <= p, with
     window >= 1 only those with j > p - window or j < sinks.  Returns (out [B, Hq, Nq, d] of q's dtype,
     contiguous; lse fp32 [B, Hq, Nq] or None); a row that sees no key gives zeros and -inf.
-    workspace: optional uint8 CUDA tensor of at least attention_cache_workspace_bytes(...) bytes; calls that
-    can overlap on the GPU need one each."""
+    workspace: optional uint8 CUDA tensor of at least attention_cache_workspace_bytes(...) bytes, 256-byte
+    aligned; calls that can overlap on the GPU need one each."""
     index = _need_rows("q", q, 4)
     B, Hq, Nq, d = q.shape
     num_pages, Hkv, dim = _need_pool(pages, k_scale, v_scale, index)

@@ -554,9 +554,9 @@ const char* apa_status_string(int status) {
     case APA_ERR_EPS: return "eps must be >= 0 and not NaN (> 0 where pass-1 operands are asked for)";
     case APA_ERR_HEAD_DIM: return "head dimension must be 64, 128 or 256";
     case APA_ERR_CUDA: return "CUDA error (see cudaGetLastError)";
-    case APA_ERR_NOMEM: return "workspace allocation failed or workspace too small";
-    case APA_ERR_DEVICE: return "a kernel recorded a device-side error (a wait timed out, or a block-table entry was outside the page pool)";
-    case APA_ERR_ALIGN: return "q, k and v must be 16-byte aligned";
+    case APA_ERR_NOMEM: return "workspace allocation failed, or the workspace is too small or not 256-byte aligned";
+    case APA_ERR_DEVICE: return "a kernel recorded a device-side error (a wait timed out, or a page, slot or length in device memory was out of range)";
+    case APA_ERR_ALIGN: return "tensors must be 16-byte aligned, and strides multiples of 8 elements";
     case APA_ERR_SCRATCH: return "problem too large for the fixed scratch of apa_quantize_noalloc";
     case APA_ERR_FLAGS: return "unknown option flag";
     case APA_ERR_DTYPE: return "unknown element type (bf16 or fp16)";
