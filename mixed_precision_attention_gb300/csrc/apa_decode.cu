@@ -101,8 +101,9 @@ struct DecCfg {
     const int r = ring_off(B) + W * stages(B) * kUnitBytes, m = kBarBytes + kMergeBytes;
     return r > m ? r : m;
   }
-  // (two stages or more, but for 16 rows at d = 256 from 2600 sequences on: one, without overlap)
-  static constexpr bool kFits = stages(kMaxSeqs) >= 1 && smem(kMaxSeqs) <= 232448 - kStaticBytes;
+  // (two stages or more, but for 16 rows at d = 256 from 2332 sequences on: one, without overlap)
+  static constexpr bool kFits = stages(D * ROWS == 4096 ? 2331 : kMaxSeqs) >= 2 && stages(kMaxSeqs) >= 1 &&
+                                smem(kMaxSeqs) <= 232448 - kStaticBytes;
   static size_t ws_bytes(int B) {
     return align256((size_t)(B + 1) * 4) + align256((size_t)kSlots * kRows * 8) + (size_t)kSlots * kRows * D * 4;
   }
