@@ -160,3 +160,148 @@ def test_strides_of_axes_of_length_one_do_not_matter():
     with pytest.raises(apa.ApaError):
         apa.cache_write(two.as_strided((1, 2, d), (1, 68, 1)), two.as_strided((1, 2, d), (1, 68, 1)),
                         _torch(np.array([3, 4], np.int32)), pages, *s)
+
+
+# ------------------------------------------------------------------ long lists
+@pytest.mark.parametrize("most", [8192, 8193, 20001])
+def test_tables_that_are_refused_fill_every_slot(most):
+    """Statuses of calls on both sides of 8192 tokens: every slot -1, every position 0, nothing changed."""
+    import mixed_precision_attention_gb300 as apa
+    i32 = lambda a: _torch(np.asarray(a, np.int32))  # noqa: E731
+    pages = most // 64 + 3
+    table, free = np.full((2, pages), -7), np.arange(pages + 1)
+    table[0, :3] = [900, 901, 902]
+    for old, new, count, status in [
+        ([0, -1], [1, 1], 3, 1), ([0, 0], [1, 64 * pages + 1], 3, 1), ([0, 0], [most, 1], pages, 2),
+        ([0, 0], [most, 0], 2, 3), ([129, 0], [0, most - 1], 0, 3), ([192, 0], [0, 1], pages, 4), ([0, 0], [1, 1], pages + 2, 4),
+    ]:
+        t, f, c = i32(table), i32(free), i32([count])
+        r = apa.cache_tables(i32(old), i32(new), t, f, c, most)
+        assert int(r["status"]) == status
+        assert (r["slots"] == -1).all() and not r["positions"].any() and not r["starts"].any()
+        assert r["slots"].numel() == most and int(r["free_count"]) == count
+        assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(f.cpu().numpy(), free)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("most", [8193, 9002, 9003])
+def test_tables_of_many_tokens_into_any_buffers(most, shift):
+    """The C entry point's slots and positions need not start on 16 bytes, nor their count be a multiple of 4."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    from mixed_precision_attention_gb300 import _lib
+    i32 = lambda a: _torch(np.asarray(a, np.int32))  # noqa: E731
+    rng = np.random.default_rng(most)
+    old, new = np.array([0, 70, 5, 64, 3]), np.array([3001, 71, 5, 0, 6000 - 6])
+    held = (old + 63) // 64
+    ids = rng.permutation(400)
+    table, at = np.full((5, 100), -1), 0
+    for b in range(5):
+        table[b, :held[b]] = ids[at:at + held[b]]
+        at += held[b]
+    free = np.full(400, -1)
+    free[:400 - at] = ids[at:]
+    if int(np.maximum(new - old, 0).sum()) > most:
+        new[4] = most - 3002 + 3
+    ref = _tables(old, new, table, free, 400 - at, most)
+    t, f, c, o, n = i32(table), i32(free), i32([400 - at]), i32(old), i32(new)
+    slots, pos = (torch.full((most + 8,), 77, dtype=torch.int32, device="cuda") for _ in range(2))
+    starts, status = torch.empty(6, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    st = _lib.load().apa_cache_tables(o.data_ptr(), n.data_ptr(), 5, t.data_ptr(), 100, f.data_ptr(), 400, c.data_ptr(), most,
+                                      slots[shift:].data_ptr(), pos[shift:].data_ptr(), starts.data_ptr(), c.data_ptr(),
+                                      status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and int(status) == 0
+    for got, want in ((slots, ref[0]), (pos, ref[1])):
+        got = got.cpu().numpy()
+        assert np.array_equal(got[shift:shift + most], want) and (got[:shift] == 77).all() and (got[shift + most:] == 77).all()
+    assert np.array_equal(starts.cpu().numpy(), ref[2]) and np.array_equal(t.cpu().numpy(), ref[3])
+    assert int(c) == len(ref[4]) and np.array_equal(f.cpu().numpy()[:len(ref[4])], ref[4])
+    apa.check_error()
+
+
+def test_one_long_sequence_among_many_rows():
+    """More than 1216 rows, so one warp joins a row, and a sequence that more than 32 CTAs hold parts of."""
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(9)
+    B, d, n = 1301, 64, 42001
+    pages, table, ks, vs, kv = _cache(rng, 1, 1, d, [n], n // 64 + 1)
+    lens = rng.integers(0, 33, B)  # a unit each, of the first page
+    lens[700] = n
+    assert n / 32 / ((n / 32 + B) / 152) > 64
+    q = _torch(rng.standard_normal((B, 1, 1, d)) * 2, _types()["bf16"])
+    out, lse = apa.attention_cache(q, pages, table.expand(B, -1).contiguous(), _torch(lens.astype(np.int32)), _torch(ks), _torch(vs))
+    apa.check_error()
+    some = np.array([0, 1, 699, 700, 701, 1300])
+    ref = _attend(q[some].double().cpu().numpy(), [[x[:, :lens[b]] for x in kv[0]] for b in some], lens[some], 0, 0)
+    _near(out[some], lse[some], ref, "bf16")
+
+
+# ------------------------------------------------------------------ two streams
+def test_every_operator_on_two_streams_at_once():
+    """Tables, writes, reads and both attentions on two streams, interleaved, each with a pool, tables and lists of its own,
+    against the same calls one after the other."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(21)
+    i32 = lambda a: _torch(np.asarray(a, np.int32))  # noqa: E731
+
+    def state(d, T, H):
+        x = [_torch(rng.standard_normal((H, T, d)), torch.bfloat16) for _ in range(2)]
+        return {"d": d, "T": T, "H": H, "kv": x, "s": [torch.full((H,), 4 / 2688, device="cuda") for _ in range(2)],
+                "q": _torch(rng.standard_normal((2, 2 * H, 3, d)), torch.bfloat16),
+                "qw": _torch(rng.standard_normal((1, 2 * H, 150, d)), torch.bfloat16)}
+
+    def loop(st):
+        d, T, H = st["d"], st["T"], st["H"]
+        pages = apa.cache_pages(2 * (T // 64 + 2), H, d)
+        table = torch.full((2, T // 64 + 2), -1, dtype=torch.int32, device="cuda")
+        free, count = torch.arange(pages.shape[0], dtype=torch.int32, device="cuda"), torch.full((1,), pages.shape[0], dtype=torch.int32, device="cuda")
+        got = []
+        old = torch.zeros(2, dtype=torch.int32, device="cuda")
+        for new in st["lens"]:
+            t = apa.cache_tables(old, new, table, free, count, T, free_count_out=count)
+            apa.cache_write(*st["kv"], t["slots"], pages, *st["s"])
+            k, v = apa.cache_read(pages, t["slots"], *st["s"])
+            got += [t["slots"], k, v, *apa.attention_cache(st["q"], pages, table, new, *st["s"], window=90, sinks=3)]
+            got += apa.attention_window(st["qw"], k[None], v[None], 70, sinks=2)
+            old = new
+        return got + [pages, table, free[:1], count]
+
+    states = [state(64, 700, 2), state(128, 300, 3)]
+    for st in states:
+        T = st["T"]
+        st["lens"] = [i32([T // 3, T // 2]), i32([T // 3 + 1, T // 2 + 1]), i32([T // 3 + 2, 0]), i32([T, 5])]
+    want = [loop(st) for st in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for i, side in enumerate(streams):
+            with torch.cuda.stream(side):
+                got[i].append(loop(states[i]))
+    torch.cuda.synchronize()
+    apa.check_error()
+    for i in range(2):
+        for run in got[i]:
+            assert len(run) == len(want[i]) and all(torch.equal(a, b) for a, b in zip(run, want[i]))
+
+
+@pytest.mark.parametrize("d,Hq,n,window,sinks,at", [(64, 1, 300, 20, 0, 130), (128, 3, 400, 200, 4, 64), (256, 2, 200, 1, 1, 100)])
+@pytest.mark.parametrize("what", [math.nan, math.inf, 3e38])
+def test_window_hides_scores_that_are_no_numbers(d, Hq, n, window, sinks, at, what):
+    """One key whose products with Q are NaN or overflow: the rows that do not see it are as they would be without it."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(n)
+    q, k, v = (_torch(rng.standard_normal((1, h, n, d)), torch.bfloat16) for h in (Hq, 1, 1))
+    if what == 3e38:
+        q[..., 0] = 8
+    want, want_lse = apa.attention_window(q, k, v, window, sinks=sinks)
+    k[0, 0, at] = what
+    out, lse = apa.attention_window(q, k, v, window, sinks=sinks)
+    apa.check_error()
+    hidden = [p for p in range(n) if p < at or p >= at + window]
+    assert torch.equal(out[:, :, hidden], want[:, :, hidden]) and torch.equal(lse[:, :, hidden], want_lse[:, :, hidden])
