@@ -453,7 +453,10 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
       }
       const int pmin = len - p.Nq + r0 / G;                             // positions of the block's first row
       const int pmax = len - p.Nq + min(r0 + kRows - 1, R - 1) / G;  // and of its last
-      const int gap_end = p.window ? pmin - p.window + 1 : 0;  // no row sees the keys from sinks to here
+      // the item's units from plain0 on, plain of them, hold only keys that some row sees; the others,
+      // those of the sinks among them, are looked at key by key
+      const int plain0 = p.window ? max(0, max(0, pmin - p.window + kUnit) / kUnit - lo) : 0;
+      const unsigned plain = max(len / kUnit - lo - plain0, 0);
 
       for (; x < seg_end; ++x) {
         if (!__all_sync(0xffffffffu, mbar_test_wait(bar0 + 8 * st, parity))) {
@@ -464,14 +467,19 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
         const int u = x - first, j0 = (u < sink ? u : u + lo) * kUnit;
         // ---- V's scales as FP16 pairs, converted once per warp (here, so that nothing below waits):
         // word i of a block holds those of keys 4 (i / kTiles) .. + 3 for tile i % kTiles.  Keys past
-        // the end: whatever the page holds there (NaN too) counts as 0.
+        // the end, and between the sinks and the first row's window, count as 0 whatever the page holds
+        // there: a weight of 0 does not hide a NaN.
+        const bool edge = (unsigned)(u - plain0) >= plain;
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
           for (int i = lane; i < 4 * kTiles; i += 32) {
-            const int kc = i / kTiles, left = len - (j0 + 16 * mb + 4 * kc);
+            const int kc = i / kTiles, j = j0 + 16 * mb + 4 * kc;
             uint32_t w = lds<uint32_t>(unit + mb * blk_bytes(D) + blk_vs(D) + 4 * i);
-            if (left < 4) w &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            if (edge)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (j + k >= len || (p.window && j + k <= pmin - p.window && j + k >= p.sinks)) w &= ~(255u << (8 * k));
             const uint32_t f0 = e4m3x2(w & 0xFFFFu), f1 = e4m3x2(w >> 16);
             uint8_t* dst = scales + mb * (C::kScaleBytes / 2) + (kQuad ? 16 : 8) * (4 * (i % kTiles) + kc);
             if constexpr (kQuad)  // (s, s) of each key
@@ -481,24 +489,6 @@ __global__ void __launch_bounds__(DecCfg<D, ROWS>::W * 32, 1) decode_kernel(cons
             else  // of two keys
               *reinterpret_cast<uint2*>(dst) = make_uint2(f0, f1);
           }
-        // nor do keys between the sinks and the first row's window (a weight of 0 does not hide a NaN):
-        // this lane's scales of them, once more
-        if (j0 < gap_end && j0 + kUnit > p.sinks) {
-#pragma unroll 1
-          for (int mb = 0; mb < 2; ++mb)
-#pragma unroll 1
-            for (int i = lane; i < 4 * kTiles; i += 32) {
-              const int kc = i / kTiles, j = j0 + 16 * mb + 4 * kc;
-              uint8_t* dst = scales + mb * (C::kScaleBytes / 2) + (kQuad ? 16 : 8) * (4 * (i % kTiles) + kc);
-              for (int k = 0; k < 4; ++k)
-                if (j + k >= p.sinks && j + k < gap_end) {
-                  if constexpr (kQuad)
-                    reinterpret_cast<uint32_t*>(dst)[k] = 0u;
-                  else
-                    reinterpret_cast<uint16_t*>(dst)[k] = 0;
-                }
-            }
-        }
         __syncwarp();
         // ---- S^T = K Q^T.  Rows g and g + 8 of the product are keys 4 (g/2) + g%2 and that + 2, so
         // that a lane's four keys of V^T below are neighbours.  Both blocks go side by side.

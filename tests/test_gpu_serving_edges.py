@@ -125,6 +125,28 @@ def test_a_nan_that_no_row_sees(d, Hq, Nq, n, window, sinks, bad):
     assert out.isnan().all() and lse.isnan().all()
 
 
+@pytest.mark.parametrize("d,Hq", [(64, 32), (128, 32), (256, 16)])
+@pytest.mark.parametrize("n,window,sinks", [(130, 20, 0), (229, 100, 7), (97, 1, 3)])
+def test_a_nan_that_later_rows_do_not_see(d, Hq, n, window, sinks):
+    """As many heads as a row block has rows, so that each position is a block of its own: the key with which the first
+    row's window starts is hidden from the other two, and a NaN there stays out of their outputs."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(n + d)
+    Nq, bad = 3, n - 3 - window + 1
+    pages, table, ks, vs, kv = _cache(rng, 1, 1, d, [n], n // 64 + 2)
+    x = torch.full((1, 1, d), math.nan, dtype=torch.bfloat16, device="cuda")
+    apa.cache_write(x, x, table[0, bad // 64].view(1) * 64 + bad % 64, pages, _torch(ks), _torch(vs))
+    q = _torch(rng.standard_normal((1, Hq, Nq, d)) * 2, torch.bfloat16)
+    out, lse = apa.attention_cache(q, pages, table, _torch(np.array([n], np.int32)), _torch(ks), _torch(vs), window=window,
+                                   sinks=sinks)
+    apa.check_error()
+    ref = _attend(q.double().cpu().numpy(), kv, [n], window, sinks)
+    _near(out[:, :, 1:], lse[:, :, 1:], [r[:, :, 1:] for r in ref], "bf16")
+    assert out[:, :, 0].isnan().all() and lse[:, :, 0].isnan().all()
+
+
 # ------------------------------------------------------------------ axes of one element
 def test_strides_of_axes_of_length_one_do_not_matter():
     """They are never used, so any value of theirs is taken: here 1, 3 and 5 elements."""
