@@ -259,8 +259,11 @@ size_t apa_q_blob_bytes(int B, int Hq, int Hkv, int Nq, int d);
  *   lse      fp32 [B, Hq, Nq], natural-log log-sum-exp of the scaled scores (nullable)
  * Exact attention, as the eps = 0 form of apa_attention: BF16 Q K^T and FP32
  * softmax statistics; here P is rounded to BF16 for the product with V itself
- * (relative error 2^-8 at most per weight, as the rounding of the output).  Only the
- * key tiles that a row block sees are read.  No workspace. */
+ * (relative error 2^-8 at most per weight, as the rounding of the output; apa_attention
+ * at eps = 0 rounds it to FP16 and returns FP32).  Only the key tiles that a row block
+ * sees are read.  V must be finite: a NaN or an infinity in it reaches, beside the rows
+ * that see its key, others of their blocks of 128 packed rows.  A K that is not finite
+ * reaches only the rows that see it.  No workspace. */
 int apa_attention_window(const void* q, const void* k, const void* v, int B, int Hq, int Hkv, int Nq, int Nkv, int d,
                          int window, int sinks, void* out, float* lse, cudaStream_t stream);
 

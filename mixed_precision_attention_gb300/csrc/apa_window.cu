@@ -4,8 +4,8 @@
 // j < sinks, x the row's position.  The matrix products bound it (4 d flop per visible
 // pair); what it comes to is set by the hand-overs between S, softmax and P.V of a tile,
 // and, as walks are short, by what happens between two row blocks.  24 heads on 8, d = 128:
-// 8192 rows, window 1024: 117 us (0.43 of the measured BF16 rate, the masked parts of
-// tiles not counted); 16384 rows at the end of 122880 keys, window 4096: 650 us (0.67).
+// 8192 rows, window 1024: 116 us (0.44 of the measured BF16 rate, the masked parts of
+// tiles not counted); 16384 rows at the end of 122880 keys, window 4096: 661 us (0.66).
 //
 // One work item = 128 GQA-packed rows of one KV head (tcgen05 M = 128), which walk the
 // 64-key tiles that hold sinks and those that their windows reach.  Persistent CTAs, two
@@ -25,6 +25,8 @@
 // P goes to the product in BF16 (2^-8 relative, the rounding of the output) against V
 // itself, so there is no copy of V and no workspace; l adds the FP32 values.  The
 // running maximum moves only when a score exceeds it by 8 (log2 units).
+// Hidden scores are masked whatever they are.  A hidden V has the weight 0 in the product,
+// which hides every finite value, but not a NaN or an infinity.
 #include <atomic>
 
 #include "apa_internal.h"

@@ -12,7 +12,9 @@ def attention_window(q, k, v, window: int, sinks: int = 0, return_lse: bool = Tr
 
     q: [B, Hq, Nq, d] bf16; k, v: [B, Hkv, Nkv, d] bf16 (CUDA, contiguous, Nkv >= Nq).  Query row i, at
     position p = i + Nkv - Nq, sees the keys j <= p with j > p - window (window >= 1 keys, its own among
-    them) or j < sinks.  Returns (out bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] or None)."""
+    them) or j < sinks.  Returns (out bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] or None).  Scores, softmax
+    and sums are FP32; the weights are rounded to bf16 (2^-8 relative) for the product with V, which must be
+    finite."""
     if not isinstance(q, _Tensor) or not q.is_cuda:
         raise ValueError("q must be on a CUDA device")
     index = q.get_device()
