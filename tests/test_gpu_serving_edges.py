@@ -327,3 +327,74 @@ def test_window_hides_scores_that_are_no_numbers(d, Hq, n, window, sinks, at, wh
     apa.check_error()
     hidden = [p for p in range(n) if p < at or p >= at + window]
     assert torch.equal(out[:, :, hidden], want[:, :, hidden]) and torch.equal(lse[:, :, hidden], want_lse[:, :, hidden])
+
+
+# ------------------------------------------------------------------ large
+@pytest.mark.parametrize("d,Hq,Nq,lens,window,sinks", [
+    (128, 8, 150, [400, 90], 0, 0), (64, 6, 333, [333], 50, 70), (256, 4, 100, [1000, 0, 31], 200, 3)])
+def test_many_query_rows(d, Hq, Nq, lens, window, sinks):
+    """The end of a prompt: hundreds of rows per head, so many row blocks of one item's keys."""
+    import mixed_precision_attention_gb300 as apa
+    rng = np.random.default_rng(Nq)
+    pages, table, ks, vs, kv = _cache(rng, len(lens), 2, d, lens, max(lens) // 64 + 2)
+    q = _torch(rng.standard_normal((len(lens), Hq, Nq, d)), _types()["bf16"])
+    out, lse = apa.attention_cache(q, pages, table, _torch(np.asarray(lens, np.int32)), _torch(ks), _torch(vs), window=window,
+                                   sinks=sinks)
+    apa.check_error()
+    _near(out, lse, _attend(q.double().cpu().numpy(), kv, lens, window, sinks), "bf16")
+
+
+def test_a_pool_and_values_past_32_bits():
+    """Pages behind the first 4 GB of a pool, and tokens behind the first 4 GB of what is written and read, are what they
+    are in a small one."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    H, d, n = 8, 256, 1200
+    rng = np.random.default_rng(6)
+    big = torch.empty(40000, H, 72 * d, dtype=torch.uint8, device="cuda")
+    small = apa.cache_pages(20, H, d)
+    big[39900:] = 0
+    assert big.numel() > 2 ** 32
+    T = 1100000  # of which the last n have slots
+    k, v = (torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda").transpose(0, 1) for _ in range(2))
+    assert k.numel() * 2 > 2 ** 32
+    for x in (k, v):
+        x[:, T - n:] = _torch(rng.standard_normal((H, n, d)), torch.bfloat16)
+    s = (_torch(np.full(H, 5 / 2688, np.float32)),) * 2
+    at = torch.arange(n, dtype=torch.int32, device="cuda")
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    slots[T - n:] = (39999 - at // 64) * 64 + at % 64
+    apa.cache_write(k, v, slots, big, *s)
+    apa.cache_write(k[:, T - n:], v[:, T - n:], at, small, *s)
+    assert torch.equal(big[39981:].flip(0), small[:19])
+    got = apa.cache_read(big, slots, *s)
+    want = apa.cache_read(small, at, *s)
+    for a, b in zip(got, want):
+        assert torch.equal(a[:, T - n:], b) and not a[:, :T - n].any()
+    q = _torch(rng.standard_normal((1, 2 * H, 1, d)), torch.bfloat16)
+    lens = _torch(np.array([n], np.int32))
+    table = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    want = apa.attention_cache(q, small, table, lens, *s)
+    got = apa.attention_cache(q, big, 39999 - table, lens, *s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    apa.check_error()
+
+
+def test_window_over_keys_past_32_bits():
+    """The last rows of a context whose keys and values are more than 4 GB each."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    g = torch.Generator(device="cuda").manual_seed(3)
+    H, d, N, Nq, tail = 8, 128, 2200000, 70, 3000
+    k, v = (torch.zeros(1, H, N, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() * 2 > 2 ** 32
+    for x in (k, v):
+        x[:, :, N - tail:] = torch.randn(1, H, tail, d, device="cuda", generator=g).bfloat16()
+    q = torch.randn(1, 2 * H, Nq, d, device="cuda", generator=g).bfloat16()
+    got = apa.attention_window(q, k, v, 500)
+    assert (N - tail - 8) % 64 == 0  # so that the short context has the same tiles
+    want = apa.attention_window(q, k[:, :, N - tail - 8:].contiguous(), v[:, :, N - tail - 8:].contiguous(), 500)
+    apa.check_error()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
