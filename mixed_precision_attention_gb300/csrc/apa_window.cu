@@ -5,7 +5,7 @@
 // pair); what it comes to is set by the hand-overs between S, softmax and P.V of a tile,
 // and, as walks are short, by what happens between two row blocks.  24 heads on 8, d = 128:
 // 8192 rows, window 1024: 116 us (0.44 of the measured BF16 rate, the masked parts of
-// tiles not counted); 16384 rows at the end of 122880 keys, window 4096: 661 us (0.66).
+// tiles not counted); 16384 rows at the end of 122880 keys, window 4096: 663 us (0.65).
 //
 // One work item = 128 GQA-packed rows of one KV head (tcgen05 M = 128), which walk the
 // 64-key tiles that hold sinks and those that their windows reach.  Persistent CTAs, two
