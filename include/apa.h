@@ -374,6 +374,32 @@ int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long
                         size_t workspace_bytes, cudaStream_t stream);
 size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
 
+/* ------------------------------------------------------------------ an encoder's states
+ * Cross attention: every query row of sequence b sees the keys below lens[b] of its
+ * encoder's states; no causal order.
+ *   q        dtype (APA_DTYPE_*) [B][Hq][Nq][d]; channels contiguous, the rest at the given
+ *            strides (in elements, multiples of 8; of an axis of length 1 any); 16-byte aligned
+ *   k, v     dtype [B][Hkv][Nkv][d]; likewise, with strides that are not negative; a batch
+ *            or head stride of 0 shares one array (a token stride of 0 is refused)
+ *   lens     int32 [B], each in [0, Nkv] (others are clamped to it and reported by
+ *            apa_check_error); null: Nkv for all.  Keys behind the end are never used,
+ *            whatever is there
+ *   out      dtype [B][Hq][Nq][d], contiguous; rows of a sequence without keys are zero
+ *   lse      fp32 [B][Hq][Nq], natural log (nullable); -inf for such rows
+ *   workspace  apa_attention_cross_workspace_bytes() bytes, 256-byte aligned, or null to
+ *            have it allocated stream-ordered for the call.  Two calls that overlap on the
+ *            GPU must not share one.
+ * Scores, softmax statistics and sums are FP32; the softmax weights are rounded to dtype for
+ * the product with V (2^-8 relative at most in BF16, 2^-11 in FP16).  Nq = 1 (a decoding step)
+ * reads each KV head's states once for its G = Hq / Hkv rows.  B <= 8192.  The work is split
+ * over the GPU by the lengths alone, so reruns are bitwise equal. */
+int apa_attention_cross(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
+                        long long q_row_stride, const void* k, long long k_batch_stride, long long k_head_stride,
+                        long long k_token_stride, const void* v, long long v_batch_stride, long long v_head_stride,
+                        long long v_token_stride, const int32_t* lens, int B, int Hq, int Hkv, int Nq, int Nkv, int d,
+                        void* out, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t apa_attention_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
 /* Measurement aid, off by default.  While enabled, every apa_attention* call
  * records CUDA events on its stream around its three stages (quantizer, pass 1,
  * pass 2 with the merge); enabling or disabling resets the record. */

@@ -23,11 +23,12 @@ __all__ = ["attention", "attention_paged", "attention_host", "quantize", "quanti
            "status_string", "hot_mask_shape", "TILE", "GROUP_ROWS", "BLOCK_ROWS", "FLAG_Q_RESIDUAL",
            "FLAG_LSE_SCALES", "FLAG_VALUE_WEIGHTED", "FLAG_ROWSUM_MMA", "attention_window", "cache_pages",
            "cache_tables", "cache_write", "cache_read", "attention_cache", "attention_cache_workspace_bytes",
-           "TABLES_STATUS"]
+           "TABLES_STATUS", "attention_cross", "attention_cross_workspace_bytes"]
 
 _LATER = {n: "cache" for n in ("cache_pages", "cache_tables", "cache_write", "cache_read", "attention_cache",
                                "attention_cache_workspace_bytes", "TABLES_STATUS")}
 _LATER["attention_window"] = "window"
+_LATER["attention_cross"] = _LATER["attention_cross_workspace_bytes"] = "cross"
 
 
 def __getattr__(name):

@@ -40,6 +40,8 @@ _SIGS = {
     "apa_cache_read": (I, [P, I, I, I, I, I, P, P, P, P, P, P]),
     "apa_attention_cache": (I, [P, I, LL, LL, LL, P, I, P, I, P, P, P, I, I, I, I, I, I, I, P, P, P, SZ, P]),
     "apa_attention_cache_workspace_bytes": (SZ, [I, I, I, I, I]),
+    "apa_attention_cross": (I, [P, I, LL, LL, LL, P, LL, LL, LL, P, LL, LL, LL, P, I, I, I, I, I, I, P, P, P, SZ, P]),
+    "apa_attention_cross_workspace_bytes": (SZ, [I, I, I, I, I]),
     "apa_check_error": (I, [P]),
     "apa_stage_timing": (I, [I]),
     "apa_stage_timing_read": (I, [P, P]),

@@ -1,0 +1,797 @@
+// rows.cuh -- exact attention of packed query rows over tiles of keys, for sources of keys
+// that bring their own producers (rows_kernel), and the joining of split walks.
+//
+// out = softmax(q K^T c + mask) V for the G * Nq rows that share a KV head's keys, taken
+// together position-major in blocks of 128 (tcgen05 M).  A source says how many blocks and
+// key tiles each sequence has, fills K and V tiles in shared memory (FP16 or BF16, 128-byte
+// swizzle, a key per row), and masks scores.
+//
+// Work: an item is one block, or two neighbouring ones, of one KV head against all its
+// tiles; a use is one block against one tile.  The uses of all sequences form one list, cut
+// evenly over one CTA per SM, so lengths need not be alike and no length is read on the
+// host.  A CTA's run of tiles of one item is a segment.  An item that one CTA holds entirely
+// is written out at once; the states (m, l, O) of the others go to the workspace and a
+// second kernel joins them in order, so results do not depend on timing.
+//
+// Inside a CTA use u goes through buffer u % 2 of the scores in tensor memory, and (d <= 128)
+// through softmax group u % 2, four warps with one thread per row: either the two blocks of
+// an item against the same tile, or one block against two tiles in turn, whose two
+// states are then joined over tensor memory.  One thread issues every product, in the order
+// P V of use u, S of use u + 2: the products execute in that order, so S may go over the P
+// that lies in its columns, and the commit of S says that P V before it is done.  While one
+// group works on its scores the tensor cores have the other's S and P V.
+// At d = 256 O takes half of tensor memory: one group, which alternates between the buffers.
+//
+// Q is an operand in tensor memory where it fits (kQT): S = Q K^T of 64 keys would otherwise
+// read 6 KB of shared memory per 32 cycles of product, 1.5 times what it delivers.
+#pragma once
+#include <atomic>
+#include <cfloat>
+#include <cmath>
+
+#include "../../include/apa.h"
+#include "apa_internal.h"
+#include "cache_page.cuh"
+#include "tc.cuh"
+
+namespace apa {
+namespace {
+
+constexpr int kRowCtas = 152;      // one per SM
+constexpr int kMaxRowSeqs = 8192;
+constexpr float kTauRows = 8.f;    // lazy-maximum threshold, log2 units
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMinUses = 4;        // a CTA takes no fewer uses than these while others have none
+
+// n things in k nearly equal runs, the longer ones first.
+struct RowCut {
+  long long q;
+  int r, k;
+  __device__ __forceinline__ RowCut(long long n, int k_) : k(k_) {
+    q = n / k;
+    r = (int)(n - q * k);
+  }
+  __device__ __forceinline__ long long first(int i) const { return i >= k ? q * k + r : q * i + min(i, r); }
+};
+__device__ __forceinline__ int cut_ctas(long long total, int grid) {
+  const long long n = (total + kMinUses - 1) / kMinUses;
+  return n < 1 ? 1 : n < grid ? (int)n : grid;
+}
+
+// The item that begins in a CTA and goes on behind it (n = 0: none).
+struct SplitRec {
+  long long first, total;  // its first use in the list; the list's length
+  int b, h, rb, n, w, pad;
+};
+
+struct RowParams {
+  int B, Hq, Hkv, Nq;
+  const uint16_t* q;
+  long long qs_b, qs_h, qs_r;
+  uint16_t* out;  // [B][Hq][Nq][d]
+  float* lse;     // [B][Hq][Nq] or null
+  int* err;
+  // workspace
+  SplitRec* rec;    // [grid]
+  float2* part_ml;  // [2 grid][slot rows] (m, l): slots 2 cta + 1 and 2 cta are the CTA's part of the
+  float* part_o;    // [2 grid][slot rows][d]      item that ends in it, and of the one that goes on behind it
+  int slot_rows;
+  __host__ __device__ int G() const { return Hq / Hkv; }
+};
+
+template <int D_, int KT_, bool QT_, int NK_, int NV_, bool F16_>
+struct RowCfg {
+  static constexpr int D = D_, KT = KT_;
+  static constexpr bool QT = QT_, F16 = F16_;
+  static constexpr int NK = NK_, NV = NV_;
+  static constexpr int NG = D <= 128 ? 2 : 1;
+  static constexpr int kBlocks = NG;  // row blocks of an item, at most
+  static constexpr int kTileBytes = KT * D * 2;
+  static constexpr int kQBytes = QT ? 0 : 128 * D * 2;  // per block
+  static constexpr uint32_t kOCol = 0, kSCol = NG * D, kQCol = NG * D + 2 * KT;
+  static constexpr uint32_t kPOff = KT / 2;  // P, two keys per column, in the upper half of its S
+  static constexpr int kQOff = 0, kKOff = NG * kQBytes, kVOff = kKOff + NK * kTileBytes;
+  static constexpr int kSrcOff = kVOff + NV * kTileBytes;  // the source's own
+  static constexpr int kSoftWarps = 4 * NG, kMmaWarp = kSoftWarps, kSrcWarp = kSoftWarps + 1;
+  static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
+  static_assert(kQCol + (QT ? NG * D / 2 : 0) <= 512, "tensor memory");
+};
+
+// A CTA's run of tiles t0 .. t1-1 (of n) of one item: blocks rb .. rb+w-1 of head h of sequence b.
+struct RowSeg {
+  int b, h, rb, w, t0, t1, n;
+};
+// The segments of a CTA in order; seq: the source's numbers of the last one's sequence.
+template <class Src, int kBlocks>
+struct RowWalk {
+  using Seq = typename Src::Seq;
+  const typename Src::Params& p;
+  int b, item, pos, left;  // item of the sequence, uses into it, uses left
+  Seq seq;
+  __device__ __forceinline__ RowWalk(const typename Src::Params& p_, int b_, int item_, int pos_, int left_)
+      : p(p_), b(b_), item(item_), pos(pos_), left(left_), seq(p_, b_) {}
+  __device__ __forceinline__ bool next(RowSeg& g) {
+    while (left > 0) {
+      int per = (seq.blocks + kBlocks - 1) / kBlocks, h = item / per, rb = (item - h * per) * kBlocks;
+      int w = min(kBlocks, seq.blocks - rb);
+      if (pos == seq.tiles * w) {  // the next item
+        pos = 0;
+        if (++item == per * p.r.Hkv) {
+          item = 0;
+          do {
+            seq = Seq(p, ++b);
+          } while (seq.uses() == 0);
+          per = (seq.blocks + kBlocks - 1) / kBlocks;
+        }
+        h = item / per;
+        rb = (item - h * per) * kBlocks;
+        w = min(kBlocks, seq.blocks - rb);
+      }
+      const int end = min(seq.tiles * w, pos + left);
+      g = RowSeg{b, h, rb, w, pos / w, end / w, seq.tiles};
+      left -= end - pos;
+      pos = end;
+      if (g.t1 > g.t0) return true;  // (half a tile of two blocks is the next CTA's)
+    }
+    return false;
+  }
+};
+
+// used only while unwinding: waits for copies and products already in flight, ignoring the abort flag
+__device__ __forceinline__ void rows_wait_in_flight(uint32_t bar, uint32_t parity, int* err) {
+  const unsigned long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > APA_WAIT_LIMIT_CYCLES) {
+      if (err) atomicCAS(err, 0, APA_DEVERR_TIMEOUT);
+      return;
+    }
+  }
+}
+
+// P of eight consecutive keys, 2^(x*c2 + nb), as four words of two 16-bit values (key 2k in the low
+// half of word k); the FP32 values are added into (s0, s1): even keys into s0, odd keys into s1.
+// The affine step and the sums run as packed FP32 pairs.
+template <bool F16>
+__device__ __forceinline__ void rows_p8(const float* x, float c2, float nb, uint32_t* h, float& s0, float& s1) {
+  uint64_t c, n, one, s, a[4];
+  asm("mov.b64 %0, {%1, %1};" : "=l"(c) : "f"(c2));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(n) : "f"(nb));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(one) : "f"(1.f));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(s0), "f"(s1));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo, hi;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a[k]) : "f"(x[2 * k]), "f"(x[2 * k + 1]));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a[k]) : "l"(c), "l"(n));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a[k]));
+    lo = ex2_approx(lo);
+    hi = ex2_approx(hi);
+    h[k] = pack2<F16>(lo, hi);
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a[k]) : "f"(lo), "f"(hi));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(s) : "l"(a[k]), "l"(one));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(s));
+}
+
+// Barriers of the core (the source's follow): K and V rings, S, P, P.V per buffer, Q, the exchange of two
+// groups' states and its end, and the issuer's drain.
+template <class C>
+struct RowBars {
+  static constexpr int kKFull = 0, kKEmpty = C::NK, kVFull = 2 * C::NK, kVEmpty = 2 * C::NK + C::NV;
+  static constexpr int kS = 2 * C::NK + 2 * C::NV, kP = kS + 2, kPV = kS + 4, kQ = kS + 6, kX = kS + 7, kXDone = kS + 8,
+                       kDrain = kS + 9, kNum = kS + 10;
+  uint32_t bar0;
+  volatile int* abort;
+  int* err;
+  __device__ __forceinline__ uint32_t at(int i) const { return bar0 + 8u * i; }
+  __device__ __forceinline__ uint32_t k_full(int T) const { return at(kKFull + T % C::NK); }
+  __device__ __forceinline__ uint32_t k_empty(int T) const { return at(kKEmpty + T % C::NK); }
+  __device__ __forceinline__ uint32_t v_full(int T) const { return at(kVFull + T % C::NV); }
+  __device__ __forceinline__ uint32_t v_empty(int T) const { return at(kVEmpty + T % C::NV); }
+  static __device__ __forceinline__ uint32_t k_par(int T) { return (T / C::NK) & 1; }
+  static __device__ __forceinline__ uint32_t v_par(int T) { return (T / C::NV) & 1; }
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const { return mbar_wait(bar, parity, abort, err); }
+  // every lane waits; the warp proceeds only if all lanes succeeded
+  __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) const {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+  }
+};
+
+// The column of O that holds channel c: sources may store V's channels in another order within each 16.
+template <class Src>
+__device__ __forceinline__ constexpr int o_column(int c) {
+  return Src::kPairedV ? (c & ~15) | ((c & 7) << 1) | ((c >> 3) & 1) : c;
+}
+
+template <class Src>
+__global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_constant__ typename Src::Params p) {
+  using C = typename Src::Cfg;
+  using Bars = RowBars<C>;
+  constexpr int D = C::D, KT = C::KT, NG = C::NG;
+  constexpr uint32_t kTmemCols = 512;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t bar_mem[Bars::kNum + Src::kBars];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float2 xml[NG == 2 ? 2 : 1][NG == 2 ? 128 : 1];  // two groups' (m, l) of a row
+  __shared__ long long warp_sum[32];
+  __shared__ long long list_total;
+  __shared__ int found[2][2];             // sequence, and uses (of a head) before it: of the first and the last use
+  const RowParams& r = p.r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_u32(smem);
+  Bars bars{smem_u32(bar_mem), &abort_flag, r.err};
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < Bars::kNum; ++i) {
+      uint32_t count = 1;
+      if (i < Bars::kKEmpty) count = Src::kKArrivals;
+      if (i >= Bars::kVFull && i < Bars::kVEmpty) count = Src::kVArrivals;
+      if (i == Bars::kP || i == Bars::kP + 1) count = 4;
+      if (i == Bars::kQ || i == Bars::kX || i == Bars::kXDone) count = C::kSoftWarps;
+      mbar_init(bars.at(i), count);
+    }
+    for (int i = 0; i < Src::kBars; ++i) mbar_init(bars.at(Bars::kNum + i), Src::bar_count(i));
+    fence_mbar_init();
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  // ---- the list's length, then this CTA's place in it
+  constexpr int kWarps = Src::kThreads / 32;
+  {
+    long long sum = 0;
+    for (int b = tid; b < r.B; b += Src::kThreads) {
+      const typename Src::Seq s(p, b);
+      s.report(p, b);
+      sum += s.uses();
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) warp_sum[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      long long t = 0;
+      for (int w = 0; w < kWarps; ++w) t += warp_sum[w];
+      list_total = t * r.Hkv;
+    }
+    __syncthreads();
+  }
+  const long long total = list_total;
+  const RowCut cut(total, cut_ctas(total, gridDim.x));
+  const long long x0 = cut.first(blockIdx.x), x1 = cut.first(blockIdx.x + 1);
+  {
+    long long carry = 0;
+    for (int b0 = 0; x1 > x0 && b0 < r.B; b0 += Src::kThreads) {
+      const int b = b0 + tid;
+      const long long n = b < r.B ? typename Src::Seq(p, b).uses() : 0;
+      long long x = n;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, s);
+        if (lane >= s) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      long long before = carry, all = carry;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+      }
+      before += x - n;
+      for (int k = 0; k < 2; ++k) {
+        const long long at = k ? x1 - 1 : x0;
+        if (n > 0 && at >= before * r.Hkv && at < (before + n) * r.Hkv) {
+          found[k][0] = b;
+          found[k][1] = (int)before;
+        }
+      }
+      carry = all;
+      __syncthreads();
+    }
+  }
+  // ---- rows that no item covers: zeros
+  {
+    const int R = r.G() * r.Nq;
+    for (int b = blockIdx.x; b < r.B; b += gridDim.x) {
+      const typename Src::Seq s(p, b);
+      const int from = s.uses() > 0 ? min(R, s.blocks * kBlockRows) : 0;
+      for (long long i = tid; i < (long long)(R - from) * r.Hkv * (D / 8); i += Src::kThreads) {
+        const int c = (int)(i % (D / 8)), P = from + (int)(i / (D / 8) % (R - from)), h = (int)(i / (D / 8) / (R - from));
+        const size_t row = ((size_t)b * r.Hq + h * r.G() + P % r.G()) * r.Nq + P / r.G();
+        *reinterpret_cast<uint4*>(r.out + row * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+        if (c == 0 && r.lse) r.lse[row] = -INFINITY;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // a place in the list as (item of its sequence, uses into the item)
+  auto place = [&](int k, long long x, int& b, int& item, int& pos) {
+    b = found[k][0];
+    const typename Src::Seq s(p, b);
+    const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, head = (int)s.uses();
+    const long long y = x - (long long)found[k][1] * r.Hkv;
+    const int h = (int)(y / head), z = (int)(y - (long long)h * head), kk = z / (C::kBlocks * s.tiles);
+    item = h * per + kk;
+    pos = z - kk * C::kBlocks * s.tiles;
+  };
+  if (tid == 0) {
+    SplitRec rec{};
+    if (x1 > x0) {
+      int b, item, pos;
+      place(1, x1 - 1, b, item, pos);
+      const typename Src::Seq s(p, b);
+      const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, rb = item % per * C::kBlocks;
+      const int w = min(C::kBlocks, s.blocks - rb);
+      const long long first = x1 - 1 - pos;
+      if (first >= x0 && first + (long long)s.tiles * w > x1) rec = SplitRec{first, total, b, item / per, rb, s.tiles, w, 0};
+    }
+    r.rec[blockIdx.x] = rec;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (x1 > x0) {
+    int sb, sitem, spos;
+    place(0, x0, sb, sitem, spos);
+    RowWalk<Src, C::kBlocks> walk(p, sb, sitem, spos, (int)(x1 - x0));
+    if (warp >= C::kSrcWarp) {
+      Src::produce(p, walk, smem, sbase, bars, warp - C::kSrcWarp, lane);
+    } else if (warp == C::kMmaWarp) {
+      // ------------------------------------------------------------ the products' issuer
+      if (lane == 0) {
+        constexpr uint32_t idS = C::F16 ? idesc_f16(128, KT, 0) : idesc_bf16(128, KT, 0);
+        constexpr uint32_t idO = C::F16 ? idesc_f16(128, D, 1) : idesc_bf16(128, D, 1);
+        RowWalk<Src, C::kBlocks> ahead = walk;
+        // the next use to get its S: use su, of tile st0 + si of segment sn (sg), the first of its segment if sfresh
+        RowSeg sg{}, pg{};
+        bool more = ahead.next(sg), ok = true, fresh = true;
+        int su = 0, sT = 0, si = sg.t0, sj = 0, sn = 0;  // sj: block within the tile; sn: segment
+        auto issue_s = [&]() -> bool {
+          if (fresh) {
+            if (!bars.wait(bars.at(Bars::kQ), sn & 1)) return false;
+            fresh = false;
+          }
+          if (sj == 0 && !bars.wait(bars.k_full(sT), Bars::k_par(sT))) return false;
+          tc_fence_after();
+          const uint32_t kaddr = sbase + C::kKOff + (sT % C::NK) * C::kTileBytes, scol = tmem + C::kSCol + (su & 1) * KT;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t bd = smem_desc(kaddr + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B);
+            if constexpr (C::QT) {
+              mma_f16_ts(scol, tmem + C::kQCol + sj * (D / 2) + 8u * kk, bd, idS, kk > 0);
+            } else {
+              const uint64_t ad =
+                  smem_desc(sbase + C::kQOff + sj * C::kQBytes + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, kSwizzle128B);
+              mma_bf16(scol, ad, bd, idS, kk > 0);
+            }
+          }
+          mma_commit(bars.at(Bars::kS + (su & 1)));
+          ++su;
+          if (++sj == sg.w) {
+            mma_commit(bars.k_empty(sT));  // this stage's K has been read
+            sj = 0;
+            ++sT;
+            if (++si == sg.t1) {
+              more = ahead.next(sg);
+              si = sg.t0;
+              ++sn;
+              fresh = true;
+            }
+          }
+          return true;
+        };
+        int u = 0, T = 0, n = 0;
+        while (ok && walk.next(pg)) {
+          const int uses = (pg.t1 - pg.t0) * pg.w;
+          // (the first segment's S; later ones' were issued behind the last P V before them)
+          while (more && sn == n && su < u + 2 && (ok = issue_s())) {
+          }
+          for (int i = 0; ok && i < uses; ++i, ++u) {
+            if (!(ok = bars.wait(bars.at(Bars::kP + (u & 1)), (u >> 1) & 1))) break;
+            const bool first_of_tile = pg.w == 1 || !(i & 1), last_of_tile = pg.w == 1 || (i & 1);
+            if (first_of_tile && !(ok = bars.wait(bars.v_full(T), Bars::v_par(T)))) break;
+            tc_fence_after();
+            const uint32_t vaddr = sbase + C::kVOff + (T % C::NV) * C::kTileBytes;
+            const uint32_t pcol = tmem + C::kSCol + (u & 1) * KT + C::kPOff;
+            const uint32_t ocol = tmem + C::kOCol + (NG == 2 ? (u & 1) * D : 0);
+            const bool begins = i < NG;  // this group's first of the segment
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              mma_f16_ts(ocol, pcol + 8u * kk, smem_desc(vaddr + kk * 2048, KT * 128, 1024, kSwizzle128B), idO,
+                         (!begins || kk > 0) ? 1u : 0u);
+            mma_commit(bars.at(Bars::kPV + (u & 1)));
+            if (last_of_tile) {
+              mma_commit(bars.v_empty(T));
+              ++T;
+            }
+            const int upto = i + 1 == uses ? n + 1 : n;  // the next segment's S only behind this one's last P V
+            while (more && sn <= upto && su <= u + 2 && (ok = issue_s())) {
+            }
+          }
+          ++n;
+        }
+        // drain: every product issued by this thread has completed before tensor memory is freed
+        mma_commit(bars.at(Bars::kDrain));
+        rows_wait_in_flight(bars.at(Bars::kDrain), 0, r.err);
+      }
+    } else {
+      // ------------------------------------------------------------ softmax (one thread per row)
+      const int g = warp >> 2, row = tid & 127;
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t tl = tmem + lane_base;
+      typename Src::Row me;  // this thread's row: me.valid, me.out_row (in rows, or -1), what masks and scales it
+      float m2 = -INFINITY, l2 = 0.f;
+      RowSeg sg;
+      // Q of a segment: both groups share the block of an item with one, a half of the channels each
+      auto put_q = [&](const RowSeg& s, int u0) {
+        const int buf = s.w == 2 ? (g ^ u0) & 1 : 0;  // the block that this group's uses are of
+        me.set(p, walk.seq, s.b, s.h, (s.rb + buf) * kBlockRows + row);
+        const uint16_t* src = me.valid ? r.q + s.b * r.qs_b + me.head * r.qs_h + me.pos * r.qs_r : nullptr;
+        me.scale(p, s.h, src);
+        const bool halves = NG == 2 && s.w == 1;
+        const int c_lo = halves ? g * (D / 2) : 0, c_hi = halves ? c_lo + D / 2 : D;
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = src ? *reinterpret_cast<const uint4*>(src + c + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+            w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = me.convert(w[k]);
+          if constexpr (C::QT) {
+            tmem_st_x16(tl + C::kQCol + buf * (D / 2) + c / 2, w);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int ch = c / 8 + k;
+              *reinterpret_cast<uint4*>(smem + C::kQOff + buf * C::kQBytes + (ch >> 3) * 16384 + row * 128 +
+                                        (((ch & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+          }
+        }
+        if constexpr (C::QT) {
+          tmem_wait_st();
+          tc_fence_before();
+        } else {
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.at(Bars::kQ));
+      };
+      int u = 0, nx = 0;  // uses before this segment; exchanges of two states so far
+      bool ok = true;
+      bool any = walk.next(sg);
+      if (any) put_q(sg, 0);
+      while (any) {
+        const int uses = (sg.t1 - sg.t0) * sg.w, w = sg.w;
+        const bool warp_idle = !__any_sync(0xffffffffu, me.valid);
+        m2 = -INFINITY;
+        l2 = 0.f;
+        bool began = false;
+        for (int i = NG == 2 ? (g ^ (u & 1)) : 0; i < uses; i += NG) {
+          const int use = u + i, buf = use & 1, tile = sg.t0 + (w == 2 ? i >> 1 : i);
+          if (!(ok = bars.warp_wait(bars.at(Bars::kS + buf), (use >> 1) & 1))) break;
+          const uint32_t scol = tl + C::kSCol + buf * KT, pcol = scol + C::kPOff;
+          if (warp_idle) {  // (rows of P that nobody uses: whatever is there)
+            if (lane == 0) mbar_arrive(bars.at(Bars::kP + buf));
+            began = true;
+            continue;
+          }
+          tc_fence_after();
+          uint32_t raw[KT];
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) tmem_ld_x32(scol + c, raw + c);
+          tmem_wait_ld();
+          float sv[KT];
+#pragma unroll
+          for (int c = 0; c < KT; ++c) sv[c] = __uint_as_float(raw[c]);
+          me.template mask<KT>(p, walk.seq, tile, sv);
+          float g8[KT / 8];
+#pragma unroll
+          for (int c = 0; c < KT / 8; ++c)
+            g8[c] = max3(max3(sv[8 * c], sv[8 * c + 1], sv[8 * c + 2]), max3(sv[8 * c + 3], sv[8 * c + 4], sv[8 * c + 5]),
+                         fmaxf(sv[8 * c + 6], sv[8 * c + 7]));
+          float rmax = g8[0];
+#pragma unroll
+          for (int c = 1; c + 1 < KT / 8; c += 2) rmax = max3(rmax, g8[c], g8[c + 1]);
+          rmax = fmaxf(rmax, g8[KT / 8 - 1]);
+          const float top = rmax * me.c2;  // (c2 > 0)
+          float f = 1.f;
+          bool rescale = false;
+          if (top > m2 + kTauRows || (m2 == -INFINITY && top > -INFINITY)) {
+            if (l2 > 0.f) {
+              f = ex2_approx(m2 - top);
+              rescale = true;
+            }
+            m2 = top;
+          }
+          // a row that has seen no key yet: its scores are -inf and its weights 0
+          const float nb = m2 == -INFINITY ? 0.f : C::kLift - m2;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < KT / 32; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              rows_p8<C::F16>(sv + 32 * c + 8 * k, me.c2, nb, pk + 4 * k, ps[k & 1], ps[2 + (k & 1)]);
+            tmem_st_x16(pcol + 16u * c, pk);
+          }
+          l2 = l2 * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          if (__any_sync(0xffffffffu, rescale)) {
+            // (two groups: the commit of this S came behind this group's last P V.)  One group: that of the
+            // use before has to land.
+            if (NG == 1 && began && !(ok = bars.warp_wait(bars.at(Bars::kPV + ((use - 1) & 1)), ((use - 1) >> 1) & 1))) break;
+            tc_fence_after();
+            const uint32_t ocol = tl + C::kOCol + (NG == 2 ? g * D : 0);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld_x32(ocol + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+              tmem_st_x16(ocol + c0, o);
+              tmem_st_x16(ocol + c0 + 16, o + 16);
+            }
+          }
+          began = true;
+          tmem_wait_st();  // P (and a rescaled O) in tensor memory before P.V is issued
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.at(Bars::kP + buf));
+        }
+        if (!ok) break;
+        // ---- the next segment's Q, once every S of this one is done; then this one's epilogue
+        const typename Src::Row mine = me;
+        const RowSeg done = sg;
+        const int u_end = u + uses;
+        auto last_of = [&](int buf) { return ((u_end - 1) & 1) == buf ? u_end - 1 : u_end - 2; };
+        bool have[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          have[k] = last_of(k) >= u;
+          if (ok && have[k]) ok = bars.warp_wait(bars.at(Bars::kS + k), (last_of(k) >> 1) & 1);
+        }
+        if (!ok) break;
+        any = walk.next(sg);
+        if (any) {
+          put_q(sg, u_end);
+        }
+        const bool joint = NG == 2 && w == 1;  // the groups' states belong to the same rows
+        float f0 = 1.f, f1 = 0.f;  // of this group's O, and the other's
+        if (joint) {
+          xml[g][row] = make_float2(m2, l2);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.at(Bars::kX));
+          if (!(ok = bars.warp_wait(bars.at(Bars::kX), nx & 1))) break;
+          const float2 y = xml[g ^ 1][row];
+          const float M = fmaxf(m2, y.x);
+          f0 = l2 == 0.f ? 0.f : ex2_approx(m2 - M);  // (a NaN sum goes on to the output)
+          f1 = y.y == 0.f ? 0.f : ex2_approx(y.x - M);
+          l2 = g == 0 ? f0 * l2 + f1 * y.y : f1 * y.y + f0 * l2;
+          m2 = M;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (ok && have[k] && (joint || NG == 1 || k == g))
+            ok = bars.warp_wait(bars.at(Bars::kPV + k), (last_of(k) >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const bool whole = done.t0 == 0 && done.t1 == done.n;
+        const size_t prow = (size_t)(2 * blockIdx.x + (done.t1 == done.n ? 1 : 0)) * r.slot_rows + (w == 2 ? ((g ^ u) & 1) * kBlockRows : 0) + row;
+        const float inv = l2 == 0.f ? 0.f : mine.v_scale / l2;
+        const uint32_t own = tl + C::kOCol + (NG == 2 ? g * D : 0), other = tl + C::kOCol + (NG == 2 ? (g ^ 1) * D : 0);
+        const int c_lo = joint ? g * (D / 2) : 0, c_hi = joint ? c_lo + D / 2 : D;
+        const bool has_own = NG == 1 || have[g], has_other = joint && have[g ^ 1];
+        if (__any_sync(0xffffffffu, mine.out_row >= 0)) {
+#pragma unroll 1
+          for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+            float o[32];
+            {
+              uint32_t x[32];
+              if (has_own) {
+                tmem_ld_x32(own + c0, x);
+                tmem_wait_ld();
+              }
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = has_own && l2 != 0.f && f0 != 0.f ? __uint_as_float(x[c]) * f0 : 0.f;
+              if (has_other) {
+                tmem_ld_x32(other + c0, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (f1 != 0.f) o[c] += __uint_as_float(x[c]) * f1;
+              }
+            }
+            if (mine.out_row >= 0) {
+              if (whole) {
+                uint4* dst = reinterpret_cast<uint4*>(r.out + (size_t)mine.out_row * D + c0);
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                  uint4 y;
+                  uint32_t* yw = &y.x;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    yw[e] = pack2<Src::kOutF16>(o[o_column<Src>(c + 2 * e)] * inv, o[o_column<Src>(c + 2 * e + 1)] * inv);
+                  dst[c / 8] = y;
+                }
+              } else {
+                float4* dst = reinterpret_cast<float4*>(r.part_o + prow * D + c0);
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                  dst[c / 4] = make_float4(o[o_column<Src>(c)], o[o_column<Src>(c + 1)], o[o_column<Src>(c + 2)],
+                                           o[o_column<Src>(c + 3)]);
+              }
+            }
+          }
+          if (mine.out_row >= 0 && (!joint || g == 0)) {
+            if (!whole)
+              r.part_ml[prow] = make_float2(m2, l2);
+            else if (r.lse)
+              r.lse[mine.out_row] = l2 == 0.f ? -INFINITY : kLn2 * (m2 - C::kLift + log2f(l2));
+          }
+        }
+        if (joint) {  // no P of the next segment before both groups have read both states
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.at(Bars::kXDone));
+          if (!(ok = bars.warp_wait(bars.at(Bars::kXDone), nx & 1))) break;
+          ++nx;
+        }
+        u = u_end;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.x of the first kernel and goes on behind it,
+// in order: a warp per row, a vector of channels per lane.
+constexpr int kRowJoinThreads = 256;
+template <class Src>
+__global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid_constant__ typename Src::Params p, int ctas) {
+  using C = typename Src::Cfg;
+  constexpr int D = C::D;
+  constexpr int kVec = D / 32 < 4 ? D / 32 : 4, kVecs = D / (32 * kVec);  // a lane's channels: kVecs vectors
+  const RowParams& r = p.r;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * (kRowJoinThreads / 32) + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SplitRec rec = r.rec[blockIdx.x];
+  if (rec.n == 0 || row >= rec.w * kBlockRows) return;
+  const typename Src::Seq seq(p, rec.b);
+  typename Src::Row me;
+  me.set(p, seq, rec.b, rec.h, rec.rb * kBlockRows + row);
+  if (me.out_row < 0) return;
+  const RowCut cut(rec.total, cut_ctas(rec.total, ctas));
+  const long long end = rec.first + (long long)rec.n * rec.w;
+  // the tiles t0 .. t1-1 of CTA c
+  auto tiles_of = [&](int c, int& t0, int& t1) {
+    const long long a = cut.first(c) - rec.first, e = cut.first(c + 1) - rec.first;
+    t0 = a <= 0 ? 0 : (int)((a < end - rec.first ? a : end - rec.first) / rec.w);
+    t1 = (int)((e < end - rec.first ? e : end - rec.first) / rec.w);
+  };
+  float acc[kVecs][kVec], M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[v][k] = 0.f;
+  for (int c0 = blockIdx.x; cut.first(c0) < end; c0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    int t0 = 0, t1 = 0;
+    size_t prow = 0;
+    if (cut.first(c0 + lane) < end) tiles_of(c0 + lane, t0, t1);
+    if (__any_sync(0xffffffffu, t0 == 0 && t1 == rec.n)) return;  // one CTA has it all, and wrote it
+    if (t1 > t0) {
+      prow = (size_t)(2 * (c0 + lane) + (t1 == rec.n ? 1 : 0)) * r.slot_rows + row;
+      ml = r.part_ml[prow];
+    }
+    float mx = fmaxf(M, ml.x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const float fo = L == 0.f ? 0.f : ex2_approx(M - mx);
+    const float f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);  // (a NaN sum goes on to the output)
+    M = mx;
+    L *= fo;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) acc[v][k] *= fo;
+    const int here = min(32, ctas - c0);
+#pragma unroll 8
+    for (int i = 0; i < here; ++i) {  // (the loads do not wait for the weights; a part without weight may hold anything)
+      const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, ml.y, i);
+      const float* src = r.part_o + __shfl_sync(0xffffffffu, prow, i) * D;
+      L = fi == 0.f ? L : fmaf(fi, li, L);
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        float y[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; k += 2) {
+          const float2 z = *reinterpret_cast<const float2*>(src + (32 * v + lane) * kVec + k);
+          y[k] = z.x;
+          y[k + 1] = z.y;
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) acc[v][k] = fi == 0.f ? acc[v][k] : fmaf(fi, y[k], acc[v][k]);
+      }
+    }
+  }
+  me.scale_v(p, rec.h);
+  const float inv = L == 0.f ? 0.f : me.v_scale / L;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(r.out + (size_t)me.out_row * D + (32 * v + lane) * kVec);
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) dst[k / 2] = pack2<Src::kOutF16>(acc[v][k] * inv, acc[v][k + 1] * inv);
+  }
+  if (lane == 0 && r.lse) r.lse[me.out_row] = L == 0.f ? -INFINITY : kLn2 * (M - C::kLift + log2f(L));
+}
+
+__host__ inline size_t rows_align(size_t x) { return (x + 255) / 256 * 256; }
+// Rows of a part's slot: those of the largest item.
+__host__ inline int rows_slot(int rows, int d) { return d <= 128 && rows > kBlockRows ? 2 * kBlockRows : kBlockRows; }
+__host__ inline size_t rows_workspace(int rows, int d) {
+  const size_t slots = 2 * (size_t)kRowCtas * rows_slot(rows, d);
+  return rows_align(kRowCtas * sizeof(SplitRec)) + rows_align(slots * 8) + slots * d * 4;
+}
+// What the sources' entry points take alike.
+__host__ inline bool rows_bad_heads(int B, int Hq, int Hkv, int Nq) {
+  return B < 1 || B > kMaxRowSeqs || Hq < 1 || Hkv < 1 || Hq % Hkv || Hkv > (1 << 16) || Nq < 1 ||
+         (long long)(Hq / Hkv) * Nq > (1 << 20) || (long long)B * Hq * Nq > 0x7FFFFFF0;
+}
+
+template <class Src>
+cudaError_t launch_rows(typename Src::Params prm, void* ws, cudaStream_t stream) {
+  RowParams& r = prm.r;
+  const int rows = r.G() * r.Nq, D = Src::Cfg::D;
+  r.slot_rows = rows_slot(rows, D);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const size_t slots = 2 * (size_t)kRowCtas * r.slot_rows;
+  r.rec = (SplitRec*)w;
+  w += rows_align(kRowCtas * sizeof(SplitRec));
+  r.part_ml = (float2*)w;
+  w += rows_align(slots * 8);
+  r.part_o = (float*)w;
+  static std::atomic<uint64_t> ready{0};  // the attribute, once per device (a bit each)
+  cudaError_t e;
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev))) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || !(ready.load() & bit)) {
+    if ((e = cudaFuncSetAttribute(rows_kernel<Src>, cudaFuncAttributeMaxDynamicSharedMemorySize, Src::kSmem))) return e;
+    if (dev <= 63) ready.fetch_or(bit);
+  }
+  rows_kernel<Src><<<kRowCtas, Src::kThreads, Src::kSmem, stream>>>(prm);
+  if ((e = cudaGetLastError())) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kRowCtas, (unsigned)((r.slot_rows < rows ? r.slot_rows : rows) + 7) / 8);
+  cfg.blockDim = dim3(kRowJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rows_join_kernel<Src>, prm, kRowCtas);
+}
+
+}  // namespace
+}  // namespace apa
