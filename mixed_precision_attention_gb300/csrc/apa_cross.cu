@@ -18,26 +18,25 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-#ifndef APA_CROSS_SS
-#define APA_CROSS_SS 0
-#endif
 template <int D, bool F16>
-using CrossCfg = std::conditional_t<D == 64, RowCfg<64, 128, true, 5, 5, F16>,
-                                    std::conditional_t<D == 128,
-                                                       std::conditional_t<APA_CROSS_SS, RowCfg<128, 128, false, 2, 2, F16>,
-                                                                          RowCfg<128, 64, true, 5, 5, F16>>,
-                                                       RowCfg<256, 64, true, 3, 3, F16>>>;
+struct CrossPick;
+template <bool F16>
+struct CrossPick<64, F16> { using Cfg = RowCfg<64, 64, 2, true, 8, 8, F16>; };
+template <bool F16>
+struct CrossPick<128, F16> { using Cfg = RowCfg<128, 64, 2, false, 4, 4, F16>; };
+template <bool F16>
+struct CrossPick<256, F16> { using Cfg = RowCfg<256, 64, 2, true, 3, 3, F16>; };
 
 template <int D, bool F16>
 struct CrossSrc {
-  using Cfg = CrossCfg<D, F16>;
-  static constexpr int kSrcWarps = 2, kThreads = (Cfg::kSoftWarps + 1 + kSrcWarps) * 32;
+  using Cfg = typename CrossPick<D, F16>::Cfg;
+  static constexpr int kSrcWarps = 2, kThreads = (Cfg::kSrcWarp + kSrcWarps) * 32;
   static constexpr int kKArrivals = 1, kVArrivals = 1;
   static constexpr int kBars = Cfg::NV;  // per stage of V: a last tile has landed, values behind the end and all
   static __device__ __forceinline__ uint32_t bar_count(int) { return 1; }
   static constexpr bool kPairedV = false, kOutF16 = F16;
   static constexpr int kSmem = Cfg::kSrcOff + 1024;
-  static_assert(kSmem <= 232448 - 2048, "shared memory");
+  static_assert(kSmem <= 232448 - 4096, "shared memory");
 
   struct Params {
     RowParams r;

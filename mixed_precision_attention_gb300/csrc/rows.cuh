@@ -13,14 +13,14 @@
 // is written out at once; the states (m, l, O) of the others go to the workspace and a
 // second kernel joins them in order, so results do not depend on timing.
 //
-// Inside a CTA use u goes through buffer u % 2 of the scores in tensor memory, and (d <= 128)
-// through softmax group u % 2, four warps with one thread per row: either the two blocks of
-// an item against the same tile, or one block against two tiles in turn, whose two
-// states are then joined over tensor memory.  One thread issues every product, in the order
-// P V of use u, S of use u + 2: the products execute in that order, so S may go over the P
-// that lies in its columns, and the commit of S says that P V before it is done.  While one
-// group works on its scores the tensor cores have the other's S and P V.
-// At d = 256 O takes half of tensor memory: one group, which alternates between the buffers.
+// Inside a CTA (d <= 128) there are two softmax groups, four warps each with one thread per
+// row, and a warp for each that issues its products: either the two blocks of an item
+// against the same tiles, or one block against every other tile each, whose two states are
+// then joined over tensor memory.  A group's issuer runs through P V of use i, S of use
+// i + NB: those products execute in that order, so S may go over the P that lies in its
+// columns, and the commit of S says that the P V before it is done.  While a group works on
+// its scores the tensor cores have the other's products and, with NB = 2 buffers of S, its
+// own next S.  At d = 256 O takes half of tensor memory: one group.
 //
 // Q is an operand in tensor memory where it fits (kQT): S = Q K^T of 64 keys would otherwise
 // read 6 KB of shared memory per 32 cycles of product, 1.5 times what it delivers.
@@ -79,27 +79,40 @@ struct RowParams {
   __host__ __device__ int G() const { return Hq / Hkv; }
 };
 
-template <int D_, int KT_, bool QT_, int NK_, int NV_, bool F16_>
+template <int D_, int KT_, int NB_, bool QT_, int NK_, int NV_, bool F16_>
 struct RowCfg {
-  static constexpr int D = D_, KT = KT_;
+  static constexpr int D = D_, KT = KT_, NB = NB_;
   static constexpr bool QT = QT_, F16 = F16_;
   static constexpr int NK = NK_, NV = NV_;
   static constexpr int NG = D <= 128 ? 2 : 1;
   static constexpr int kBlocks = NG;  // row blocks of an item, at most
   static constexpr int kTileBytes = KT * D * 2;
   static constexpr int kQBytes = QT ? 0 : 128 * D * 2;  // per block
-  static constexpr uint32_t kOCol = 0, kSCol = NG * D, kQCol = NG * D + 2 * KT;
+  static constexpr uint32_t kOCol = 0, kSCol = NG * D, kQCol = kSCol + NG * NB * KT;  // S: NB buffers per group
   static constexpr uint32_t kPOff = KT / 2;  // P, two keys per column, in the upper half of its S
   static constexpr int kQOff = 0, kKOff = NG * kQBytes, kVOff = kKOff + NK * kTileBytes;
   static constexpr int kSrcOff = kVOff + NV * kTileBytes;  // the source's own
-  static constexpr int kSoftWarps = 4 * NG, kMmaWarp = kSoftWarps, kSrcWarp = kSoftWarps + 1;
+  static constexpr int kSoftWarps = 4 * NG, kMmaWarp = kSoftWarps, kSrcWarp = kSoftWarps + NG;
   static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
+  static_assert(NG == 1 || (NK % 2 == 0 && NV % 2 == 0), "RowShare");
   static_assert(kQCol + (QT ? NG * D / 2 : 0) <= 512, "tensor memory");
 };
 
 // A CTA's run of tiles t0 .. t1-1 (of n) of one item: blocks rb .. rb+w-1 of head h of sequence b.
 struct RowSeg {
   int b, h, rb, w, t0, t1, n;
+};
+// A group's uses of a segment with T tiles before it in the CTA: all its tiles, or (two groups, one block) those with
+// the group's parity in the CTA's count.  The rings have an even number of stages then, so that such a tile's stage
+// is its group's: nobody skips a phase of a barrier that it waits for within the segment.
+struct RowShare {
+  int first, step, uses;
+  __device__ __forceinline__ RowShare(int NG, int w, int tiles, int g, int T) {
+    step = NG == 2 && w == 1 ? 2 : 1;
+    first = step == 2 ? (g ^ T) & 1 : 0;
+    uses = (tiles - first + step - 1) / step;
+  }
+  __device__ __forceinline__ int tile(int i) const { return first + step * i; }  // counted from the segment's first
 };
 // The segments of a CTA in order; seq: the source's numbers of the last one's sequence.
 template <class Src, int kBlocks>
@@ -136,6 +149,17 @@ struct RowWalk {
     return false;
   }
 };
+
+// One lane of a warp that is together.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(e));
+  return e != 0;
+}
 
 // used only while unwinding: waits for copies and products already in flight, ignoring the abort flag
 __device__ __forceinline__ void rows_wait_in_flight(uint32_t bar, uint32_t parity, int* err) {
@@ -174,13 +198,14 @@ __device__ __forceinline__ void rows_p8(const float* x, float c2, float nb, uint
   asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(s));
 }
 
-// Barriers of the core (the source's follow): K and V rings, S, P, P.V per buffer, Q, the exchange of two
-// groups' states and its end, and the issuer's drain.
+// Barriers of the core (the source's follow): K and V rings, S and P per buffer, a segment's last P.V and the
+// last but one per group, Q there and read, the exchange of
+// two groups' states and its end, and the issuers' drains.
 template <class C>
 struct RowBars {
   static constexpr int kKFull = 0, kKEmpty = C::NK, kVFull = 2 * C::NK, kVEmpty = 2 * C::NK + C::NV;
-  static constexpr int kS = 2 * C::NK + 2 * C::NV, kP = kS + 2, kPV = kS + 4, kQ = kS + 6, kX = kS + 7, kXDone = kS + 8,
-                       kDrain = kS + 9, kNum = kS + 10;
+  static constexpr int kBufs = C::NG * C::NB, kS = 2 * C::NK + 2 * C::NV, kP = kS + kBufs, kPV = kP + kBufs, kPV2 = kPV + C::NG, kQ = kPV2 + C::NG,
+                       kQFree = kQ + 1, kX = kQ + 2, kXDone = kX + 1, kDrain = kXDone + 1, kNum = kDrain + C::NG;
   uint32_t bar0;
   volatile int* abort;
   int* err;
@@ -231,7 +256,9 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
       uint32_t count = 1;
       if (i < Bars::kKEmpty) count = Src::kKArrivals;
       if (i >= Bars::kVFull && i < Bars::kVEmpty) count = Src::kVArrivals;
-      if (i == Bars::kP || i == Bars::kP + 1) count = 4;
+      if ((i >= Bars::kKEmpty && i < Bars::kVFull) || (i >= Bars::kVEmpty && i < Bars::kS)) count = NG;
+      if (i >= Bars::kP && i < Bars::kPV) count = 4;
+      if (i == Bars::kQFree) count = 2 * NG;  // a lane of each group, and its issuer
       if (i == Bars::kQ || i == Bars::kX || i == Bars::kXDone) count = C::kSoftWarps;
       mbar_init(bars.at(i), count);
     }
@@ -345,84 +372,84 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
     RowWalk<Src, C::kBlocks> walk(p, sb, sitem, spos, (int)(x1 - x0));
     if (warp >= C::kSrcWarp) {
       Src::produce(p, walk, smem, sbase, bars, warp - C::kSrcWarp, lane);
-    } else if (warp == C::kMmaWarp) {
-      // ------------------------------------------------------------ the products' issuer
-      if (lane == 0) {
-        constexpr uint32_t idS = C::F16 ? idesc_f16(128, KT, 0) : idesc_bf16(128, KT, 0);
-        constexpr uint32_t idO = C::F16 ? idesc_f16(128, D, 1) : idesc_bf16(128, D, 1);
-        RowWalk<Src, C::kBlocks> ahead = walk;
-        // the next use to get its S: use su, of tile st0 + si of segment sn (sg), the first of its segment if sfresh
-        RowSeg sg{}, pg{};
-        bool more = ahead.next(sg), ok = true, fresh = true;
-        int su = 0, sT = 0, si = sg.t0, sj = 0, sn = 0;  // sj: block within the tile; sn: segment
-        auto issue_s = [&]() -> bool {
-          if (fresh) {
-            if (!bars.wait(bars.at(Bars::kQ), sn & 1)) return false;
-            fresh = false;
-          }
-          if (sj == 0 && !bars.wait(bars.k_full(sT), Bars::k_par(sT))) return false;
-          tc_fence_after();
-          const uint32_t kaddr = sbase + C::kKOff + (sT % C::NK) * C::kTileBytes, scol = tmem + C::kSCol + (su & 1) * KT;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t bd = smem_desc(kaddr + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B);
-            if constexpr (C::QT) {
-              mma_f16_ts(scol, tmem + C::kQCol + sj * (D / 2) + 8u * kk, bd, idS, kk > 0);
-            } else {
-              const uint64_t ad =
-                  smem_desc(sbase + C::kQOff + sj * C::kQBytes + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, kSwizzle128B);
-              mma_bf16(scol, ad, bd, idS, kk > 0);
-            }
-          }
-          mma_commit(bars.at(Bars::kS + (su & 1)));
-          ++su;
-          if (++sj == sg.w) {
-            mma_commit(bars.k_empty(sT));  // this stage's K has been read
-            sj = 0;
-            ++sT;
-            if (++si == sg.t1) {
-              more = ahead.next(sg);
-              si = sg.t0;
-              ++sn;
-              fresh = true;
-            }
-          }
-          return true;
-        };
-        int u = 0, T = 0, n = 0;
-        while (ok && walk.next(pg)) {
-          const int uses = (pg.t1 - pg.t0) * pg.w;
-          // (the first segment's S; later ones' were issued behind the last P V before them)
-          while (more && sn == n && su < u + 2 && (ok = issue_s())) {
-          }
-          for (int i = 0; ok && i < uses; ++i, ++u) {
-            if (!(ok = bars.wait(bars.at(Bars::kP + (u & 1)), (u >> 1) & 1))) break;
-            const bool first_of_tile = pg.w == 1 || !(i & 1), last_of_tile = pg.w == 1 || (i & 1);
-            if (first_of_tile && !(ok = bars.wait(bars.v_full(T), Bars::v_par(T)))) break;
+    } else if (warp >= C::kMmaWarp) {
+      // ------------------------------------------------------------ a group's issuer
+      // The warp stays together and one lane issues: what the products take is the same in all lanes and so
+      // in uniform registers.
+      constexpr uint32_t idS = C::F16 ? idesc_f16(128, KT, 0) : idesc_bf16(128, KT, 0);
+      constexpr uint32_t idO = C::F16 ? idesc_f16(128, D, 1) : idesc_bf16(128, D, 1);
+      const int g = __shfl_sync(0xffffffffu, warp, 0) - C::kMmaWarp;
+      const bool elected = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ocol = tm + C::kOCol + g * D;
+      const uint64_t qd0 = smem_desc(sbase + C::kQOff, 16, 1024, kSwizzle128B);
+      const uint64_t kd0 = smem_desc(sbase + C::kKOff, 16, 1024, kSwizzle128B);
+      const uint64_t vd0 = smem_desc(sbase + C::kVOff, KT * 128, 1024, kSwizzle128B);
+      uint32_t T = 0, n = 0, qpar = 0;  // tiles before the segment; this group's uses before it
+      RowSeg sg;
+      bool ok = true;
+      while (ok && __any_sync(0xffffffffu, walk.next(sg))) {
+        const int w = __shfl_sync(0xffffffffu, sg.w, 0), tiles = __shfl_sync(0xffffffffu, sg.t1 - sg.t0, 0);
+        const RowShare mine(NG, w, tiles, g, T);
+        if (!(ok = bars.warp_wait(bars.at(Bars::kQ), qpar))) break;
+        qpar ^= 1;
+        // (an issuer without a use in the segment has to have seen its Q, too, before the next one comes)
+        if (NG == 2 && elected) mbar_arrive(bars.at(Bars::kQFree));
+        const bool alone = NG == 2 && w == 1;  // (a tile that the other group has no part in counts twice)
+        const uint32_t blk = w == 2 ? g : 0, qcol = tm + C::kQCol + blk * (D / 2);
+        const uint64_t qd = qd0 + blk * (C::kQBytes >> 4);
+        // P V of use i, then S of use i + NB, in whose columns that P lies: its commit says as well that this P V is done.
+        for (int i = -C::NB; i < mine.uses; ++i) {
+          const int j = i + C::NB;
+          const uint32_t buf = (n + j) % C::NB;
+          const uint32_t scol = tm + C::kSCol + (g * C::NB + buf) * KT;
+          if (i >= 0) {
+            const uint32_t t = T + mine.tile(i), st = t % C::NV;
+            // (P first: it comes behind the end of the last segment, when all of V there has been read)
+            if (!(ok = bars.warp_wait(bars.at(Bars::kP + g * C::NB + buf), ((n + i) / C::NB) & 1))) break;
+            if (!(ok = bars.warp_wait(bars.v_full(t), Bars::v_par(t)))) break;
             tc_fence_after();
-            const uint32_t vaddr = sbase + C::kVOff + (T % C::NV) * C::kTileBytes;
-            const uint32_t pcol = tmem + C::kSCol + (u & 1) * KT + C::kPOff;
-            const uint32_t ocol = tmem + C::kOCol + (NG == 2 ? (u & 1) * D : 0);
-            const bool begins = i < NG;  // this group's first of the segment
+            const uint64_t vd = vd0 + st * (C::kTileBytes >> 4);
+            if (elected) {
+              mma_f16_ts(ocol, scol + C::kPOff, vd, idO, i > 0 ? 1u : 0u);  // (the first of the segment starts O anew)
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              mma_f16_ts(ocol, pcol + 8u * kk, smem_desc(vaddr + kk * 2048, KT * 128, 1024, kSwizzle128B), idO,
-                         (!begins || kk > 0) ? 1u : 0u);
-            mma_commit(bars.at(Bars::kPV + (u & 1)));
-            if (last_of_tile) {
-              mma_commit(bars.v_empty(T));
-              ++T;
+              for (int kk = 1; kk < KT / 16; ++kk)
+                mma_f16_ts(ocol, scol + C::kPOff + 8u * kk, vd + kk * (2048 >> 4), idO, 1u);
+              if (j >= mine.uses) mma_commit(bars.at((i + 1 == mine.uses ? Bars::kPV : Bars::kPV2) + g));
+              mma_commit(bars.v_empty(t));
+              if (alone) mma_commit(bars.v_empty(t));
             }
-            const int upto = i + 1 == uses ? n + 1 : n;  // the next segment's S only behind this one's last P V
-            while (more && sn <= upto && su <= u + 2 && (ok = issue_s())) {
-            }
+            __syncwarp();
           }
-          ++n;
+          if (j < mine.uses) {
+            const uint32_t t = T + mine.tile(j), st = t % C::NK;
+            if (!(ok = bars.warp_wait(bars.k_full(t), Bars::k_par(t)))) break;
+            tc_fence_after();
+            const uint64_t kd = kd0 + st * (C::kTileBytes >> 4);
+            if (elected) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t bd = kd + (((kk >> 2) * (KT * 128) + (kk & 3) * 32) >> 4);
+                if constexpr (C::QT)
+                  mma_f16_ts(scol, qcol + 8u * kk, bd, idS, kk > 0);
+                else
+                  mma_bf16(scol, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), bd, idS, kk > 0);
+              }
+              mma_commit(bars.at(Bars::kS + g * C::NB + buf));
+              mma_commit(bars.k_empty(t));
+              if (alone) mma_commit(bars.k_empty(t));
+            }
+            __syncwarp();
+          }
         }
-        // drain: every product issued by this thread has completed before tensor memory is freed
-        mma_commit(bars.at(Bars::kDrain));
-        rows_wait_in_flight(bars.at(Bars::kDrain), 0, r.err);
+        T += tiles;
+        n += mine.uses;
       }
+      // drain: every product issued by this thread has completed before tensor memory is freed
+      if (elected) {
+        mma_commit(bars.at(Bars::kDrain + g));
+        rows_wait_in_flight(bars.at(Bars::kDrain + g), 0, r.err);
+      }
+      __syncwarp();
     } else {
       // ------------------------------------------------------------ softmax (one thread per row)
       const int g = warp >> 2, row = tid & 127;
@@ -432,8 +459,8 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
       float m2 = -INFINITY, l2 = 0.f;
       RowSeg sg;
       // Q of a segment: both groups share the block of an item with one, a half of the channels each
-      auto put_q = [&](const RowSeg& s, int u0) {
-        const int buf = s.w == 2 ? (g ^ u0) & 1 : 0;  // the block that this group's uses are of
+      auto put_q = [&](const RowSeg& s) {
+        const int buf = s.w == 2 ? g : 0;  // the block that this group's uses are of
         me.set(p, walk.seq, s.b, s.h, (s.rb + buf) * kBlockRows + row);
         const uint16_t* src = me.valid ? r.q + s.b * r.qs_b + me.head * r.qs_h + me.pos * r.qs_r : nullptr;
         me.scale(p, s.h, src);
@@ -470,23 +497,23 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.at(Bars::kQ));
       };
-      int u = 0, nx = 0;  // uses before this segment; exchanges of two states so far
+      // before the segment: tiles, each group's uses and commits of P V; exchanges of two states, segments
+      int T = 0, n[2] = {0, 0}, npv[2] = {0, 0}, npv2 = 0, nx = 0, nseg = 0;
       bool ok = true;
       bool any = walk.next(sg);
-      if (any) put_q(sg, 0);
+      if (any) put_q(sg);
       while (any) {
-        const int uses = (sg.t1 - sg.t0) * sg.w, w = sg.w;
+        const int tiles = sg.t1 - sg.t0, w = sg.w;
+        const RowShare share(NG, w, tiles, g, T);
         const bool warp_idle = !__any_sync(0xffffffffu, me.valid);
         m2 = -INFINITY;
         l2 = 0.f;
-        bool began = false;
-        for (int i = NG == 2 ? (g ^ (u & 1)) : 0; i < uses; i += NG) {
-          const int use = u + i, buf = use & 1, tile = sg.t0 + (w == 2 ? i >> 1 : i);
-          if (!(ok = bars.warp_wait(bars.at(Bars::kS + buf), (use >> 1) & 1))) break;
-          const uint32_t scol = tl + C::kSCol + buf * KT, pcol = scol + C::kPOff;
+        for (int i = 0; i < share.uses; ++i) {
+          const int v = n[g] + i, buf = v % C::NB, tile = sg.t0 + share.tile(i);
+          if (!(ok = bars.warp_wait(bars.at(Bars::kS + g * C::NB + buf), (v / C::NB) & 1))) break;
+          const uint32_t scol = tl + C::kSCol + (g * C::NB + buf) * KT, pcol = scol + C::kPOff;
           if (warp_idle) {  // (rows of P that nobody uses: whatever is there)
-            if (lane == 0) mbar_arrive(bars.at(Bars::kP + buf));
-            began = true;
+            if (lane == 0) mbar_arrive(bars.at(Bars::kP + g * C::NB + buf));
             continue;
           }
           tc_fence_after();
@@ -530,11 +557,15 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
           }
           l2 = l2 * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
           if (__any_sync(0xffffffffu, rescale)) {
-            // (two groups: the commit of this S came behind this group's last P V.)  One group: that of the
-            // use before has to land.
-            if (NG == 1 && began && !(ok = bars.warp_wait(bars.at(Bars::kPV + ((use - 1) & 1)), ((use - 1) >> 1) & 1))) break;
+            // This S came behind P V of use i - NB.  With two buffers, that of use i - 1 has to land: the S behind it
+            // says so, or its own commit.
+            if (C::NB == 2 && i > 0) {
+              if (!(ok = i + 1 < share.uses ? bars.warp_wait(bars.at(Bars::kS + g * C::NB + (buf ^ 1)), ((v + 1) / C::NB) & 1)
+                                            : bars.warp_wait(bars.at(Bars::kPV2 + g), npv2 & 1)))
+                break;
+            }
             tc_fence_after();
-            const uint32_t ocol = tl + C::kOCol + (NG == 2 ? g * D : 0);
+            const uint32_t ocol = tl + C::kOCol + g * D;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t o[32];
@@ -546,28 +577,26 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
               tmem_st_x16(ocol + c0 + 16, o + 16);
             }
           }
-          began = true;
           tmem_wait_st();  // P (and a rescaled O) in tensor memory before P.V is issued
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars.at(Bars::kP + buf));
+          if (lane == 0) mbar_arrive(bars.at(Bars::kP + g * C::NB + buf));
         }
         if (!ok) break;
         // ---- the next segment's Q, once every S of this one is done; then this one's epilogue
         const typename Src::Row mine = me;
         const RowSeg done = sg;
-        const int u_end = u + uses;
-        auto last_of = [&](int buf) { return ((u_end - 1) & 1) == buf ? u_end - 1 : u_end - 2; };
-        bool have[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          have[k] = last_of(k) >= u;
-          if (ok && have[k]) ok = bars.warp_wait(bars.at(Bars::kS + k), (last_of(k) >> 1) & 1);
+        if (NG == 2) {
+          if ((warp & 3) == 0 && lane == 0) mbar_arrive(bars.at(Bars::kQFree));
+          if (!(ok = bars.warp_wait(bars.at(Bars::kQFree), nseg & 1))) break;
         }
-        if (!ok) break;
+        ++nseg;
+        int uses[2];
+#pragma unroll
+        for (int k = 0; k < NG; ++k) uses[k] = RowShare(NG, w, tiles, k, T).uses;
         any = walk.next(sg);
         if (any) {
-          put_q(sg, u_end);
+          put_q(sg);
         }
         const bool joint = NG == 2 && w == 1;  // the groups' states belong to the same rows
         float f0 = 1.f, f1 = 0.f;  // of this group's O, and the other's
@@ -584,17 +613,20 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
           m2 = M;
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (ok && have[k] && (joint || NG == 1 || k == g))
-            ok = bars.warp_wait(bars.at(Bars::kPV + k), (last_of(k) >> 1) & 1);
+        for (int k = 0; k < NG; ++k) {
+          if (ok && uses[k] > 0 && (joint || k == g)) ok = bars.warp_wait(bars.at(Bars::kPV + k), npv[k] & 1);
+          npv[k] += uses[k] > 0;
+          n[k] += uses[k];
+        }
+        npv2 += C::NB == 2 && share.uses > 1;
         if (!ok) break;
         tc_fence_after();
         const bool whole = done.t0 == 0 && done.t1 == done.n;
-        const size_t prow = (size_t)(2 * blockIdx.x + (done.t1 == done.n ? 1 : 0)) * r.slot_rows + (w == 2 ? ((g ^ u) & 1) * kBlockRows : 0) + row;
+        const size_t prow = (size_t)(2 * blockIdx.x + (done.t1 == done.n ? 1 : 0)) * r.slot_rows + (w == 2 ? g * kBlockRows : 0) + row;
         const float inv = l2 == 0.f ? 0.f : mine.v_scale / l2;
-        const uint32_t own = tl + C::kOCol + (NG == 2 ? g * D : 0), other = tl + C::kOCol + (NG == 2 ? (g ^ 1) * D : 0);
+        const uint32_t own = tl + C::kOCol + g * D, other = tl + C::kOCol + (NG == 2 ? (g ^ 1) * D : 0);
         const int c_lo = joint ? g * (D / 2) : 0, c_hi = joint ? c_lo + D / 2 : D;
-        const bool has_own = NG == 1 || have[g], has_other = joint && have[g ^ 1];
+        const bool has_own = share.uses > 0, has_other = joint && uses[NG - 1 - g] > 0;
         if (__any_sync(0xffffffffu, mine.out_row >= 0)) {
 #pragma unroll 1
           for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
@@ -650,7 +682,7 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
           if (!(ok = bars.warp_wait(bars.at(Bars::kXDone), nx & 1))) break;
           ++nx;
         }
-        u = u_end;
+        T += tiles;
       }
     }
   }
@@ -714,7 +746,7 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
       for (int k = 0; k < kVec; ++k) acc[v][k] *= fo;
-    const int here = min(32, ctas - c0);
+    const int here = __popc(__ballot_sync(0xffffffffu, cut.first(c0 + lane) < end));
 #pragma unroll 8
     for (int i = 0; i < here; ++i) {  // (the loads do not wait for the weights; a part without weight may hold anything)
       const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, ml.y, i);

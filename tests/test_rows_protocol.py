@@ -25,25 +25,32 @@ class Bar:
 
 
 class Machine:
-    def __init__(self, segs, NG, NK, NV, rng, drop=None):
+    def __init__(self, segs, NG, NB, NK, NV, rng, drop=None):
         """segs: (tiles, blocks of the item) of each segment."""
-        self.segs, self.NG, self.NK, self.NV, self.rng, self.drop = segs, NG, NK, NV, rng, drop
+        self.segs, self.NG, self.NB, self.NK, self.NV, self.rng, self.drop = segs, NG, NB, NK, NV, rng, drop
         W = self.W = 4 * NG
-        self.kf, self.ke = [Bar(1) for _ in range(NK)], [Bar(1) for _ in range(NK)]
-        self.vf, self.ve = [Bar(1) for _ in range(NV)], [Bar(1) for _ in range(NV)]
-        self.s, self.p, self.pv = [Bar(1), Bar(1)], [Bar(4), Bar(4)], [Bar(1), Bar(1)]
-        self.q, self.x, self.xd = Bar(W), Bar(W), Bar(W)
+        self.kf, self.ke = [Bar(1) for _ in range(NK)], [Bar(NG) for _ in range(NK)]
+        self.vf, self.ve = [Bar(1) for _ in range(NV)], [Bar(NG) for _ in range(NV)]
+        self.s, self.p = ([[Bar(c) for _ in range(NB)] for _ in range(NG)] for c in (1, 4))
+        self.pv, self.pv2 = [Bar(1) for _ in range(NG)], [Bar(1) for _ in range(NG)]
+        self.q, self.qfree, self.x, self.xd = Bar(W), Bar(2 * NG), Bar(W), Bar(W)
+        self.bars = [*self.kf, *self.ke, *self.vf, *self.ve, *sum(self.s, []), *sum(self.p, []), *self.pv, *self.pv2, self.q,
+                     self.qfree, self.x, self.xd]
         self.K, self.V = [None] * NK, [None] * NV
-        self.S = [None, None]                       # use whose scores are there
-        self.P = [[None] * 4, [None] * 4]           # per warp of a group: use
-        self.Q = [[None] * W, [None] * W]           # per block: the segment that each warp stored
-        self.O = [[], []]                           # per group: the uses summed up in it
-        self.queue = []                             # products and commits in flight
-        self.seen = []                              # what the epilogues read
+        self.S = [[None] * NB for _ in range(NG)]               # the group's use whose scores are there
+        self.P = [[[None] * 4 for _ in range(NB)] for _ in range(NG)]  # per warp of a group: use
+        self.Q = [[None] * W, [None] * W]                       # per block: the segment that each warp stored
+        self.O = [[] for _ in range(NG)]                        # per group: the uses summed up in it
+        self.queue = [[] for _ in range(NG)]                    # products and commits in flight, per issuer
+        self.X = [[None] * 4, [None] * 4]
+        self.seen = []                                          # what the epilogues read
 
-    # ---- products, executed in order
-    def execute(self):
-        kind, *a = self.queue.pop(0)
+    def share(self, w, tiles, g, T):
+        return range((g ^ T) & 1, tiles, 2) if self.NG == 2 and w == 1 else range(tiles)
+
+    # ---- an issuer's products, executed in its order
+    def execute(self, g):
+        kind, *a = self.queue[g].pop(0)
         if kind == "commit":
             a[0].arrive()
         elif kind == "S":
@@ -51,11 +58,11 @@ class Machine:
             assert self.K[T % self.NK] == T, "S reads another tile's K"
             for w in warps:
                 assert self.Q[blk][w] == seg, "S reads another segment's Q"
-            self.S[use & 1] = use
-            self.P[use & 1] = [None] * 4            # they share columns
+            self.S[g][use % self.NB] = use
+            self.P[g][use % self.NB] = [None] * 4               # they share columns
         else:
-            use, T, g, first = a
-            assert self.P[use & 1] == [use] * 4, "P V reads another use's P"
+            use, T, first = a
+            assert self.P[g][use % self.NB] == [use] * 4, "P V reads another use's P"
             assert self.V[T % self.NV] == T, "P V reads another tile's V"
             self.O[g] = [use] if first else self.O[g] + [use]
 
@@ -79,159 +86,151 @@ class Machine:
                 full[T % n].arrive()
                 T += 1
 
-    def issuer(self):
-        segs, NG = self.segs, self.NG
-        st = dict(su=0, sT=0, si=0, sj=0, sn=0, fresh=True)
-
-        def issue_s():
-            tiles, w = segs[st["sn"]]
-            if st["fresh"]:
-                yield from self.wait("q", self.q, st["sn"] & 1)
-                st["fresh"] = False
-            if st["sj"] == 0:
-                yield from self.wait("k", self.kf[st["sT"] % self.NK], (st["sT"] // self.NK) & 1)
-            # the warps that store the block's rows: of the group whose uses it is, or (one block) all
-            warps = range(self.W) if w == 1 else range(4 * (st["su"] & 1), 4 * (st["su"] & 1) + 4)
-            self.queue.append(("S", st["su"], st["sT"], st["sn"], st["sj"], warps))
-            self.queue.append(("commit", self.s[st["su"] & 1]))
-            st["su"] += 1
-            st["sj"] += 1
-            if st["sj"] == w:
-                self.queue.append(("commit", self.ke[st["sT"] % self.NK]))
-                st["sj"] = 0
-                st["sT"] += 1
-                st["si"] += 1
-                if st["si"] == tiles:
-                    st["si"], st["fresh"] = 0, True
-                    st["sn"] += 1
-
-        u = T = 0
-        for n, (tiles, w) in enumerate(segs):
-            uses = tiles * w
-            while st["sn"] == n and st["su"] < u + 2:
-                yield from issue_s()
-            for i in range(uses):
-                yield from self.wait("p", self.p[u & 1], (u >> 1) & 1)
-                if w == 1 or not i & 1:
-                    yield from self.wait("v", self.vf[T % self.NV], (T // self.NV) & 1)
-                self.queue.append(("PV", u, T, (u & 1) if NG == 2 else 0, i < NG))
-                self.queue.append(("commit", self.pv[u & 1]))
-                if w == 1 or i & 1:
-                    self.queue.append(("commit", self.ve[T % self.NV]))
-                    T += 1
-                upto = n + 1 if i + 1 == uses else n
-                while st["sn"] < len(segs) and st["sn"] <= upto and st["su"] <= u + 2:
-                    yield from issue_s()
-                u += 1
+    def issuer(self, g):
+        NB = self.NB
+        n = T = 0
+        for seg, (tiles, w) in enumerate(self.segs):
+            mine = self.share(w, tiles, g, T)
+            yield from self.wait("q", self.q, seg & 1)
+            if self.NG == 2:
+                self.qfree.arrive()
+            count = 2 if self.NG == 2 and w == 1 else 1
+            # the warps that store a block's rows: of the group whose uses it is, or (one block) all
+            warps = range(self.W) if w == 1 else range(4 * g, 4 * g + 4)
+            for i in range(-NB, len(mine)):
+                j = i + NB
+                buf = (n + j) % NB
+                if i >= 0:
+                    t = T + mine[i]
+                    yield from self.wait("p", self.p[g][buf], ((n + i) // NB) & 1)
+                    yield from self.wait("v", self.vf[t % self.NV], (t // self.NV) & 1)
+                    self.queue[g].append(("PV", n + i, t, i == 0))
+                    if j >= len(mine):
+                        self.queue[g].append(("commit", (self.pv if i + 1 == len(mine) else self.pv2)[g]))
+                    self.queue[g] += [("commit", self.ve[t % self.NV])] * count
+                if j < len(mine):
+                    t = T + mine[j]
+                    yield from self.wait("k", self.kf[t % self.NK], (t // self.NK) & 1)
+                    self.queue[g].append(("S", n + j, t, seg, g if w == 2 else 0, warps))
+                    self.queue[g].append(("commit", self.s[g][buf]))
+                    self.queue[g] += [("commit", self.ke[t % self.NK])] * count
+            T += tiles
+            n += len(mine)
 
     def softmax(self, warp):
-        segs, NG = self.segs, self.NG
+        segs, NG, NB = self.segs, self.NG, self.NB
         g, wi = warp >> 2, warp & 3
 
-        def put_q(n, u0):
-            w = segs[n][1]
-            self.Q[(g ^ u0) & 1 if w == 2 else 0][warp] = n
+        def put_q(seg):
+            self.Q[g if segs[seg][1] == 2 else 0][warp] = seg
             yield
             self.q.arrive()
 
-        u = nx = 0
-        yield from put_q(0, 0)
-        for n, (tiles, w) in enumerate(segs):
-            uses = tiles * w
-            mine, began = [], False
-            for i in range((g ^ (u & 1)) if NG == 2 else 0, uses, NG):
-                use = u + i
-                buf = use & 1
-                yield from self.wait("s", self.s[buf], (use >> 1) & 1)
-                assert self.S[buf] == use, "softmax reads another use's scores"
-                if self.rng.random() < 0.3 and began:  # O is scaled
-                    if NG == 1:
-                        yield from self.wait("rescale", self.pv[(use - 1) & 1], ((use - 1) >> 1) & 1)
+        T = nx = npv2 = 0
+        n, npv = [0] * NG, [0] * NG
+        yield from put_q(0)
+        for seg, (tiles, w) in enumerate(segs):
+            share = self.share(w, tiles, g, T)
+            joint = NG == 2 and w == 1
+            mine = []
+            for i, t in enumerate(share):
+                v = n[g] + i
+                buf = v % NB
+                yield from self.wait("s", self.s[g][buf], (v // NB) & 1)
+                assert self.S[g][buf] == v, "softmax reads another use's scores"
+                if self.rng.random() < 0.3 and i:  # O is scaled
+                    if NB == 2 and i + 1 < len(share):
+                        yield from self.wait("rescale", self.s[g][buf ^ 1], ((v + 1) // NB) & 1)
+                    elif NB == 2:
+                        yield from self.wait("rescale", self.pv2[g], npv2 & 1)
                     assert self.O[g] == mine, "O is scaled before its last product"
                     yield
                     assert self.O[g] == mine, "O changes while it is scaled"
-                began = True
                 yield
-                assert self.S[buf] == use
-                self.P[buf][wi] = use
-                mine.append(use)
-                self.p[buf].arrive()
-            end = u + uses
-            last = [end - 1 if (end - 1) & 1 == k else end - 2 for k in range(2)]
-            have = [x >= u for x in last]
-            for k in range(2):
-                if have[k]:
-                    yield from self.wait("s_end", self.s[k], (last[k] >> 1) & 1)
-            if n + 1 < len(segs):
-                yield from put_q(n + 1, end)
-            joint = NG == 2 and w == 1
+                assert self.S[g][buf] == v
+                self.P[g][buf][wi] = v
+                mine.append(v)
+                self.p[g][buf].arrive()
+            if NG == 2:
+                if wi == 0:
+                    self.qfree.arrive()
+                yield from self.wait("qfree", self.qfree, seg & 1)
+            if seg + 1 < len(segs):
+                yield from put_q(seg + 1)
             if joint:
+                self.X[g][wi] = seg
                 self.x.arrive()
                 yield from self.wait("x", self.x, nx & 1)
-            for k in range(2):
-                if have[k] and (joint or NG == 1 or k == g):
-                    yield from self.wait("pv", self.pv[k], (last[k] >> 1) & 1)
+                assert self.X[g ^ 1][wi] == seg, "the other group's sums are of another segment"
+            want = [list(range(n[k], n[k] + len(self.share(w, tiles, k, T)))) for k in range(NG)]
+            for k in range(NG):
+                if want[k] and (joint or k == g):
+                    yield from self.wait("pv", self.pv[k], npv[k] & 1)
+                npv[k] += len(want[k]) > 0
+                n[k] += len(want[k])
+            npv2 += NB == 2 and len(share) > 1
+            reads = [k for k in range(NG) if want[k] and (joint or k == g)]
+            for _ in range(2):
+                for k in reads:
+                    assert self.O[k] == want[k], "the epilogue reads O too early or too late"
+                yield
             if joint:
-                for h in range(2):
-                    if have[h]:
-                        want = [x for x in range(u, end) if x & 1 == h]
-                        assert self.O[h] == want, "the epilogue reads O too early or too late"
-                        yield
-                        assert self.O[h] == want
                 self.xd.arrive()
                 yield from self.wait("xd", self.xd, nx & 1)
                 nx += 1
-            else:
-                assert self.O[g] == mine, "the epilogue reads O too early or too late"
-                yield
-                assert self.O[g] == mine
-            self.seen.append((n, warp, tuple(mine)))
-            u = end
+            self.seen.append((seg, warp, tuple(mine)))
+            T += tiles
 
     def run(self):
-        roles = [self.issuer(), self.producer(self.kf, self.ke, self.K, self.NK, "k_empty"),
+        roles = [self.producer(self.kf, self.ke, self.K, self.NK, "k_empty"),
                  self.producer(self.vf, self.ve, self.V, self.NV, "v_empty")]
+        roles += [self.issuer(g) for g in range(self.NG)]
         roles += [self.softmax(w) for w in range(self.W)]
         pace = {r: self.rng.choice([0.05, 0.6, 0.9]) for r in roles}
+        drain = [self.rng.choice([0.1, 0.5, 0.9]) for _ in self.queue]
+        state = lambda: (sum(b.phase for b in self.bars), len(roles), sum(map(len, self.queue)))  # noqa: E731
         idle = 0
-        while roles or self.queue:
-            state = (sum(b.phase for b in [*self.kf, *self.ke, *self.vf, *self.ve, *self.s, *self.p, *self.pv, self.q,
-                                           self.x, self.xd]), len(roles), len(self.queue))
+        while roles or any(self.queue):
+            before = state()
             for r in self.rng.sample(roles, len(roles)):
                 if self.rng.random() < pace[r]:
                     if next(r, "end") == "end":
                         roles.remove(r)
-            while self.queue and self.rng.random() < 0.5:
-                self.execute()
-            now = (sum(b.phase for b in [*self.kf, *self.ke, *self.vf, *self.ve, *self.s, *self.p, *self.pv, self.q, self.x,
-                                         self.xd]), len(roles), len(self.queue))
-            idle = idle + 1 if now == state else 0
-            assert idle < 400, "deadlock"
-        total = sum(t * w for t, w in self.segs)
-        done = [x for _, w, m in self.seen if w % 4 == 0 for x in m]
-        assert sorted(done) == list(range(total))
+            for g, q in enumerate(self.queue):
+                while q and self.rng.random() < drain[g]:
+                    self.execute(g)
+            idle = idle + 1 if state() == before else 0
+            assert idle < 1000, "deadlock"
+        for g in range(self.NG):
+            done = [x for _, w, m in self.seen if w == 4 * g for x in m]
+            before = [sum(t for t, _ in self.segs[:i]) for i in range(len(self.segs))]
+            assert done == list(range(sum(len(self.share(w, t, g, T)) for (t, w), T in zip(self.segs, before))))
 
 
 def _segs(rng, NG):
     return [(rng.choice([1, 1, 2, 3, 4, 7]), rng.randint(1, 2) if NG == 2 else 1) for _ in range(rng.randint(1, 7))]
 
 
-@pytest.mark.parametrize("NG", [1, 2])
-@pytest.mark.parametrize("rings", [(2, 2), (3, 2), (5, 5)])
-def test_protocol_keeps_every_value_for_its_reader(NG, rings):
+@pytest.mark.parametrize("NG,NB", [(1, 2), (2, 1), (2, 2)])
+@pytest.mark.parametrize("rings", [(2, 2), (4, 4), (4, 6), (8, 8), (3, 3)])
+def test_protocol_keeps_every_value_for_its_reader(NG, NB, rings):
+    if NG == 2 and rings[0] % 2 or NB == 2 and rings[1] == 2:
+        pytest.skip("no such form: two groups need rings of an even length, two buffers more than two stages")
     for seed in range(120):
         rng = random.Random(1000 * NG + seed)
-        Machine(_segs(rng, NG), NG, *rings, rng).run()
+        Machine(_segs(rng, NG), NG, NB, *rings, rng).run()
 
 
-@pytest.mark.parametrize("drop", ["k", "v", "q", "s", "p", "k_empty", "v_empty", "pv", "xd", "s_end", "rescale"])
-def test_protocol_model_sees_a_wait_left_out(drop):
+@pytest.mark.parametrize("NB", [1, 2])
+@pytest.mark.parametrize("drop", ["k", "v", "q", "s", "p", "k_empty", "v_empty", "pv", "x", "xd", "qfree", "rescale"])
+def test_protocol_model_sees_a_wait_left_out(drop, NB):
     """Without one of the waits some schedule goes wrong: the model can tell."""
-    for seed in range(400):
-        NG = 1 if drop == "rescale" else 2
+    if drop == "rescale" and NB == 1:
+        pytest.skip("no such wait")
+    for seed in range(600):
         rng = random.Random(seed)
         try:
-            Machine(_segs(rng, NG), NG, 2, 2, rng, drop=drop).run()
+            Machine(_segs(rng, 2), 2, NB, 4, 4, rng, drop=drop).run()
         except AssertionError:
             return
     raise AssertionError(f"no schedule shows that the wait {drop} is needed")
