@@ -374,6 +374,73 @@ int apa_attention_cache(const void* q, int dtype, long long q_batch_stride, long
                         size_t workspace_bytes, cudaStream_t stream);
 size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
 
+/* ------------------------------------------------------------------ drafted trees
+ * A step that checks a tree of drafted tokens (nodes) for each request: their keys are in
+ * the cache behind the context, node n of sequence b at key base + n, base = lens[b] -
+ * nodes[b] (so apa_cache_tables from base to lens gives the slots to write them to).
+ * Positions go by depth: node n stands at base + depth(n), context key j at j. */
+#define APA_TREE_MAX_NODES 1024
+
+/* Attention of the drafted rows over the cache.  Row i < nodes[b] of sequence b sees the
+ * context's keys j < base and the keys of the nodes n < nodes[b] whose bit it has; with
+ * window >= 1 only those of them whose position is above base + depth(i) - window, or below
+ * sinks.  window = 0: all of them.
+ *   q        dtype (APA_DTYPE_*) [B][Hq][Nq][d]; channels contiguous, the rest at the given
+ *            strides (in elements, multiples of 8; of an axis of length 1 any); 16-byte aligned
+ *   pages, block_table, k_scale, v_scale  as in apa_attention_cache
+ *   lens     int32 [B]: keys per sequence, the nodes' among them, in [0, 64 * max_pages]
+ *   nodes    int32 [B], each in [0, min(Nq, lens[b])]; null: Nq for all.  (Lengths out of
+ *            range are clamped to it and reported by apa_check_error)
+ *   mask     uint32 [B][Nq][ceil(Nq/32)], sequences mask_stride words apart (0: one mask for
+ *            all): bit n%32 of word n/32 of row i: row i sees node n.  Any bits will do; a
+ *            tree's are those of a node's ancestors and its own (apa_draft_tree)
+ *   depths   int32 [B][Nq], sequences depth_stride apart, each in [0, Nq) (others are clamped
+ *            to it); only read where there is a window, else nullable
+ *   out      dtype [B][Hq][Nq][d], contiguous; rows that see no key, and those from nodes[b]
+ *            on, are zero
+ *   lse      fp32 [B][Hq][Nq], natural log (nullable); -inf for such rows
+ *   workspace  apa_attention_tree_workspace_bytes() bytes, 256-byte aligned, or null to have
+ *            it allocated stream-ordered for the call.  Two calls that overlap on the GPU
+ *            must not share one.
+ * Keys that no row sees are never used, whatever a page holds there; a NaN in V at a key that
+ * some of the sequence's rows see may reach the others' outputs too.  Numerics are those of
+ * apa_attention_cache.  Nq <= APA_TREE_MAX_NODES, B <= 8192, B * max_pages < 2^29.  The work
+ * is split over the GPU by the lengths alone, so reruns are bitwise equal. */
+int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
+                       long long q_row_stride, const uint8_t* pages, int num_pages, const int32_t* block_table,
+                       int max_pages, const int32_t* lens, const int32_t* nodes, const uint32_t* mask,
+                       long long mask_stride, const int32_t* depths, long long depth_stride, const float* k_scale,
+                       const float* v_scale, int B, int Hq, int Hkv, int Nq, int d, int window, int sinks, void* out,
+                       float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t apa_attention_tree_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
+/* What apa_attention_tree reads, from the trees, on the GPU.
+ *   parents  int32 [B][Nq]: a node's parent, a node before it, or -1: the context (others
+ *            count as -1 and are reported by apa_check_error)
+ *   nodes    int32 [B], each in [0, Nq] (clamped and reported); null: Nq for all
+ *   mask     uint32 [B][Nq][ceil(Nq/32)]: a node's ancestors and itself; 0 from nodes[b] on
+ *   depths   int32 [B][Nq]: its ancestors' number (a rotary position is base + depth); 0 from
+ *            nodes[b] on
+ * Nq <= APA_TREE_MAX_NODES. */
+int apa_draft_tree(const int32_t* parents, const int32_t* nodes, int B, int Nq, uint32_t* mask, int32_t* depths,
+                   cudaStream_t stream);
+
+/* Keeps the accepted path of each tree: the keys of nodes path[b][0 .. counts[b]-1] move to
+ * base, base + 1, ..., in the pools of all layers; what lies behind them stays as it is (its
+ * pages go back with apa_cache_tables from lens to new_lens).
+ *   pages    uint8 [layers][num_pages][Hkv][72*d], 16-byte aligned; block_table as above (the
+ *            same for all layers)
+ *   lens, nodes  int32 [B], as in apa_attention_tree
+ *   path     int32 [B][path_len], rising node numbers below nodes[b] in the first counts[b]
+ *            places; counts int32 [B], each in [0, min(path_len, nodes[b])]
+ *   new_lens int32 [B]: base + counts[b]; not lens itself
+ * A sequence whose lengths, count or path break this keeps its context (new_lens is base) and
+ * nothing of it moves; that, and a table entry outside the pool (nothing is moved from or to
+ * it), is reported by apa_check_error.  Keys move as whole bytes: nothing is quantized anew. */
+int apa_cache_accept(uint8_t* pages, int layers, int num_pages, int Hkv, int d, const int32_t* block_table, int max_pages,
+                     const int32_t* lens, const int32_t* nodes, const int32_t* path, int path_len, const int32_t* counts,
+                     int B, int32_t* new_lens, cudaStream_t stream);
+
 /* ------------------------------------------------------------------ an encoder's states
  * Cross attention: every query row of sequence b sees the keys below lens[b] of its
  * encoder's states; no causal order.

@@ -23,11 +23,14 @@ __all__ = ["attention", "attention_paged", "attention_host", "quantize", "quanti
            "status_string", "hot_mask_shape", "TILE", "GROUP_ROWS", "BLOCK_ROWS", "FLAG_Q_RESIDUAL",
            "FLAG_LSE_SCALES", "FLAG_VALUE_WEIGHTED", "FLAG_ROWSUM_MMA", "attention_window", "cache_pages",
            "cache_tables", "cache_write", "cache_read", "attention_cache", "attention_cache_workspace_bytes",
-           "TABLES_STATUS", "attention_cross", "attention_cross_workspace_bytes"]
+           "TABLES_STATUS", "draft_tree", "attention_tree", "attention_tree_workspace_bytes", "cache_accept",
+           "TREE_MAX_NODES", "attention_cross", "attention_cross_workspace_bytes"]
 
 _LATER = {n: "cache" for n in ("cache_pages", "cache_tables", "cache_write", "cache_read", "attention_cache",
                                "attention_cache_workspace_bytes", "TABLES_STATUS")}
 _LATER["attention_window"] = "window"
+_LATER.update({n: "tree" for n in ("draft_tree", "attention_tree", "attention_tree_workspace_bytes", "cache_accept",
+                                   "TREE_MAX_NODES")})
 _LATER["attention_cross"] = _LATER["attention_cross_workspace_bytes"] = "cross"
 
 

@@ -40,6 +40,10 @@ _SIGS = {
     "apa_cache_read": (I, [P, I, I, I, I, I, P, P, P, P, P, P]),
     "apa_attention_cache": (I, [P, I, LL, LL, LL, P, I, P, I, P, P, P, I, I, I, I, I, I, I, P, P, P, SZ, P]),
     "apa_attention_cache_workspace_bytes": (SZ, [I, I, I, I, I]),
+    "apa_draft_tree": (I, [P, P, I, I, P, P, P]),
+    "apa_attention_tree": (I, [P, I, LL, LL, LL, P, I, P, I, P, P, P, LL, P, LL, P, P, I, I, I, I, I, I, I, P, P, P, SZ, P]),
+    "apa_attention_tree_workspace_bytes": (SZ, [I, I, I, I, I]),
+    "apa_cache_accept": (I, [P, I, I, I, I, P, I, P, P, P, I, P, I, P, P]),
     "apa_attention_cross": (I, [P, I, LL, LL, LL, P, LL, LL, LL, P, LL, LL, LL, P, I, I, I, I, I, I, P, P, P, SZ, P]),
     "apa_attention_cross_workspace_bytes": (SZ, [I, I, I, I, I]),
     "apa_check_error": (I, [P]),

@@ -1,0 +1,428 @@
+// apa_tree.cu -- attention of a tree of drafted tokens over the 4-bit paged K/V cache.
+//
+// out = softmax(q K^T / sqrt(d)) V, row i (a drafted token, or node) over the context's keys and
+// the drafted keys whose bits it has, under an optional window and sinks, by positions: a
+// context key stands at its index, node n at base + depth(n).
+//
+// Trees have tens of nodes, and G rows for each, so the products run on tcgen05 tiles of 128 rows
+// (rows.cuh) and what bounds it is turning codes into FP16 operands in shared memory: 2 x 64 x d
+// values per page and KV head, once for up to 256 rows.  One warp brings pages in (a bulk copy
+// each: a page's part of a head is contiguous), two turn K's codes and two V's.  E2M1 * UE4M3 has
+// 6 significant bits and lies in 2^-10 .. 2688, so K and V are exact in FP16; Q's rows are
+// scaled by a power of two to 2^14 .. 2^16 as in the decode kernel (apa_decode.cu).  A V code byte
+// holds channels g and 8 + g of 16, one FP16 pair: the pairs are stored side by side (kPairedV),
+// and the epilogue puts O's columns in order again, which costs no instruction.
+#include "rows.cuh"
+
+namespace apa {
+namespace {
+
+// Eight E2M1 codes -> four FP16 pairs.
+__device__ __forceinline__ void tree_e2m1x8(uint32_t w, uint32_t* h) {
+  asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t tree_e4m3x2(uint32_t w) {  // two scale codes -> an FP16 pair
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+  return r;
+}
+__device__ __forceinline__ uint32_t tree_hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+#ifndef APA_TREE_V
+#define APA_TREE_V 0
+#endif
+template <int D>
+struct TreePick;
+template <>
+struct TreePick<64> { using Cfg = RowCfg<64, 64, 2, true, 4, 4, true>; static constexpr int kRaw = 8; };
+#if APA_TREE_V == 0
+template <>
+struct TreePick<128> { using Cfg = RowCfg<128, 64, 1, true, 4, 4, true>; static constexpr int kRaw = 6; };
+#else
+template <>
+struct TreePick<128> { using Cfg = RowCfg<128, 64, 2, false, 4, 4, true>; static constexpr int kRaw = 3; };
+#endif
+template <>
+struct TreePick<256> { using Cfg = RowCfg<256, 64, 2, true, 2, 3, true>; static constexpr int kRaw = 3; };
+
+template <int D, bool F16>
+struct TreeSrc {
+  using Cfg = typename TreePick<D>::Cfg;
+  static constexpr int KT = Cfg::KT, kRaw = TreePick<D>::kRaw;
+  static_assert(KT == kTile, "a tile is a page");
+  static constexpr int kPageBytes = page_head_bytes(D);
+  static constexpr int kKWarps = 2, kVWarps = 2, kSrcWarps = 1 + kKWarps + kVWarps;
+  static constexpr int kThreads = (Cfg::kSrcWarp + kSrcWarps) * 32;
+  static constexpr int kKArrivals = kKWarps, kVArrivals = kVWarps;
+  static constexpr int kBars = 2 * kRaw;  // pages there, pages read
+  static __device__ __forceinline__ uint32_t bar_count(int i) { return i < kRaw ? 1 : kKWarps + kVWarps; }
+  static constexpr bool kPairedV = true, kOutF16 = F16;
+  static constexpr int kSmem = Cfg::kSrcOff + kRaw * kPageBytes + 1024;
+  static_assert(kSmem <= 232448 - 4096, "shared memory");
+
+  struct Params {
+    RowParams r;
+    const uint8_t* pages;
+    int num_pages;
+    const int32_t* table;
+    int max_pages;
+    const int32_t* lens;
+    const int32_t* nodes;  // or null: Nq for all
+    const uint32_t* mask;  // [B][Nq][words], sequences mask_stride apart
+    long long mask_stride;
+    int words;
+    const int32_t* depths;  // [B][Nq], sequences depth_stride apart; or null (no window)
+    long long depth_stride;
+    const float *k_scale, *v_scale;
+    int window, sinks;
+  };
+  // Keys len, of which the last `nodes` are the drafted ones; tiles: pages that hold sinks, then those from lo on.
+  struct Seq {
+    int blocks, tiles, len, base, nodes, n_sink, lo;
+    __device__ __forceinline__ Seq(const Params& p, int b) {
+      len = max(0, min(p.lens[b], p.max_pages * kTile));
+      nodes = max(0, min(p.nodes ? p.nodes[b] : p.r.Nq, min(p.r.Nq, len)));
+      base = len - nodes;
+      blocks = (p.r.G() * nodes + kBlockRows - 1) / kBlockRows;
+      lo = p.window ? max(0, base - p.window + 1) / kTile : 0;
+      n_sink = p.window ? min((p.sinks + kTile - 1) / kTile, lo) : 0;
+      tiles = nodes ? n_sink + (len + kTile - 1) / kTile - lo : 0;
+    }
+    __device__ __forceinline__ long long uses() const { return (long long)blocks * tiles; }
+    __device__ __forceinline__ void report(const Params& p, int b) const {
+      if (blockIdx.x == 0 && p.r.err && (p.lens[b] != len || (p.nodes ? p.nodes[b] : p.r.Nq) != nodes))
+        atomicCAS(p.r.err, 0, APA_DEVERR_BOUNDS);
+    }
+    __device__ __forceinline__ int page(int tile) const { return tile < n_sink ? tile : lo + tile - n_sink; }
+  };
+
+  struct Row {
+    bool valid;
+    int out_row, head, pos;
+    float c2, v_scale;
+    int depth;
+    long long depth_row;
+    const uint32_t* bits;
+    __device__ __forceinline__ void set(const Params& p, const Seq& s, int b, int h, int P) {
+      const int G = p.r.G();
+      pos = P / G;
+      head = h * G + P % G;
+      valid = pos < s.nodes;
+      out_row = pos < p.r.Nq ? (b * p.r.Hq + head) * p.r.Nq + pos : -1;
+      bits = p.mask + b * p.mask_stride + (long long)pos * p.words;
+      depth_row = b * p.depth_stride;
+      depth = valid && p.depths ? max(0, min(p.depths[b * p.depth_stride + pos], p.r.Nq - 1)) : 0;
+    }
+    float up;  // the power of two that brings the row's largest value to 2^14 .. 2^16
+    __device__ __forceinline__ void scale(const Params& p, int h, const uint16_t* src) {
+      float amax = 0.f;
+      if (src) {
+#pragma unroll 4
+        for (int c = 0; c < D; c += 8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack2<F16>(w[k]);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+      }
+      int e = (int)((__float_as_uint(amax) >> 23) & 255) - 127;
+      e = max(-100, min(126, e));
+      up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      const float down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+      // (a positive finite number, so that a masked score stays -inf and a key of zeros 0)
+      const float f = down * (p.k_scale[h] * kLog2e * rsqrtf((float)D));
+      c2 = f < FLT_MIN ? FLT_MIN : f > FLT_MAX ? FLT_MAX : f;
+      v_scale = p.v_scale[h];
+    }
+    __device__ __forceinline__ void scale_v(const Params& p, int h) { v_scale = p.v_scale[h]; }
+    __device__ __forceinline__ uint32_t convert(uint32_t w) const {
+      const float2 f = unpack2<F16>(w);
+      return pack2<true>(f.x * up, f.y * up);
+    }
+    // which of the keys j .. j + 31 the row sees
+    __device__ __forceinline__ uint32_t sees(const Params& p, const Seq& s, int j) const {
+      if (!valid) return 0u;
+      auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+      uint32_t ctx = below(s.base - j), drafted = 0u;
+      const int at = j - s.base;  // node of key j
+      if (at > -32 && at < s.nodes) {
+        const int w = at >> 5, sh = at & 31;  // (at = -1: word -1, shifted by 31)
+        const uint32_t a = w >= 0 ? bits[w] : 0u, c = w + 1 < p.words ? bits[w + 1] : 0u;
+        drafted = __funnelshift_r(a, c, sh) & below(s.nodes - at) & ~ctx;
+      }
+      if (p.window) {
+        const int first = s.base + depth - p.window + 1;  // the window's first position
+        ctx &= ~below(first - j) | below(p.sinks - j);
+        if (p.window < p.r.Nq)  // only then may a drafted key lie behind it
+          for (uint32_t x = drafted; x; x &= x - 1) {
+            const int k = __ffs(x) - 1;
+            const int pk = s.base + max(0, min(p.depths[depth_row + at + k], p.r.Nq - 1));
+            if (pk < first && pk >= p.sinks) drafted &= ~(1u << k);
+          }
+      }
+      return ctx | drafted;
+    }
+    template <int N>
+    __device__ __forceinline__ void mask(const Params& p, const Seq& s, int tile, float* sv) const {
+      const int j0 = s.page(tile) * kTile;
+      // all rows see all keys?
+      if (j0 + N <= s.base && (!p.window || j0 + N <= p.sinks || j0 > s.base + p.r.Nq - 1 - p.window) &&
+          __all_sync(0xffffffffu, valid))
+        return;
+#pragma unroll
+      for (int c = 0; c < N; c += 32) {
+        const uint32_t v = sees(p, s, j0 + c);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (!((v >> k) & 1u)) sv[c + k] = -INFINITY;
+      }
+    }
+  };
+
+  template <class Walk, class Bars>
+  static __device__ __forceinline__ void produce(const Params& p, Walk& walk, uint8_t* smem, uint32_t sbase,
+                                                 const Bars& bars, int warp, int lane) {
+    using C = Cfg;
+    auto raw_full = [&](int T) { return bars.at(Bars::kNum + T % kRaw); };
+    auto raw_empty = [&](int T) { return bars.at(Bars::kNum + kRaw + T % kRaw); };
+    RowSeg g;
+    int T = 0;
+    bool ok = true;
+    if (warp == 0) {
+      // ---- pages come in
+      while (ok && walk.next(g)) {
+        const uint8_t* head = p.pages + (size_t)g.h * kPageBytes;
+        const int32_t* table = p.table + (size_t)g.b * p.max_pages;
+        const int held = (walk.seq.len + kTile - 1) / kTile;
+        int tbase = -64, entry = 0;  // entry: this lane's of the 32 table entries from tbase
+        for (int t = g.t0; t < g.t1; ++t, ++T) {
+          const int e = walk.seq.page(t);
+          if ((unsigned)(e - tbase) >= 32u) {
+            tbase = e;
+            entry = e + lane < held ? table[e + lane] : 0;
+          }
+          int page = __shfl_sync(0xffffffffu, entry, e - tbase);
+          if (T >= kRaw && !(ok = bars.warp_wait(raw_empty(T), ((T / kRaw) & 1) ^ 1))) break;
+          if (lane == 0) {
+            if ((unsigned)page >= (unsigned)p.num_pages) {  // reads page 0, and is reported
+              if (p.r.err) atomicCAS(p.r.err, 0, APA_DEVERR_BOUNDS);
+              page = 0;
+            }
+            mbar_arrive_expect_tx(raw_full(T), kPageBytes);
+            bulk_g2s(sbase + C::kSrcOff + T % kRaw * kPageBytes, head + (size_t)page * p.r.Hkv * kPageBytes, kPageBytes,
+                     raw_full(T));
+          }
+          __syncwarp();
+        }
+      }
+      // every copy issued lands before the CTA exits, also when another warp gave up
+      if (lane == 0)
+        for (int x = max(0, T - kRaw); x < T; ++x) rows_wait_in_flight(raw_full(x), (x / kRaw) & 1, p.r.err);
+      __syncwarp();
+      return;
+    }
+    const bool of_k = warp <= kKWarps;
+    const int w = of_k ? warp - 1 : warp - 1 - kKWarps;
+    while (ok && walk.next(g)) {
+      for (int t = g.t0; t < g.t1; ++t, ++T) {
+        const uint8_t* raw = smem + C::kSrcOff + T % kRaw * kPageBytes;
+        if (!(ok = bars.warp_wait(raw_full(T), (T / kRaw) & 1))) break;
+        if (of_k) {
+          if (T >= C::NK && !(ok = bars.warp_wait(bars.k_empty(T), Bars::k_par(T) ^ 1))) break;
+          uint8_t* dst = smem + C::kKOff + T % C::NK * C::kTileBytes;
+          // A lane takes 32 channels (16 code bytes, two scales) of a key.  Eight neighbouring lanes store to four
+          // keys and both halves of 64 channels: all banks once.
+          constexpr int kQuarters = D / 32 < 4 ? D / 32 : 4, kUnits = kTile * D / 1024;
+#pragma unroll
+          for (int u = 0; u < kUnits / kKWarps; ++u) {
+            const int unit = u * kKWarps + w;
+            int key, q;
+            if constexpr (D == 64) {
+              key = 16 * unit + (lane & 3) + 4 * (lane >> 3);
+              q = (lane >> 2) & 1;
+            } else {
+              key = 8 * (unit / (D / 128)) + (lane & 3) + 4 * ((lane >> 3) & 1);
+              q = ((lane >> 2) & 1) + 2 * (lane >> 4) + 4 * (unit % (D / 128));
+            }
+            static_assert(kQuarters >= 2, "channels");
+            const uint8_t* blk = raw + key / kBlkKeys * blk_bytes(D);
+            const uint4 code = *reinterpret_cast<const uint4*>(blk + key % kBlkKeys * (D / 2) + 16 * q);
+            const uint32_t sc = tree_e4m3x2(*reinterpret_cast<const uint16_t*>(blk + ks_byte(D, key % kBlkKeys, 2 * q)));
+            const uint32_t f[2] = {__byte_perm(sc, 0, 0x1010), __byte_perm(sc, 0, 0x3232)};
+            const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+            uint8_t* row = dst + (q >> 1) * (KT * 128) + key * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h[4];
+              tree_e2m1x8(cw[k], h);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) h[e] = tree_hmul2(h[e], f[k >> 1]);
+              *reinterpret_cast<uint4*>(row + ((((q & 1) * 4 + k) ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(raw_empty(T));
+            mbar_arrive(bars.k_full(T));
+          }
+        } else {
+          if (T >= C::NV && !(ok = bars.warp_wait(bars.v_empty(T), Bars::v_par(T) ^ 1))) break;
+          uint8_t* dst = smem + C::kVOff + T % C::NV * C::kTileBytes;
+          const Seq& s = walk.seq;
+          const int j0 = s.page(t) * kTile;
+          // keys that no row sees count as 0 whatever the page holds there: a weight of 0 does not hide a NaN
+          const int gap = p.window ? s.base - p.window : -1;  // the last key before every row's window
+          const bool edge = j0 + kTile > s.len || (j0 <= gap && j0 + kTile > p.sinks);
+          // A lane takes four keys and four of the eight byte rows (channels g, g + 8) of 64 channels.
+          const int q = lane & 3, gh = (lane >> 2) & 1, mb = lane >> 3;
+          const uint8_t* blk = raw + mb * blk_bytes(D);
+#pragma unroll
+          for (int u = 0; u < D / 64; ++u) {
+            if (D == 64 ? (T & 1) != w : u % kVWarps != w) continue;
+            uint4 code[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              code[j] = *reinterpret_cast<const uint4*>(blk + blk_v(D) + 512 * u + 64 * (4 * gh + j) + 16 * q);
+            const uint4 sc4 = *reinterpret_cast<const uint4*>(blk + blk_vs(D) + 4 * (q * (D / 16) + 4 * u));
+            const uint32_t sc[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
+            uint32_t keep = ~0u;
+            if (edge)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int j = j0 + 16 * mb + 4 * q + k;
+                if (j >= s.len || (j <= gap && j >= p.sinks)) keep &= ~(255u << (8 * k));
+              }
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) {
+              const uint32_t b = sc[tt] & keep, f01 = tree_e4m3x2(b & 0xFFFFu), f23 = tree_e4m3x2(b >> 16);
+              const uint32_t f[4] = {__byte_perm(f01, 0, 0x1010), __byte_perm(f01, 0, 0x3232), __byte_perm(f23, 0, 0x1010),
+                                     __byte_perm(f23, 0, 0x3232)};
+              uint32_t h[4][4];  // [byte row][key]
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t cw[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+                tree_e2m1x8(cw[tt], h[j]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int key = 16 * mb + 4 * q + k;
+                *reinterpret_cast<uint4*>(dst + u * (KT * 128) + key * 128 + (((2 * tt + gh) ^ (key & 7)) << 4)) =
+                    make_uint4(tree_hmul2(h[0][k], f[k]), tree_hmul2(h[1][k], f[k]), tree_hmul2(h[2][k], f[k]),
+                               tree_hmul2(h[3][k], f[k]));
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(raw_empty(T));
+            mbar_arrive(bars.v_full(T));
+          }
+        }
+      }
+    }
+  }
+};
+
+}  // namespace
+}  // namespace apa
+
+using namespace apa;
+
+extern "C" {
+
+size_t apa_attention_tree_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+  if (rows_bad_heads(B, Hq, Hkv, Nq) || Nq > APA_TREE_MAX_NODES || (d != 64 && d != 128 && d != 256)) return 0;
+  return rows_workspace(Hq / Hkv * Nq, d);
+}
+
+int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
+                       long long q_row_stride, const uint8_t* pages, int num_pages, const int32_t* block_table,
+                       int max_pages, const int32_t* lens, const int32_t* nodes, const uint32_t* mask,
+                       long long mask_stride, const int32_t* depths, long long depth_stride, const float* k_scale,
+                       const float* v_scale, int B, int Hq, int Hkv, int Nq, int d, int window, int sinks, void* out,
+                       float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !pages || !block_table || !lens || !mask || !k_scale || !v_scale || !out || (window && !depths))
+    return APA_ERR_NULL;
+  if (rows_bad_heads(B, Hq, Hkv, Nq) || Nq > APA_TREE_MAX_NODES || num_pages < 1 || num_pages >= (1 << 25) ||
+      max_pages < 1 || (long long)B * max_pages >= (1 << 29) || max_pages >= (1 << 25) || mask_stride < 0 || depth_stride < 0)
+    return APA_ERR_SHAPE;
+  if (d != 64 && d != 128 && d != 256) return APA_ERR_HEAD_DIM;
+  if (dtype != APA_DTYPE_BF16 && dtype != APA_DTYPE_F16) return APA_ERR_DTYPE;
+  if (window < 0 || sinks < 0) return APA_ERR_WINDOW;
+  // (uses are counted in 32 bits per head, and per CTA)
+  const double uses = (double)B * max_pages * (((double)(Hq / Hkv) * Nq + 127) / 128 + 1);
+  if (uses >= 2147483648.0 || uses * Hkv >= 137438953472.0) return APA_ERR_SHAPE;
+  // (the stride of an axis of length 1 is never used: any value will do)
+  if (B == 1) q_batch_stride = mask_stride = depth_stride = 0;
+  if (Hq == 1) q_head_stride = 0;
+  if (Nq == 1) q_row_stride = 0;
+  if ((((uintptr_t)q | (uintptr_t)pages | (uintptr_t)out) & 15) || ((q_batch_stride | q_head_stride | q_row_stride) & 7))
+    return APA_ERR_ALIGN;
+  const size_t need = apa_attention_tree_workspace_bytes(B, Hq, Hkv, Nq, d);
+  void* ws = workspace;
+  if (ws && (workspace_bytes < need || ((uintptr_t)ws & 255))) return APA_ERR_NOMEM;
+  // (positions stay within 32 bits: none exceeds 64 * max_pages + Nq)
+  const int most = max_pages * kTile + Nq;
+  if (window > most) window = 0;
+  if (sinks > most) sinks = most;
+  if (!ws && cudaMallocAsync(&ws, need, stream) != cudaSuccess) return APA_ERR_NOMEM;
+  const bool f16 = dtype == APA_DTYPE_F16;
+  auto go = [&](auto src) {
+    using Src = decltype(src);
+    typename Src::Params p{};
+    p.r.B = B;
+    p.r.Hq = Hq;
+    p.r.Hkv = Hkv;
+    p.r.Nq = Nq;
+    p.r.q = (const uint16_t*)q;
+    p.r.qs_b = q_batch_stride;
+    p.r.qs_h = q_head_stride;
+    p.r.qs_r = q_row_stride;
+    p.r.out = (uint16_t*)out;
+    p.r.lse = lse;
+    p.r.err = device_error_word();
+    p.pages = pages;
+    p.num_pages = num_pages;
+    p.table = block_table;
+    p.max_pages = max_pages;
+    p.lens = lens;
+    p.nodes = nodes;
+    p.mask = mask;
+    p.mask_stride = mask_stride;
+    p.words = (Nq + 31) / 32;
+    p.depths = depths;
+    p.depth_stride = depth_stride;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.window = window;
+    p.sinks = sinks;
+    return launch_rows<Src>(p, ws, stream);
+  };
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (d) {
+    case 64: e = f16 ? go(TreeSrc<64, true>{}) : go(TreeSrc<64, false>{}); break;
+    case 128: e = f16 ? go(TreeSrc<128, true>{}) : go(TreeSrc<128, false>{}); break;
+    case 256: e = f16 ? go(TreeSrc<256, true>{}) : go(TreeSrc<256, false>{}); break;
+  }
+  int st = e == cudaSuccess ? APA_OK : APA_ERR_CUDA;
+  if (!workspace && cudaFreeAsync(ws, stream) != cudaSuccess && st == APA_OK) st = APA_ERR_CUDA;
+  return st;
+}
+
+}  // extern "C"
