@@ -34,7 +34,7 @@ struct CrossSrc {
   static constexpr int kKArrivals = 1, kVArrivals = 1;
   static constexpr int kBars = Cfg::NV;  // per stage of V: a last tile has landed, values behind the end and all
   static __device__ __forceinline__ uint32_t bar_count(int) { return 1; }
-  static constexpr bool kPairedV = false, kOutF16 = F16;
+  static constexpr bool kPairedV = false, kOutF16 = F16, kScaledQ = false;
   static constexpr int kSmem = Cfg::kSrcOff + 1024;
   static_assert(kSmem <= 232448 - 4096, "shared memory");
 
@@ -47,6 +47,7 @@ struct CrossSrc {
   };
   struct Seq {
     int blocks, tiles, len;
+    Seq() = default;
     __device__ __forceinline__ Seq(const Params& p, int b) {
       len = p.lens ? max(0, min(p.lens[b], p.Nkv)) : p.Nkv;
       tiles = (len + Cfg::KT - 1) / Cfg::KT;
@@ -61,80 +62,90 @@ struct CrossSrc {
   };
   struct Row {
     bool valid;
-    int out_row, head, pos;
+    int out_row;
     float c2, v_scale;
     __device__ __forceinline__ void set(const Params& p, const Seq&, int b, int h, int P) {
       const int G = p.r.G();
       valid = P < G * p.r.Nq;
-      pos = P / G;
-      head = h * G + P % G;
-      out_row = valid ? (b * p.r.Hq + head) * p.r.Nq + pos : -1;
+      out_row = valid ? (b * p.r.Hq + h * G + P % G) * p.r.Nq + P / G : -1;
       v_scale = 1.f;
     }
-    __device__ __forceinline__ void scale(const Params&, int, const uint16_t*) { c2 = kLog2e * rsqrtf((float)D); }
+    __device__ __forceinline__ float scale(const Params&, int, float) {
+      c2 = kLog2e * rsqrtf((float)D);
+      return 1.f;
+    }
     __device__ __forceinline__ void scale_v(const Params&, int) {}
-    __device__ __forceinline__ uint32_t convert(uint32_t w) const { return w; }
-    template <int KT>
-    __device__ __forceinline__ void mask(const Params&, const Seq& s, int tile, float* sv) const {
-      const int n = s.len - tile * KT;
-      if (n >= KT) return;
+    __device__ __forceinline__ uint32_t convert(uint32_t w, float) const { return w; }
+    // which of a tile's keys the row sees, in words of 32
+    template <int N>
+    __device__ __forceinline__ void mask(const Params&, const RowWalk<CrossSrc>& walk, int tile, uint32_t* vis) const {
+      const int left = walk.seq.len - (walk.g.t0 + tile) * Cfg::KT;
 #pragma unroll
-      for (int c = 0; c < KT; ++c)
-        if (c >= n) sv[c] = -INFINITY;
+      for (int c = 0; c < N; ++c) {
+        const int n = left - 32 * c;
+        vis[c] = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+      }
     }
   };
 
-  template <class Walk, class Bars>
-  static __device__ __forceinline__ void produce(const Params& p, Walk& walk, uint8_t* smem, uint32_t sbase,
+  template <class Bars>
+  static __device__ __forceinline__ void produce(const Params& p, RowWalk<CrossSrc>& walk, uint8_t* smem, uint32_t sbase,
                                                  const Bars& bars, int warp, int lane) {
     using C = Cfg;
     constexpr int KT = C::KT, kAtoms = D / 64;
     auto landed = [&](int T) { return bars.at(Bars::kNum + T % C::NV); };
-    RowSeg g;
+    const RowSeg& g = walk.g;
+    int T = 0;
+    bool ok = true;
     if (warp == 0) {
-      if (lane != 0) return;
-      prefetch_tmap(&p.kmap);
-      prefetch_tmap(&p.vmap);
-      int T = 0, issued_k = 0, issued_v = 0;
+      int issued_k = 0, issued_v = 0;
       uint32_t last = 0, last_par = 0;  // bit per stage of V: its copy counts on `landed`, and that barrier's parity
-      bool ok = true;
-      while (ok && walk.next(g)) {
-        const bool ragged = walk.seq.ragged(p);
-        for (int t = g.t0; t < g.t1; ++t, ++T) {
-          if (T >= C::NK && !(ok = bars.wait(bars.k_empty(T), Bars::k_par(T) ^ 1))) break;
-          mbar_arrive_expect_tx(bars.k_full(T), C::kTileBytes);
+      if (lane == 0) {
+        prefetch_tmap(&p.kmap);
+        prefetch_tmap(&p.vmap);
+      }
+      while (ok && walk.next(p, lane)) {
+        if (lane == 0) {
+          const bool ragged = walk.seq.ragged(p);
+          for (int t = g.t0; t < g.t1; ++t, ++T) {
+            if (T >= C::NK && !(ok = bars.wait(bars.k_empty(T), Bars::k_par(T) ^ 1))) break;
+            mbar_arrive_expect_tx(bars.k_full(T), C::kTileBytes);
 #pragma unroll
-          for (int a = 0; a < kAtoms; ++a)
-            tma_load_4d(sbase + C::kKOff + (T % C::NK) * C::kTileBytes + a * (KT * 128), &p.kmap, a * 64, t * KT,
-                        g.h * p.kh, g.b * p.kb, bars.k_full(T));
-          issued_k = T + 1;
-          if (T >= C::NV && !(ok = bars.wait(bars.v_empty(T), Bars::v_par(T) ^ 1))) break;
-          const bool fix = ragged && t == g.n - 1;
-          const uint32_t bit = 1u << (T % C::NV), bar = fix ? landed(T) : bars.v_full(T);
-          if (last & bit) last_par ^= bit;
-          last = fix ? last | bit : last & ~bit;
-          mbar_arrive_expect_tx(bar, C::kTileBytes);
+            for (int a = 0; a < kAtoms; ++a)
+              tma_load_4d(sbase + C::kKOff + (T % C::NK) * C::kTileBytes + a * (KT * 128), &p.kmap, a * 64, t * KT,
+                          g.h * p.kh, g.b * p.kb, bars.k_full(T));
+            issued_k = T + 1;
+            if (T >= C::NV && !(ok = bars.wait(bars.v_empty(T), Bars::v_par(T) ^ 1))) break;
+            const bool fix = ragged && t == g.n - 1;
+            const uint32_t bit = 1u << (T % C::NV), bar = fix ? landed(T) : bars.v_full(T);
+            if (last & bit) last_par ^= bit;
+            last = fix ? last | bit : last & ~bit;
+            mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
-          for (int a = 0; a < kAtoms; ++a)
-            tma_load_4d(sbase + C::kVOff + (T % C::NV) * C::kTileBytes + a * (KT * 128), &p.vmap, a * 64, t * KT,
-                        g.h * p.vh, g.b * p.vb, bar);
-          issued_v = T + 1;
+            for (int a = 0; a < kAtoms; ++a)
+              tma_load_4d(sbase + C::kVOff + (T % C::NV) * C::kTileBytes + a * (KT * 128), &p.vmap, a * 64, t * KT,
+                          g.h * p.vh, g.b * p.vb, bar);
+            issued_v = T + 1;
+          }
         }
+        ok = __all_sync(0xffffffffu, ok);
       }
       // every copy issued lands before the CTA exits, also when another warp gave up
-      for (int x = max(0, issued_k - C::NK); x < issued_k; ++x) rows_wait_in_flight(bars.k_full(x), Bars::k_par(x), p.r.err);
-      for (int x = max(0, issued_v - C::NV); x < issued_v; ++x) {
-        const uint32_t bit = 1u << (x % C::NV);
-        if (last & bit)
-          rows_wait_in_flight(landed(x), last_par & bit ? 1 : 0, p.r.err);
-        else
-          rows_wait_in_flight(bars.v_full(x), Bars::v_par(x), p.r.err);
+      if (lane == 0) {
+        for (int x = max(0, issued_k - C::NK); x < issued_k; ++x) rows_wait_in_flight(bars.k_full(x), Bars::k_par(x), p.r.err);
+        for (int x = max(0, issued_v - C::NV); x < issued_v; ++x) {
+          const uint32_t bit = 1u << (x % C::NV);
+          if (last & bit)
+            rows_wait_in_flight(landed(x), last_par & bit ? 1 : 0, p.r.err);
+          else
+            rows_wait_in_flight(bars.v_full(x), Bars::v_par(x), p.r.err);
+        }
       }
+      __syncwarp();
     } else {
       // the last tiles' values behind the end: zeros
-      int T = 0;
       uint32_t par = 0;
-      while (walk.next(g)) {
+      while (walk.next(p, lane)) {
         T += g.t1 - g.t0;
         if (g.t1 < g.n || !walk.seq.ragged(p)) continue;
         const int x = T - 1, st = x % C::NV;

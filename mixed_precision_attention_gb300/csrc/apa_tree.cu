@@ -51,10 +51,10 @@ template <>
 struct TreePick<128> { using Cfg = RowCfg<128, 64, 1, true, 4, 4, true>; static constexpr int kRaw = 6; };
 #else
 template <>
-struct TreePick<128> { using Cfg = RowCfg<128, 64, 2, false, 4, 4, true>; static constexpr int kRaw = 3; };
+struct TreePick<128> { using Cfg = RowCfg<128, 64, 2, false, 4, 4, true>; static constexpr int kRaw = 2; };
 #endif
 template <>
-struct TreePick<256> { using Cfg = RowCfg<256, 64, 2, true, 2, 3, true>; static constexpr int kRaw = 3; };
+struct TreePick<256> { using Cfg = RowCfg<256, 64, 2, true, 2, 2, true>; static constexpr int kRaw = 4; };
 
 template <int D, bool F16>
 struct TreeSrc {
@@ -62,14 +62,28 @@ struct TreeSrc {
   static constexpr int KT = Cfg::KT, kRaw = TreePick<D>::kRaw;
   static_assert(KT == kTile, "a tile is a page");
   static constexpr int kPageBytes = page_head_bytes(D);
-  static constexpr int kKWarps = 2, kVWarps = 2, kSrcWarps = 1 + kKWarps + kVWarps;
-  static constexpr int kThreads = (Cfg::kSrcWarp + kSrcWarps) * 32;
+  // Two teams take the pages in turn; each has two warps for K and two for V.
+  static constexpr int kKWarps = 2, kVWarps = 2, kTeams = 2;
+  static constexpr int kTurnWarp = (Cfg::kSrcWarp + 4) / 4 * 4;  // the teams' first warp, behind the one that loads
+  static constexpr int kThreads = (kTurnWarp + kTeams * (kKWarps + kVWarps)) * 32;
+  static_assert(kRaw % 2 == 0 && Cfg::NK % 2 == 0 && Cfg::NV % 2 == 0, "a stage is one team's");
   static constexpr int kKArrivals = kKWarps, kVArrivals = kVWarps;
   static constexpr int kBars = 2 * kRaw;  // pages there, pages read
   static __device__ __forceinline__ uint32_t bar_count(int i) { return i < kRaw ? 1 : kKWarps + kVWarps; }
-  static constexpr bool kPairedV = true, kOutF16 = F16;
+  static constexpr bool kPairedV = true, kOutF16 = F16, kScaledQ = true;
   static constexpr int kSmem = Cfg::kSrcOff + kRaw * kPageBytes + 1024;
   static_assert(kSmem <= 232448 - 4096, "shared memory");
+
+  static __device__ __forceinline__ float largest(uint4 v) {  // magnitude of eight values
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack2<F16>(w[k]);
+      a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+    return a;
+  }
 
   struct Params {
     RowParams r;
@@ -90,6 +104,7 @@ struct TreeSrc {
   // Keys len, of which the last `nodes` are the drafted ones; tiles: pages that hold sinks, then those from lo on.
   struct Seq {
     int blocks, tiles, len, base, nodes, n_sink, lo;
+    Seq() = default;
     __device__ __forceinline__ Seq(const Params& p, int b) {
       len = max(0, min(p.lens[b], p.max_pages * kTile));
       nodes = max(0, min(p.nodes ? p.nodes[b] : p.r.Nq, min(p.r.Nq, len)));
@@ -109,60 +124,41 @@ struct TreeSrc {
 
   struct Row {
     bool valid;
-    int out_row, head, pos;
+    int out_row, pos, depth;
     float c2, v_scale;
-    int depth;
-    long long depth_row;
-    const uint32_t* bits;
     __device__ __forceinline__ void set(const Params& p, const Seq& s, int b, int h, int P) {
       const int G = p.r.G();
       pos = P / G;
-      head = h * G + P % G;
       valid = pos < s.nodes;
-      out_row = pos < p.r.Nq ? (b * p.r.Hq + head) * p.r.Nq + pos : -1;
-      bits = p.mask + b * p.mask_stride + (long long)pos * p.words;
-      depth_row = b * p.depth_stride;
+      out_row = pos < p.r.Nq ? (b * p.r.Hq + h * G + P % G) * p.r.Nq + pos : -1;
       depth = valid && p.depths ? max(0, min(p.depths[b * p.depth_stride + pos], p.r.Nq - 1)) : 0;
     }
-    float up;  // the power of two that brings the row's largest value to 2^14 .. 2^16
-    __device__ __forceinline__ void scale(const Params& p, int h, const uint16_t* src) {
-      float amax = 0.f;
-      if (src) {
-#pragma unroll 4
-        for (int c = 0; c < D; c += 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + c);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack2<F16>(w[k]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-      }
+    // The row's factors; returns the power of two that brings its largest magnitude to 2^14 .. 2^16.
+    __device__ __forceinline__ float scale(const Params& p, int h, float amax) {
       int e = (int)((__float_as_uint(amax) >> 23) & 255) - 127;
       e = max(-100, min(126, e));
-      up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
       const float down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
       // (a positive finite number, so that a masked score stays -inf and a key of zeros 0)
       const float f = down * (p.k_scale[h] * kLog2e * rsqrtf((float)D));
       c2 = f < FLT_MIN ? FLT_MIN : f > FLT_MAX ? FLT_MAX : f;
       v_scale = p.v_scale[h];
+      return __uint_as_float((uint32_t)(127 + 14 - e) << 23);
     }
     __device__ __forceinline__ void scale_v(const Params& p, int h) { v_scale = p.v_scale[h]; }
-    __device__ __forceinline__ uint32_t convert(uint32_t w) const {
+    __device__ __forceinline__ uint32_t convert(uint32_t w, float up) const {
       const float2 f = unpack2<F16>(w);
       return pack2<true>(f.x * up, f.y * up);
     }
-    // which of the keys j .. j + 31 the row sees
-    __device__ __forceinline__ uint32_t sees(const Params& p, const Seq& s, int j) const {
-      if (!valid) return 0u;
+    // which of the keys j .. j + 31 of sequence b the row sees (out of line: few tiles need it)
+    static __device__ __noinline__ uint32_t sees(const Params& p, const Seq& s, int b, int pos, int depth, int j) {
       auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
       uint32_t ctx = below(s.base - j), drafted = 0u;
       const int at = j - s.base;  // node of key j
       if (at > -32 && at < s.nodes) {
+        const uint32_t* bits = p.mask + b * p.mask_stride + (long long)pos * p.words;
         const int w = at >> 5, sh = at & 31;  // (at = -1: word -1, shifted by 31)
-        const uint32_t a = w >= 0 ? bits[w] : 0u, c = w + 1 < p.words ? bits[w + 1] : 0u;
-        drafted = __funnelshift_r(a, c, sh) & below(s.nodes - at) & ~ctx;
+        const uint32_t lo = w >= 0 ? bits[w] : 0u, hi = w + 1 < p.words ? bits[w + 1] : 0u;
+        drafted = __funnelshift_r(lo, hi, sh) & below(s.nodes - at) & ~ctx;
       }
       if (p.window) {
         const int first = s.base + depth - p.window + 1;  // the window's first position
@@ -170,41 +166,40 @@ struct TreeSrc {
         if (p.window < p.r.Nq)  // only then may a drafted key lie behind it
           for (uint32_t x = drafted; x; x &= x - 1) {
             const int k = __ffs(x) - 1;
-            const int pk = s.base + max(0, min(p.depths[depth_row + at + k], p.r.Nq - 1));
+            const int pk = s.base + max(0, min(p.depths[b * p.depth_stride + at + k], p.r.Nq - 1));
             if (pk < first && pk >= p.sinks) drafted &= ~(1u << k);
           }
       }
       return ctx | drafted;
     }
+    // which of a tile's keys the row sees, in words of 32
     template <int N>
-    __device__ __forceinline__ void mask(const Params& p, const Seq& s, int tile, float* sv) const {
-      const int j0 = s.page(tile) * kTile;
+    __device__ __forceinline__ void mask(const Params& p, const RowWalk<TreeSrc>& walk, int tile, uint32_t* vis) const {
+      const Seq& s = walk.seq;
+      const int j0 = s.page(walk.g.t0 + tile) * kTile;
       // all rows see all keys?
-      if (j0 + N <= s.base && (!p.window || j0 + N <= p.sinks || j0 > s.base + p.r.Nq - 1 - p.window) &&
-          __all_sync(0xffffffffu, valid))
-        return;
+      if (j0 + 32 * N <= s.base && (!p.window || j0 + 32 * N <= p.sinks || j0 > s.base + p.r.Nq - 1 - p.window)) {
 #pragma unroll
-      for (int c = 0; c < N; c += 32) {
-        const uint32_t v = sees(p, s, j0 + c);
+        for (int c = 0; c < N; ++c) vis[c] = valid ? ~0u : 0u;
+      } else {
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (!((v >> k) & 1u)) sv[c + k] = -INFINITY;
+        for (int c = 0; c < N; ++c) vis[c] = valid ? sees(p, s, walk.g.b, pos, depth, j0 + 32 * c) : 0u;
       }
     }
   };
 
-  template <class Walk, class Bars>
-  static __device__ __forceinline__ void produce(const Params& p, Walk& walk, uint8_t* smem, uint32_t sbase,
+  template <class Bars>
+  static __device__ __forceinline__ void produce(const Params& p, RowWalk<TreeSrc>& walk, uint8_t* smem, uint32_t sbase,
                                                  const Bars& bars, int warp, int lane) {
     using C = Cfg;
     auto raw_full = [&](int T) { return bars.at(Bars::kNum + T % kRaw); };
     auto raw_empty = [&](int T) { return bars.at(Bars::kNum + kRaw + T % kRaw); };
-    RowSeg g;
+    const RowSeg& g = walk.g;
     int T = 0;
     bool ok = true;
     if (warp == 0) {
       // ---- pages come in
-      while (ok && walk.next(g)) {
+      while (ok && walk.next(p, lane)) {
         const uint8_t* head = p.pages + (size_t)g.h * kPageBytes;
         const int32_t* table = p.table + (size_t)g.b * p.max_pages;
         const int held = (walk.seq.len + kTile - 1) / kTile;
@@ -235,10 +230,14 @@ struct TreeSrc {
       __syncwarp();
       return;
     }
-    const bool of_k = warp <= kKWarps;
-    const int w = of_k ? warp - 1 : warp - 1 - kKWarps;
-    while (ok && walk.next(g)) {
+    warp -= kTurnWarp - C::kSrcWarp;
+    if (warp < 0) return;
+    const int team = warp / (kKWarps + kVWarps), in_team = warp % (kKWarps + kVWarps);
+    const bool of_k = in_team < kKWarps;
+    const int w = of_k ? in_team : in_team - kKWarps;
+    while (ok && walk.next(p, lane)) {
       for (int t = g.t0; t < g.t1; ++t, ++T) {
+        if (kTeams == 2 && (T & 1) != team) continue;
         const uint8_t* raw = smem + C::kSrcOff + T % kRaw * kPageBytes;
         if (!(ok = bars.warp_wait(raw_full(T), (T / kRaw) & 1))) break;
         if (of_k) {
@@ -247,7 +246,7 @@ struct TreeSrc {
           // A lane takes 32 channels (16 code bytes, two scales) of a key.  Eight neighbouring lanes store to four
           // keys and both halves of 64 channels: all banks once.
           constexpr int kQuarters = D / 32 < 4 ? D / 32 : 4, kUnits = kTile * D / 1024;
-#pragma unroll
+#pragma unroll 2
           for (int u = 0; u < kUnits / kKWarps; ++u) {
             const int unit = u * kKWarps + w;
             int key, q;
@@ -293,7 +292,7 @@ struct TreeSrc {
           const uint8_t* blk = raw + mb * blk_bytes(D);
 #pragma unroll
           for (int u = 0; u < D / 64; ++u) {
-            if (D == 64 ? (T & 1) != w : u % kVWarps != w) continue;
+            if (D == 64 ? ((T >> 1) & 1) != w : u % kVWarps != w) continue;
             uint4 code[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)

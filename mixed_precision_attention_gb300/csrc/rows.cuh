@@ -43,18 +43,23 @@ constexpr float kTauRows = 8.f;    // lazy-maximum threshold, log2 units
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinUses = 4;        // a CTA takes no fewer uses than these while others have none
 
+// x / n for x >= 0; nearly always a 32-bit division.
+__device__ __forceinline__ long long rows_quotient(long long x, int n) {
+  if (((unsigned long long)x >> 32) == 0) return (unsigned)x / (unsigned)n;
+  return x / n;
+}
 // n things in k nearly equal runs, the longer ones first.
 struct RowCut {
   long long q;
   int r, k;
   __device__ __forceinline__ RowCut(long long n, int k_) : k(k_) {
-    q = n / k;
+    q = rows_quotient(n, k);
     r = (int)(n - q * k);
   }
   __device__ __forceinline__ long long first(int i) const { return i >= k ? q * k + r : q * i + min(i, r); }
 };
 __device__ __forceinline__ int cut_ctas(long long total, int grid) {
-  const long long n = (total + kMinUses - 1) / kMinUses;
+  const long long n = rows_quotient(total + kMinUses - 1, kMinUses);
   return n < 1 ? 1 : n < grid ? (int)n : grid;
 }
 
@@ -73,8 +78,9 @@ struct RowParams {
   int* err;
   // workspace
   SplitRec* rec;    // [grid]
-  float2* part_ml;  // [2 grid][slot rows] (m, l): slots 2 cta + 1 and 2 cta are the CTA's part of the
-  float* part_o;    // [2 grid][slot rows][d]      item that ends in it, and of the one that goes on behind it
+  // Slots 2 cta + 1 and 2 cta hold the CTA's part of the item that ends in it, and of the one that goes on behind it.
+  float2* part_ml;  // [2 grid][slot rows] (m, l)
+  float* part_o;    // [2 grid][d / 4][slot rows][4], so that 32 neighbouring rows' vectors are 512 bytes in a run
   int slot_rows;
   __host__ __device__ int G() const { return Hq / Hkv; }
 };
@@ -114,16 +120,24 @@ struct RowShare {
   }
   __device__ __forceinline__ int tile(int i) const { return first + step * i; }  // counted from the segment's first
 };
-// The segments of a CTA in order; seq: the source's numbers of the last one's sequence.
-template <class Src, int kBlocks>
+// A warp's way through the segments of its CTA, in shared memory: what is the same for all its lanes, and
+// looked up now and then, does not take every lane's registers.
+template <class Src>
 struct RowWalk {
-  using Seq = typename Src::Seq;
-  const typename Src::Params& p;
-  int b, item, pos, left;  // item of the sequence, uses into it, uses left
-  Seq seq;
-  __device__ __forceinline__ RowWalk(const typename Src::Params& p_, int b_, int item_, int pos_, int left_)
-      : p(p_), b(b_), item(item_), pos(pos_), left(left_), seq(p_, b_) {}
-  __device__ __forceinline__ bool next(RowSeg& g) {
+  static constexpr int kBlocks = Src::Cfg::kBlocks;
+  using Params = typename Src::Params;
+  int b, item, pos, left;     // item of the sequence, uses into it, uses left
+  typename Src::Seq seq;      // the source's numbers of the segment's sequence
+  RowSeg g;                   // the segment
+  __device__ __forceinline__ void start(const Params& p, int b_, int item_, int pos_, int left_) {
+    b = b_;
+    item = item_;
+    pos = pos_;
+    left = left_;
+    seq = typename Src::Seq(p, b_);
+  }
+  // one lane's work
+  __device__ __noinline__ bool step(const Params& p) {
     while (left > 0) {
       int per = (seq.blocks + kBlocks - 1) / kBlocks, h = item / per, rb = (item - h * per) * kBlocks;
       int w = min(kBlocks, seq.blocks - rb);
@@ -132,7 +146,7 @@ struct RowWalk {
         if (++item == per * p.r.Hkv) {
           item = 0;
           do {
-            seq = Seq(p, ++b);
+            seq = typename Src::Seq(p, ++b);
           } while (seq.uses() == 0);
           per = (seq.blocks + kBlocks - 1) / kBlocks;
         }
@@ -147,6 +161,14 @@ struct RowWalk {
       if (g.t1 > g.t0) return true;  // (half a tile of two blocks is the next CTA's)
     }
     return false;
+  }
+  // the whole warp's
+  __device__ __forceinline__ bool next(const Params& p, int lane) {
+    __syncwarp();
+    bool any = false;
+    if (lane == 0) any = step(p);
+    __syncwarp();
+    return __any_sync(0xffffffffu, any);
   }
 };
 
@@ -242,8 +264,8 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float2 xml[NG == 2 ? 2 : 1][NG == 2 ? 128 : 1];  // two groups' (m, l) of a row
+  __shared__ RowWalk<Src> walks[Src::kThreads / 32];
   __shared__ long long warp_sum[32];
-  __shared__ long long list_total;
   __shared__ int found[2][2];             // sequence, and uses (of a head) before it: of the first and the last use
   const RowParams& r = p.r;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -269,70 +291,45 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
     tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  // ---- the list's length, then this CTA's place in it
+  // ---- the list's length, and this CTA's place in it: each thread sums up a run of sequences
   constexpr int kWarps = Src::kThreads / 32;
-  {
-    long long sum = 0;
-    for (int b = tid; b < r.B; b += Src::kThreads) {
-      const typename Src::Seq s(p, b);
-      s.report(p, b);
-      sum += s.uses();
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) warp_sum[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-      long long t = 0;
-      for (int w = 0; w < kWarps; ++w) t += warp_sum[w];
-      list_total = t * r.Hkv;
-    }
-    __syncthreads();
+  const int run = (r.B + Src::kThreads - 1) / Src::kThreads, b_lo = min(r.B, tid * run), b_hi = min(r.B, b_lo + run);
+  long long before = 0, total = 0, mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const typename Src::Seq s(p, b);
+    s.report(p, b);
+    mine += s.uses();
   }
-  const long long total = list_total;
+  {
+    long long x = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, s);
+      if (lane >= s) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    before += x - mine;
+  }
+  total *= r.Hkv;
   const RowCut cut(total, cut_ctas(total, gridDim.x));
   const long long x0 = cut.first(blockIdx.x), x1 = cut.first(blockIdx.x + 1);
-  {
-    long long carry = 0;
-    for (int b0 = 0; x1 > x0 && b0 < r.B; b0 += Src::kThreads) {
-      const int b = b0 + tid;
-      const long long n = b < r.B ? typename Src::Seq(p, b).uses() : 0;
-      long long x = n;
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, s);
-        if (lane >= s) x += y;
-      }
-      if (lane == 31) warp_sum[warp] = x;
-      __syncthreads();
-      long long before = carry, all = carry;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warp_sum[w];
-        all += warp_sum[w];
-      }
-      before += x - n;
-      for (int k = 0; k < 2; ++k) {
-        const long long at = k ? x1 - 1 : x0;
-        if (n > 0 && at >= before * r.Hkv && at < (before + n) * r.Hkv) {
+  for (int k = 0; k < 2; ++k) {
+    const long long at = k ? x1 - 1 : x0;
+    if (x1 > x0 && at >= before * r.Hkv && at < (before + mine) * r.Hkv) {
+      long long sum = before;
+      for (int b = b_lo; b < b_hi; ++b) {
+        const long long n = typename Src::Seq(p, b).uses();
+        if (at >= sum * r.Hkv && at < (sum + n) * r.Hkv) {
           found[k][0] = b;
-          found[k][1] = (int)before;
+          found[k][1] = (int)sum;
         }
-      }
-      carry = all;
-      __syncthreads();
-    }
-  }
-  // ---- rows that no item covers: zeros
-  {
-    const int R = r.G() * r.Nq;
-    for (int b = blockIdx.x; b < r.B; b += gridDim.x) {
-      const typename Src::Seq s(p, b);
-      const int from = s.uses() > 0 ? min(R, s.blocks * kBlockRows) : 0;
-      for (long long i = tid; i < (long long)(R - from) * r.Hkv * (D / 8); i += Src::kThreads) {
-        const int c = (int)(i % (D / 8)), P = from + (int)(i / (D / 8) % (R - from)), h = (int)(i / (D / 8) / (R - from));
-        const size_t row = ((size_t)b * r.Hq + h * r.G() + P % r.G()) * r.Nq + P / r.G();
-        *reinterpret_cast<uint4*>(r.out + row * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
-        if (c == 0 && r.lse) r.lse[row] = -INFINITY;
+        sum += n;
       }
     }
   }
@@ -347,11 +344,13 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
     const typename Src::Seq s(p, b);
     const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, head = (int)s.uses();
     const long long y = x - (long long)found[k][1] * r.Hkv;
-    const int h = (int)(y / head), z = (int)(y - (long long)h * head), kk = z / (C::kBlocks * s.tiles);
+    const int h = (int)rows_quotient(y, head), z = (int)(y - (long long)h * head), kk = z / (C::kBlocks * s.tiles);
     item = h * per + kk;
     pos = z - kk * C::kBlocks * s.tiles;
   };
-  if (tid == 0) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == C::kSrcWarp + 1 && lane == 0) {  // (a warp that has time)
     SplitRec rec{};
     if (x1 > x0) {
       int b, item, pos;
@@ -364,12 +363,13 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
     }
     r.rec[blockIdx.x] = rec;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   if (x1 > x0) {
-    int sb, sitem, spos;
-    place(0, x0, sb, sitem, spos);
-    RowWalk<Src, C::kBlocks> walk(p, sb, sitem, spos, (int)(x1 - x0));
+    RowWalk<Src>& walk = walks[warp];
+    if (lane == 0) {
+      int sb, sitem, spos;
+      place(0, x0, sb, sitem, spos);
+      walk.start(p, sb, sitem, spos, (int)(x1 - x0));
+    }
     if (warp >= C::kSrcWarp) {
       Src::produce(p, walk, smem, sbase, bars, warp - C::kSrcWarp, lane);
     } else if (warp >= C::kMmaWarp) {
@@ -385,10 +385,9 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
       const uint64_t kd0 = smem_desc(sbase + C::kKOff, 16, 1024, kSwizzle128B);
       const uint64_t vd0 = smem_desc(sbase + C::kVOff, KT * 128, 1024, kSwizzle128B);
       uint32_t T = 0, n = 0, qpar = 0;  // tiles before the segment; this group's uses before it
-      RowSeg sg;
       bool ok = true;
-      while (ok && __any_sync(0xffffffffu, walk.next(sg))) {
-        const int w = __shfl_sync(0xffffffffu, sg.w, 0), tiles = __shfl_sync(0xffffffffu, sg.t1 - sg.t0, 0);
+      while (ok && walk.next(p, lane)) {
+        const int w = __shfl_sync(0xffffffffu, walk.g.w, 0), tiles = __shfl_sync(0xffffffffu, walk.g.t1 - walk.g.t0, 0);
         const RowShare mine(NG, w, tiles, g, T);
         if (!(ok = bars.warp_wait(bars.at(Bars::kQ), qpar))) break;
         qpar ^= 1;
@@ -457,34 +456,61 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
       const uint32_t tl = tmem + lane_base;
       typename Src::Row me;  // this thread's row: me.valid, me.out_row (in rows, or -1), what masks and scales it
       float m2 = -INFINITY, l2 = 0.f;
-      RowSeg sg;
       // Q of a segment: both groups share the block of an item with one, a half of the channels each
-      auto put_q = [&](const RowSeg& s) {
+      auto put_q = [&]() {
+        const RowSeg& s = walk.g;
         const int buf = s.w == 2 ? g : 0;  // the block that this group's uses are of
         me.set(p, walk.seq, s.b, s.h, (s.rb + buf) * kBlockRows + row);
-        const uint16_t* src = me.valid ? r.q + s.b * r.qs_b + me.head * r.qs_h + me.pos * r.qs_r : nullptr;
-        me.scale(p, s.h, src);
-        const bool halves = NG == 2 && s.w == 1;
-        const int c_lo = halves ? g * (D / 2) : 0, c_hi = halves ? c_lo + D / 2 : D;
+        const uint16_t* src = nullptr;
+        if (me.valid) {
+          const int P = (s.rb + buf) * kBlockRows + row, G = r.G();
+          src = r.q + s.b * r.qs_b + (s.h * G + P % G) * r.qs_h + (P / G) * r.qs_r;
+        }
+        // (as much of the row at once as registers allow, so that its loads are under way together)
+        constexpr int kMost = Src::kThreads > 512 ? 8 : 16, kVecs = D / 8 < kMost ? D / 8 : kMost;
+        uint4 qv[kVecs];
+        auto load_q = [&](int c0) {
+#pragma unroll
+          for (int k = 0; k < kVecs; ++k)
+            qv[k] = src ? *reinterpret_cast<const uint4*>(src + c0 + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        float amax = 0.f;
+        if constexpr (Src::kScaledQ) {
 #pragma unroll 1
-        for (int c = c_lo; c < c_hi; c += 32) {
-          uint32_t w[16];
+          for (int c0 = D - 8 * kVecs; c0 >= 0; c0 -= 8 * kVecs) {  // (the first half last: it stays)
+            load_q(c0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 v = src ? *reinterpret_cast<const uint4*>(src + c + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
-            w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+            for (int k = 0; k < kVecs; ++k) amax = fmaxf(amax, Src::largest(qv[k]));
           }
+        } else {
+          load_q(0);
+        }
+        const float up = me.scale(p, s.h, amax);
+        const bool halves = NG == 2 && s.w == 1;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = me.convert(w[k]);
-          if constexpr (C::QT) {
-            tmem_st_x16(tl + C::kQCol + buf * (D / 2) + c / 2, w);
-          } else {
+        for (int c0 = 0; c0 < D; c0 += 8 * kVecs) {
+          if (c0 > 0) load_q(c0);
+#pragma unroll
+          for (int c = 0; c < kVecs; c += 4) {  // 32 channels
+            if (halves && (c0 + 8 * c >= D / 2) != (g == 1)) continue;
+            uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int ch = c / 8 + k;
-              *reinterpret_cast<uint4*>(smem + C::kQOff + buf * C::kQBytes + (ch >> 3) * 16384 + row * 128 +
-                                        (((ch & 7) ^ (row & 7)) << 4)) =
-                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              w[4 * k] = me.convert(qv[c + k].x, up);
+              w[4 * k + 1] = me.convert(qv[c + k].y, up);
+              w[4 * k + 2] = me.convert(qv[c + k].z, up);
+              w[4 * k + 3] = me.convert(qv[c + k].w, up);
+            }
+            if constexpr (C::QT) {
+              tmem_st_x16(tl + C::kQCol + buf * (D / 2) + c0 / 2 + 4 * c, w);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int ch = c0 / 8 + c + k;
+                *reinterpret_cast<uint4*>(smem + C::kQOff + buf * C::kQBytes + (ch >> 3) * 16384 + row * 128 +
+                                          (((ch & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              }
             }
           }
         }
@@ -497,43 +523,54 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.at(Bars::kQ));
       };
-      // before the segment: tiles, each group's uses and commits of P V; exchanges of two states, segments
-      int T = 0, n[2] = {0, 0}, npv[2] = {0, 0}, npv2 = 0, nx = 0, nseg = 0;
-      bool ok = true;
-      bool any = walk.next(sg);
-      if (any) put_q(sg);
+      // Parities: tiles before the segment, segments, each group's commits of P V, this group's of the last but one,
+      // exchanges of two states; and this group's uses before the segment.
+      constexpr uint32_t kParT = 1, kParSeg = 2, kParPV = 4, kParPV2 = 16, kParX = 32;
+      uint32_t par = 0;
+      int n = 0;
+      bool ok = true, any = walk.next(p, lane);
+      if (any) put_q();
       while (any) {
-        const int tiles = sg.t1 - sg.t0, w = sg.w;
-        const RowShare share(NG, w, tiles, g, T);
+        const int tiles = walk.g.t1 - walk.g.t0, w = walk.g.w;
+        const RowShare share(NG, w, tiles, g, par & kParT);
         const bool warp_idle = !__any_sync(0xffffffffu, me.valid);
         m2 = -INFINITY;
         l2 = 0.f;
         for (int i = 0; i < share.uses; ++i) {
-          const int v = n[g] + i, buf = v % C::NB, tile = sg.t0 + share.tile(i);
-          if (!(ok = bars.warp_wait(bars.at(Bars::kS + g * C::NB + buf), (v / C::NB) & 1))) break;
+          const int buf = (n + i) % C::NB;
+          uint32_t vis[KT / 32];
+          me.template mask<KT / 32>(p, walk, share.tile(i), vis);
+          if (!(ok = bars.warp_wait(bars.at(Bars::kS + g * C::NB + buf), ((n + i) / C::NB) & 1))) break;
           const uint32_t scol = tl + C::kSCol + (g * C::NB + buf) * KT, pcol = scol + C::kPOff;
           if (warp_idle) {  // (rows of P that nobody uses: whatever is there)
             if (lane == 0) mbar_arrive(bars.at(Bars::kP + g * C::NB + buf));
             continue;
           }
           tc_fence_after();
-          uint32_t raw[KT];
+          // 32 keys at a time, so that few registers are live; the first 32 are loaded again after the maximum
+          float sv[32], rmax = -INFINITY;
+          auto load = [&](int c) {
+            uint32_t raw[32];
+            tmem_ld_x32(scol + 32 * c, raw);
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < KT; c += 32) tmem_ld_x32(scol + c, raw + c);
-          tmem_wait_ld();
-          float sv[KT];
+            for (int k = 0; k < 32; ++k) sv[k] = __uint_as_float(raw[k]);
+            if (__any_sync(0xffffffffu, vis[c] != ~0u)) {
 #pragma unroll
-          for (int c = 0; c < KT; ++c) sv[c] = __uint_as_float(raw[c]);
-          me.template mask<KT>(p, walk.seq, tile, sv);
-          float g8[KT / 8];
+              for (int k = 0; k < 32; ++k)
+                if (!((vis[c] >> k) & 1u)) sv[k] = -INFINITY;
+            }
+          };
 #pragma unroll
-          for (int c = 0; c < KT / 8; ++c)
-            g8[c] = max3(max3(sv[8 * c], sv[8 * c + 1], sv[8 * c + 2]), max3(sv[8 * c + 3], sv[8 * c + 4], sv[8 * c + 5]),
-                         fmaxf(sv[8 * c + 6], sv[8 * c + 7]));
-          float rmax = g8[0];
+          for (int c = 0; c < KT / 32; ++c) {
+            load(c);
+            float g8[4];
 #pragma unroll
-          for (int c = 1; c + 1 < KT / 8; c += 2) rmax = max3(rmax, g8[c], g8[c + 1]);
-          rmax = fmaxf(rmax, g8[KT / 8 - 1]);
+            for (int k = 0; k < 4; ++k)
+              g8[k] = max3(max3(sv[8 * k], sv[8 * k + 1], sv[8 * k + 2]), max3(sv[8 * k + 3], sv[8 * k + 4], sv[8 * k + 5]),
+                           fmaxf(sv[8 * k + 6], sv[8 * k + 7]));
+            rmax = fmaxf(rmax, max3(max3(g8[0], g8[1], g8[2]), g8[3], g8[3]));
+          }
           const float top = rmax * me.c2;  // (c2 > 0)
           float f = 1.f;
           bool rescale = false;
@@ -548,11 +585,11 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
           const float nb = m2 == -INFINITY ? 0.f : C::kLift - m2;
           float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < KT / 32; ++c) {
+          for (int c = KT / 32 - 1; c >= 0; --c) {
+            if (c < KT / 32 - 1) load(c);
             uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              rows_p8<C::F16>(sv + 32 * c + 8 * k, me.c2, nb, pk + 4 * k, ps[k & 1], ps[2 + (k & 1)]);
+            for (int k = 0; k < 4; ++k) rows_p8<C::F16>(sv + 8 * k, me.c2, nb, pk + 4 * k, ps[k & 1], ps[2 + (k & 1)]);
             tmem_st_x16(pcol + 16u * c, pk);
           }
           l2 = l2 * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
@@ -560,8 +597,9 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
             // This S came behind P V of use i - NB.  With two buffers, that of use i - 1 has to land: the S behind it
             // says so, or its own commit.
             if (C::NB == 2 && i > 0) {
-              if (!(ok = i + 1 < share.uses ? bars.warp_wait(bars.at(Bars::kS + g * C::NB + (buf ^ 1)), ((v + 1) / C::NB) & 1)
-                                            : bars.warp_wait(bars.at(Bars::kPV2 + g), npv2 & 1)))
+              if (!(ok = i + 1 < share.uses
+                             ? bars.warp_wait(bars.at(Bars::kS + g * C::NB + (buf ^ 1)), ((n + i + 1) / C::NB) & 1)
+                             : bars.warp_wait(bars.at(Bars::kPV2 + g), par & kParPV2 ? 1 : 0)))
                 break;
             }
             tc_fence_after();
@@ -584,27 +622,22 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
         }
         if (!ok) break;
         // ---- the next segment's Q, once every S of this one is done; then this one's epilogue
-        const typename Src::Row mine = me;
-        const RowSeg done = sg;
+        const int out_row = me.out_row;
+        const float v_scale = me.v_scale;
+        const bool whole = walk.g.t0 == 0 && walk.g.t1 == walk.g.n, ends = walk.g.t1 == walk.g.n;
         if (NG == 2) {
           if ((warp & 3) == 0 && lane == 0) mbar_arrive(bars.at(Bars::kQFree));
-          if (!(ok = bars.warp_wait(bars.at(Bars::kQFree), nseg & 1))) break;
+          if (!(ok = bars.warp_wait(bars.at(Bars::kQFree), par & kParSeg ? 1 : 0))) break;
         }
-        ++nseg;
-        int uses[2];
-#pragma unroll
-        for (int k = 0; k < NG; ++k) uses[k] = RowShare(NG, w, tiles, k, T).uses;
-        any = walk.next(sg);
-        if (any) {
-          put_q(sg);
-        }
+        any = walk.next(p, lane);
+        if (any) put_q();
         const bool joint = NG == 2 && w == 1;  // the groups' states belong to the same rows
         float f0 = 1.f, f1 = 0.f;  // of this group's O, and the other's
         if (joint) {
           xml[g][row] = make_float2(m2, l2);
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.at(Bars::kX));
-          if (!(ok = bars.warp_wait(bars.at(Bars::kX), nx & 1))) break;
+          if (!(ok = bars.warp_wait(bars.at(Bars::kX), par & kParX ? 1 : 0))) break;
           const float2 y = xml[g ^ 1][row];
           const float M = fmaxf(m2, y.x);
           f0 = l2 == 0.f ? 0.f : ex2_approx(m2 - M);  // (a NaN sum goes on to the output)
@@ -612,46 +645,49 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
           l2 = g == 0 ? f0 * l2 + f1 * y.y : f1 * y.y + f0 * l2;
           m2 = M;
         }
+        bool has_own = true, has_other = false;
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          if (ok && uses[k] > 0 && (joint || k == g)) ok = bars.warp_wait(bars.at(Bars::kPV + k), npv[k] & 1);
-          npv[k] += uses[k] > 0;
-          n[k] += uses[k];
+          const int uses = RowShare(NG, w, tiles, k, par & kParT).uses;
+          if (k == g)
+            has_own = uses > 0;
+          else
+            has_other = joint && uses > 0;
+          if (ok && uses > 0 && (joint || k == g)) ok = bars.warp_wait(bars.at(Bars::kPV + k), par & (kParPV << k) ? 1 : 0);
+          if (uses > 0) par ^= kParPV << k;
         }
-        npv2 += C::NB == 2 && share.uses > 1;
         if (!ok) break;
         tc_fence_after();
-        const bool whole = done.t0 == 0 && done.t1 == done.n;
-        const size_t prow = (size_t)(2 * blockIdx.x + (done.t1 == done.n ? 1 : 0)) * r.slot_rows + (w == 2 ? g * kBlockRows : 0) + row;
-        const float inv = l2 == 0.f ? 0.f : mine.v_scale / l2;
+        const int slot = 2 * blockIdx.x + (ends ? 1 : 0), prow = (w == 2 ? g * kBlockRows : 0) + row;
+        float* part = r.part_o + (size_t)slot * r.slot_rows * D + 4 * prow;
+        const float inv = l2 == 0.f ? 0.f : v_scale / l2;
         const uint32_t own = tl + C::kOCol + g * D, other = tl + C::kOCol + (NG == 2 ? (g ^ 1) * D : 0);
         const int c_lo = joint ? g * (D / 2) : 0, c_hi = joint ? c_lo + D / 2 : D;
-        const bool has_own = share.uses > 0, has_other = joint && uses[NG - 1 - g] > 0;
-        if (__any_sync(0xffffffffu, mine.out_row >= 0)) {
+        if (__any_sync(0xffffffffu, out_row >= 0)) {
 #pragma unroll 1
-          for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-            float o[32];
+          for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
+            float o[16];
             {
-              uint32_t x[32];
+              uint32_t x[16];
               if (has_own) {
-                tmem_ld_x32(own + c0, x);
+                tmem_ld_x16(own + c0, x);
                 tmem_wait_ld();
               }
 #pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = has_own && l2 != 0.f && f0 != 0.f ? __uint_as_float(x[c]) * f0 : 0.f;
+              for (int c = 0; c < 16; ++c) o[c] = has_own && l2 != 0.f && f0 != 0.f ? __uint_as_float(x[c]) * f0 : 0.f;
               if (has_other) {
-                tmem_ld_x32(other + c0, x);
+                tmem_ld_x16(other + c0, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
+                for (int c = 0; c < 16; ++c)
                   if (f1 != 0.f) o[c] += __uint_as_float(x[c]) * f1;
               }
             }
-            if (mine.out_row >= 0) {
+            if (out_row >= 0) {
               if (whole) {
-                uint4* dst = reinterpret_cast<uint4*>(r.out + (size_t)mine.out_row * D + c0);
+                uint4* dst = reinterpret_cast<uint4*>(r.out + (size_t)out_row * D + c0);
 #pragma unroll
-                for (int c = 0; c < 32; c += 8) {
+                for (int c = 0; c < 16; c += 8) {
                   uint4 y;
                   uint32_t* yw = &y.x;
 #pragma unroll
@@ -660,29 +696,54 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
                   dst[c / 8] = y;
                 }
               } else {
-                float4* dst = reinterpret_cast<float4*>(r.part_o + prow * D + c0);
 #pragma unroll
-                for (int c = 0; c < 32; c += 4)
-                  dst[c / 4] = make_float4(o[o_column<Src>(c)], o[o_column<Src>(c + 1)], o[o_column<Src>(c + 2)],
-                                           o[o_column<Src>(c + 3)]);
+                for (int c = 0; c < 16; c += 4)
+                  *reinterpret_cast<float4*>(part + (size_t)(c0 + c) * r.slot_rows) =
+                      make_float4(o[o_column<Src>(c)], o[o_column<Src>(c + 1)], o[o_column<Src>(c + 2)], o[o_column<Src>(c + 3)]);
               }
             }
           }
-          if (mine.out_row >= 0 && (!joint || g == 0)) {
+          if (out_row >= 0 && (!joint || g == 0)) {
             if (!whole)
-              r.part_ml[prow] = make_float2(m2, l2);
+              r.part_ml[(size_t)slot * r.slot_rows + prow] = make_float2(m2, l2);
             else if (r.lse)
-              r.lse[mine.out_row] = l2 == 0.f ? -INFINITY : kLn2 * (m2 - C::kLift + log2f(l2));
+              r.lse[out_row] = l2 == 0.f ? -INFINITY : kLn2 * (m2 - C::kLift + log2f(l2));
           }
         }
         if (joint) {  // no P of the next segment before both groups have read both states
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.at(Bars::kXDone));
-          if (!(ok = bars.warp_wait(bars.at(Bars::kXDone), nx & 1))) break;
-          ++nx;
+          if (!(ok = bars.warp_wait(bars.at(Bars::kXDone), par & kParX ? 1 : 0))) break;
+          par ^= kParX;
         }
-        T += tiles;
+        if (C::NB == 2 && share.uses > 1) par ^= kParPV2;
+        if (tiles & 1) par ^= kParT;
+        par ^= kParSeg;
+        n += share.uses;
+      }
+    }
+  }
+
+  if (warp == C::kSrcWarp + 1) {
+    // ---- rows that no item covers: zeros, every CTA's warp its share of them
+    const int R = r.G() * r.Nq;
+    for (int b0 = 0; b0 < r.B; b0 += 32) {
+      int from = R;
+      if (b0 + lane < r.B) {
+        const typename Src::Seq s(p, b0 + lane);
+        from = s.uses() > 0 ? min(R, s.blocks * kBlockRows) : 0;
+      }
+      for (unsigned todo = __ballot_sync(0xffffffffu, from < R); todo; todo &= todo - 1) {
+        const int k = __ffs(todo) - 1, b = b0 + k, first = __shfl_sync(0xffffffffu, from, k);
+        const long long n = (long long)(R - first) * r.Hkv * (D / 8);
+        for (long long i = blockIdx.x * 32 + lane; i < n; i += gridDim.x * 32) {
+          const long long y = rows_quotient(i, D / 8);
+          const int c = (int)(i % (D / 8)), h = (int)rows_quotient(y, R - first), P = first + (int)(y - (long long)h * (R - first));
+          const size_t row = ((size_t)b * r.Hq + h * r.G() + P % r.G()) * r.Nq + P / r.G();
+          *reinterpret_cast<uint4*>(r.out + row * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+          if (c == 0 && r.lse) r.lse[row] = -INFINITY;
+        }
       }
     }
   }
@@ -696,85 +757,72 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x of the first kernel and goes on behind it,
-// in order: a warp per row, a vector of channels per lane.
+// in order: a warp takes 32 rows, one per lane, and 16 channels of them.
 constexpr int kRowJoinThreads = 256;
 template <class Src>
 __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid_constant__ typename Src::Params p, int ctas) {
   using C = typename Src::Cfg;
-  constexpr int D = C::D;
-  constexpr int kVec = D / 32 < 4 ? D / 32 : 4, kVecs = D / (32 * kVec);  // a lane's channels: kVecs vectors
+  constexpr int D = C::D, kCols = D / 16, kAhead = 4;  // parts whose loads are under way together
   const RowParams& r = p.r;
-  const int lane = threadIdx.x & 31, row = blockIdx.y * (kRowJoinThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, task = blockIdx.y * (kRowJoinThreads / 32) + (threadIdx.x >> 5);
+  const int row = task / kCols * 32 + lane, c0 = task % kCols * 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SplitRec rec = r.rec[blockIdx.x];
-  if (rec.n == 0 || row >= rec.w * kBlockRows) return;
+  if (rec.n == 0 || task / kCols * 32 >= rec.w * kBlockRows) return;
+  const RowCut cut(rec.total, cut_ctas(rec.total, ctas));
+  const long long uses = (long long)rec.n * rec.w;
+  float acc[16], M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+  for (int cta = blockIdx.x; cut.first(cta) - rec.first < uses; cta += kAhead) {
+    float2 ml[kAhead];
+    float4 o[kAhead][4];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      // the tiles t0 .. t1-1 of CTA cta + k
+      const long long a = cut.first(cta + k) - rec.first, e = cut.first(cta + k + 1) - rec.first;
+      const int t0 = a <= 0 ? 0 : (int)((a < uses ? a : uses) >> (rec.w - 1)), t1 = (int)((e < uses ? e : uses) >> (rec.w - 1));
+      if (t0 == 0 && t1 == rec.n) return;  // it has the item alone, and wrote it
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t1 > t0) {
+        const size_t slot = 2 * (size_t)(cta + k) + (t1 == rec.n ? 1 : 0);
+        ml[k] = r.part_ml[slot * r.slot_rows + row];
+        const float* src = r.part_o + slot * r.slot_rows * D + 4 * row;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[k][c] = *reinterpret_cast<const float4*>(src + (size_t)(c0 + 4 * c) * r.slot_rows);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const float mx = fmaxf(M, ml[k].x);
+      const float fo = L == 0.f ? 0.f : ex2_approx(M - mx);
+      const float f = ml[k].y == 0.f ? 0.f : ex2_approx(ml[k].x - mx);  // (a NaN sum goes on to the output)
+      M = mx;
+      L = f == 0.f ? L * fo : fmaf(f, ml[k].y, L * fo);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // (a part without weight may hold anything)
+        acc[4 * c] = f == 0.f ? acc[4 * c] * fo : fmaf(f, o[k][c].x, acc[4 * c] * fo);
+        acc[4 * c + 1] = f == 0.f ? acc[4 * c + 1] * fo : fmaf(f, o[k][c].y, acc[4 * c + 1] * fo);
+        acc[4 * c + 2] = f == 0.f ? acc[4 * c + 2] * fo : fmaf(f, o[k][c].z, acc[4 * c + 2] * fo);
+        acc[4 * c + 3] = f == 0.f ? acc[4 * c + 3] * fo : fmaf(f, o[k][c].w, acc[4 * c + 3] * fo);
+      }
+    }
+  }
   const typename Src::Seq seq(p, rec.b);
   typename Src::Row me;
   me.set(p, seq, rec.b, rec.h, rec.rb * kBlockRows + row);
   if (me.out_row < 0) return;
-  const RowCut cut(rec.total, cut_ctas(rec.total, ctas));
-  const long long end = rec.first + (long long)rec.n * rec.w;
-  // the tiles t0 .. t1-1 of CTA c
-  auto tiles_of = [&](int c, int& t0, int& t1) {
-    const long long a = cut.first(c) - rec.first, e = cut.first(c + 1) - rec.first;
-    t0 = a <= 0 ? 0 : (int)((a < end - rec.first ? a : end - rec.first) / rec.w);
-    t1 = (int)((e < end - rec.first ? e : end - rec.first) / rec.w);
-  };
-  float acc[kVecs][kVec], M = -INFINITY, L = 0.f;
-#pragma unroll
-  for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) acc[v][k] = 0.f;
-  for (int c0 = blockIdx.x; cut.first(c0) < end; c0 += 32) {
-    float2 ml = make_float2(-INFINITY, 0.f);
-    int t0 = 0, t1 = 0;
-    size_t prow = 0;
-    if (cut.first(c0 + lane) < end) tiles_of(c0 + lane, t0, t1);
-    if (__any_sync(0xffffffffu, t0 == 0 && t1 == rec.n)) return;  // one CTA has it all, and wrote it
-    if (t1 > t0) {
-      prow = (size_t)(2 * (c0 + lane) + (t1 == rec.n ? 1 : 0)) * r.slot_rows + row;
-      ml = r.part_ml[prow];
-    }
-    float mx = fmaxf(M, ml.x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const float fo = L == 0.f ? 0.f : ex2_approx(M - mx);
-    const float f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - mx);  // (a NaN sum goes on to the output)
-    M = mx;
-    L *= fo;
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) acc[v][k] *= fo;
-    const int here = __popc(__ballot_sync(0xffffffffu, cut.first(c0 + lane) < end));
-#pragma unroll 8
-    for (int i = 0; i < here; ++i) {  // (the loads do not wait for the weights; a part without weight may hold anything)
-      const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, ml.y, i);
-      const float* src = r.part_o + __shfl_sync(0xffffffffu, prow, i) * D;
-      L = fi == 0.f ? L : fmaf(fi, li, L);
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        float y[kVec];
-#pragma unroll
-        for (int k = 0; k < kVec; k += 2) {
-          const float2 z = *reinterpret_cast<const float2*>(src + (32 * v + lane) * kVec + k);
-          y[k] = z.x;
-          y[k + 1] = z.y;
-        }
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) acc[v][k] = fi == 0.f ? acc[v][k] : fmaf(fi, y[k], acc[v][k]);
-      }
-    }
-  }
   me.scale_v(p, rec.h);
   const float inv = L == 0.f ? 0.f : me.v_scale / L;
+  uint32_t y[8];
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(r.out + (size_t)me.out_row * D + (32 * v + lane) * kVec);
-#pragma unroll
-    for (int k = 0; k < kVec; k += 2) dst[k / 2] = pack2<Src::kOutF16>(acc[v][k] * inv, acc[v][k + 1] * inv);
-  }
-  if (lane == 0 && r.lse) r.lse[me.out_row] = L == 0.f ? -INFINITY : kLn2 * (M - C::kLift + log2f(L));
+  for (int k = 0; k < 8; ++k) y[k] = pack2<Src::kOutF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  uint4* dst = reinterpret_cast<uint4*>(r.out + (size_t)me.out_row * D + c0);
+  dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  if (c0 == 0 && r.lse) r.lse[me.out_row] = L == 0.f ? -INFINITY : kLn2 * (M - C::kLift + log2f(L));
 }
 
 __host__ inline size_t rows_align(size_t x) { return (x + 255) / 256 * 256; }
@@ -814,7 +862,8 @@ cudaError_t launch_rows(typename Src::Params prm, void* ws, cudaStream_t stream)
   rows_kernel<Src><<<kRowCtas, Src::kThreads, Src::kSmem, stream>>>(prm);
   if ((e = cudaGetLastError())) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kRowCtas, (unsigned)((r.slot_rows < rows ? r.slot_rows : rows) + 7) / 8);
+  const int most = r.slot_rows < rows ? r.slot_rows : rows;
+  cfg.gridDim = dim3(kRowCtas, (unsigned)((most + 31) / 32 * (D / 16) + 7) / 8);
   cfg.blockDim = dim3(kRowJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
