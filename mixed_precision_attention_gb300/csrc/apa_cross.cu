@@ -18,25 +18,31 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-template <int D, bool F16>
+// kTwo: items of up to two blocks, else of one.
+template <int D, bool F16, bool kTwo>
 struct CrossPick;
 template <bool F16>
-struct CrossPick<64, F16> { using Cfg = RowCfg<64, 64, 2, true, 8, 8, F16>; };
+struct CrossPick<64, F16, true> { using Cfg = RowCfg<64, 64, 2, 2, true, 8, 8, F16>; };
 template <bool F16>
-struct CrossPick<128, F16> { using Cfg = RowCfg<128, 64, 2, false, 4, 4, F16>; };
+struct CrossPick<64, F16, false> { using Cfg = RowCfg<64, 64, 1, 2, true, 6, 6, F16>; };
 template <bool F16>
-struct CrossPick<256, F16> { using Cfg = RowCfg<256, 64, 2, true, 3, 3, F16>; };
+struct CrossPick<128, F16, true> { using Cfg = RowCfg<128, 64, 2, 2, false, 4, 4, F16>; };
+template <bool F16>
+struct CrossPick<128, F16, false> { using Cfg = RowCfg<128, 64, 1, 1, true, 3, 3, F16>; };
+template <bool F16>
+struct CrossPick<256, F16, false> { using Cfg = RowCfg<256, 64, 1, 2, true, 3, 3, F16>; };
 
-template <int D, bool F16>
+template <int D, bool F16, bool kTwo>
 struct CrossSrc {
-  using Cfg = typename CrossPick<D, F16>::Cfg;
+  using Cfg = typename CrossPick<D, F16, kTwo>::Cfg;
   static constexpr int kSrcWarps = 2, kThreads = (Cfg::kSrcWarp + kSrcWarps) * 32;
   static constexpr int kKArrivals = 1, kVArrivals = 1;
+  static constexpr bool kVFirst = true;  // stages of V go back before S is issued: the copies behind them are long
   static constexpr int kBars = Cfg::NV;  // per stage of V: a last tile has landed, values behind the end and all
   static __device__ __forceinline__ uint32_t bar_count(int) { return 1; }
   static constexpr bool kPairedV = false, kOutF16 = F16, kScaledQ = false;
   static constexpr int kSmem = Cfg::kSrcOff + 1024;
-  static_assert(kSmem <= 232448 - 4096, "shared memory");
+  static_assert(Cfg::kCtasPerSm * (kSmem + 4096 + 1024) <= 233472, "shared memory");
 
   struct Params {
     RowParams r;
@@ -198,9 +204,9 @@ struct CrossArgs {
   const int32_t* lens;
   int Nkv;
 };
-template <int D, bool F16>
-cudaError_t launch_cross(const CrossArgs& a, void* ws, cudaStream_t stream) {
-  using Src = CrossSrc<D, F16>;
+template <int D, bool F16, bool kTwo>
+cudaError_t launch_cross_rows(const CrossArgs& a, void* ws, cudaStream_t stream) {
+  using Src = CrossSrc<D, F16, kTwo>;
   typename Src::Params p{};
   p.r = a.r;
   p.lens = a.lens;
@@ -213,6 +219,12 @@ cudaError_t launch_cross(const CrossArgs& a, void* ws, cudaStream_t stream) {
       !cross_map(&p.vmap, a.v, F16, a.r.B, a.r.Hkv, a.Nkv, D, a.vs[0], a.vs[1], a.vs[2], Src::Cfg::KT))
     return cudaErrorInvalidValue;
   return launch_rows<Src>(p, ws, stream);
+}
+template <int D, bool F16>
+cudaError_t launch_cross(const CrossArgs& a, void* ws, cudaStream_t stream) {
+  if constexpr (D <= 128)
+    if (rows_two_blocks(a.r.G() * a.r.Nq, D)) return launch_cross_rows<D, F16, true>(a, ws, stream);
+  return launch_cross_rows<D, F16, false>(a, ws, stream);
 }
 
 }  // namespace

@@ -39,40 +39,35 @@ __device__ __forceinline__ uint32_t tree_hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-#ifndef APA_TREE_V
-#define APA_TREE_V 0
-#endif
-template <int D>
+// kTwo: items of up to two blocks, else of one.
+template <int D, bool kTwo>
 struct TreePick;
 template <>
-struct TreePick<64> { using Cfg = RowCfg<64, 64, 2, true, 4, 4, true>; static constexpr int kRaw = 8; };
-#if APA_TREE_V == 0
+struct TreePick<64, true> { using Cfg = RowCfg<64, 64, 2, 2, true, 4, 4, true>; static constexpr int kRaw = 8; };
 template <>
-struct TreePick<128> { using Cfg = RowCfg<128, 64, 1, true, 4, 4, true>; static constexpr int kRaw = 6; };
-#else
+struct TreePick<64, false> { using Cfg = RowCfg<64, 64, 1, 2, true, 3, 3, true>; static constexpr int kRaw = 8; };
 template <>
-struct TreePick<128> { using Cfg = RowCfg<128, 64, 2, false, 4, 4, true>; static constexpr int kRaw = 2; };
-#endif
+struct TreePick<128, true> { using Cfg = RowCfg<128, 64, 2, 2, false, 2, 4, true>; static constexpr int kRaw = 4; };
 template <>
-struct TreePick<256> { using Cfg = RowCfg<256, 64, 2, true, 2, 2, true>; static constexpr int kRaw = 4; };
+struct TreePick<128, false> { using Cfg = RowCfg<128, 64, 1, 1, true, 2, 2, true>; static constexpr int kRaw = 4; };
+template <>
+struct TreePick<256, false> { using Cfg = RowCfg<256, 64, 1, 2, true, 2, 2, true>; static constexpr int kRaw = 4; };
 
-template <int D, bool F16>
+template <int D, bool F16, bool kTwo>
 struct TreeSrc {
-  using Cfg = typename TreePick<D>::Cfg;
-  static constexpr int KT = Cfg::KT, kRaw = TreePick<D>::kRaw;
+  using Cfg = typename TreePick<D, kTwo>::Cfg;
+  static constexpr int KT = Cfg::KT, kRaw = TreePick<D, kTwo>::kRaw;
   static_assert(KT == kTile, "a tile is a page");
   static constexpr int kPageBytes = page_head_bytes(D);
-  // Two teams take the pages in turn; each has two warps for K and two for V.
-  static constexpr int kKWarps = 2, kVWarps = 2, kTeams = 2;
-  static constexpr int kTurnWarp = (Cfg::kSrcWarp + 4) / 4 * 4;  // the teams' first warp, behind the one that loads
-  static constexpr int kThreads = (kTurnWarp + kTeams * (kKWarps + kVWarps)) * 32;
-  static_assert(kRaw % 2 == 0 && Cfg::NK % 2 == 0 && Cfg::NV % 2 == 0, "a stage is one team's");
+  static constexpr int kKWarps = 2, kVWarps = 2, kSrcWarps = 1 + kKWarps + kVWarps;
+  static constexpr int kThreads = (Cfg::kSrcWarp + kSrcWarps) * 32;
   static constexpr int kKArrivals = kKWarps, kVArrivals = kVWarps;
+  static constexpr bool kVFirst = false;
   static constexpr int kBars = 2 * kRaw;  // pages there, pages read
   static __device__ __forceinline__ uint32_t bar_count(int i) { return i < kRaw ? 1 : kKWarps + kVWarps; }
   static constexpr bool kPairedV = true, kOutF16 = F16, kScaledQ = true;
   static constexpr int kSmem = Cfg::kSrcOff + kRaw * kPageBytes + 1024;
-  static_assert(kSmem <= 232448 - 4096, "shared memory");
+  static_assert(Cfg::kCtasPerSm * (kSmem + 5120 + 1024) <= 233472, "shared memory");
 
   static __device__ __forceinline__ float largest(uint4 v) {  // magnitude of eight values
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -150,7 +145,7 @@ struct TreeSrc {
       return pack2<true>(f.x * up, f.y * up);
     }
     // which of the keys j .. j + 31 of sequence b the row sees (out of line: few tiles need it)
-    static __device__ __noinline__ uint32_t sees(const Params& p, const Seq& s, int b, int pos, int depth, int j) {
+    static __device__ __forceinline__ uint32_t sees(const Params& p, const Seq& s, int b, int pos, int depth, int j) {
       auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
       uint32_t ctx = below(s.base - j), drafted = 0u;
       const int at = j - s.base;  // node of key j
@@ -182,8 +177,13 @@ struct TreeSrc {
 #pragma unroll
         for (int c = 0; c < N; ++c) vis[c] = valid ? ~0u : 0u;
       } else {
+#pragma unroll 1
+        for (int c = 0; c < N; ++c) {
+          const uint32_t v = valid ? sees(p, s, walk.g.b, pos, depth, j0 + 32 * c) : 0u;
 #pragma unroll
-        for (int c = 0; c < N; ++c) vis[c] = valid ? sees(p, s, walk.g.b, pos, depth, j0 + 32 * c) : 0u;
+          for (int k = 0; k < N; ++k)
+            if (k == c) vis[k] = v;
+        }
       }
     }
   };
@@ -230,14 +230,10 @@ struct TreeSrc {
       __syncwarp();
       return;
     }
-    warp -= kTurnWarp - C::kSrcWarp;
-    if (warp < 0) return;
-    const int team = warp / (kKWarps + kVWarps), in_team = warp % (kKWarps + kVWarps);
-    const bool of_k = in_team < kKWarps;
-    const int w = of_k ? in_team : in_team - kKWarps;
+    const bool of_k = warp <= kKWarps;
+    const int w = of_k ? warp - 1 : warp - 1 - kKWarps;
     while (ok && walk.next(p, lane)) {
       for (int t = g.t0; t < g.t1; ++t, ++T) {
-        if (kTeams == 2 && (T & 1) != team) continue;
         const uint8_t* raw = smem + C::kSrcOff + T % kRaw * kPageBytes;
         if (!(ok = bars.warp_wait(raw_full(T), (T / kRaw) & 1))) break;
         if (of_k) {
@@ -292,7 +288,7 @@ struct TreeSrc {
           const uint8_t* blk = raw + mb * blk_bytes(D);
 #pragma unroll
           for (int u = 0; u < D / 64; ++u) {
-            if (D == 64 ? ((T >> 1) & 1) != w : u % kVWarps != w) continue;
+            if (D == 64 ? (T & 1) != w : u % kVWarps != w) continue;
             uint4 code[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -414,10 +410,17 @@ int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long 
     return launch_rows<Src>(p, ws, stream);
   };
   cudaError_t e = cudaErrorInvalidValue;
+  const bool two = rows_two_blocks(Hq / Hkv * Nq, d);
   switch (d) {
-    case 64: e = f16 ? go(TreeSrc<64, true>{}) : go(TreeSrc<64, false>{}); break;
-    case 128: e = f16 ? go(TreeSrc<128, true>{}) : go(TreeSrc<128, false>{}); break;
-    case 256: e = f16 ? go(TreeSrc<256, true>{}) : go(TreeSrc<256, false>{}); break;
+    case 64:
+      e = two ? (f16 ? go(TreeSrc<64, true, true>{}) : go(TreeSrc<64, false, true>{}))
+              : (f16 ? go(TreeSrc<64, true, false>{}) : go(TreeSrc<64, false, false>{}));
+      break;
+    case 128:
+      e = two ? (f16 ? go(TreeSrc<128, true, true>{}) : go(TreeSrc<128, false, true>{}))
+              : (f16 ? go(TreeSrc<128, true, false>{}) : go(TreeSrc<128, false, false>{}));
+      break;
+    case 256: e = f16 ? go(TreeSrc<256, true, false>{}) : go(TreeSrc<256, false, false>{}); break;
   }
   int st = e == cudaSuccess ? APA_OK : APA_ERR_CUDA;
   if (!workspace && cudaFreeAsync(ws, stream) != cudaSuccess && st == APA_OK) st = APA_ERR_CUDA;

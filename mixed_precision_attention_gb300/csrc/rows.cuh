@@ -37,7 +37,7 @@
 namespace apa {
 namespace {
 
-constexpr int kRowCtas = 152;      // one per SM
+constexpr int kRowSms = 152;
 constexpr int kMaxRowSeqs = 8192;
 constexpr float kTauRows = 8.f;    // lazy-maximum threshold, log2 units
 constexpr float kLn2 = 0.6931471805599453f;
@@ -85,12 +85,14 @@ struct RowParams {
   __host__ __device__ int G() const { return Hq / Hkv; }
 };
 
-template <int D_, int KT_, int NB_, bool QT_, int NK_, int NV_, bool F16_>
+template <int D_, int KT_, int NG_, int NB_, bool QT_, int NK_, int NV_, bool F16_>
 struct RowCfg {
-  static constexpr int D = D_, KT = KT_, NB = NB_;
+  static constexpr int D = D_, KT = KT_, NG = NG_, NB = NB_;
   static constexpr bool QT = QT_, F16 = F16_;
   static constexpr int NK = NK_, NV = NV_;
-  static constexpr int NG = D <= 128 ? 2 : 1;
+  // One group at d <= 128: two CTAs share an SM, and its tensor memory.
+  static constexpr int kCtasPerSm = NG == 1 && D <= 128 ? 2 : 1, kCtas = kRowSms * kCtasPerSm;
+  static constexpr uint32_t kTmemCols = 512 / kCtasPerSm;
   static constexpr int kBlocks = NG;  // row blocks of an item, at most
   static constexpr int kTileBytes = KT * D * 2;
   static constexpr int kQBytes = QT ? 0 : 128 * D * 2;  // per block
@@ -99,9 +101,12 @@ struct RowCfg {
   static constexpr int kQOff = 0, kKOff = NG * kQBytes, kVOff = kKOff + NK * kTileBytes;
   static constexpr int kSrcOff = kVOff + NV * kTileBytes;  // the source's own
   static constexpr int kSoftWarps = 4 * NG, kMmaWarp = kSoftWarps, kSrcWarp = kSoftWarps + NG;
+  // With one buffer the commit of S(i + 1) says that K of that use and V of use i have been read: a lane of the softmax
+  // group hands the stages back.  With two, V would wait for another use: the issuer's commits do.
+  static constexpr bool kSoftRelease = NB == 1;
   static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
   static_assert(NG == 1 || (NK % 2 == 0 && NV % 2 == 0), "RowShare");
-  static_assert(kQCol + (QT ? NG * D / 2 : 0) <= 512, "tensor memory");
+  static_assert(kQCol + (QT ? NG * D / 2 : 0) <= kTmemCols, "tensor memory");
 };
 
 // A CTA's run of tiles t0 .. t1-1 (of n) of one item: blocks rb .. rb+w-1 of head h of sequence b.
@@ -137,7 +142,7 @@ struct RowWalk {
     seq = typename Src::Seq(p, b_);
   }
   // one lane's work
-  __device__ __noinline__ bool step(const Params& p) {
+  __device__ __forceinline__ bool step(const Params& p) {
     while (left > 0) {
       int per = (seq.blocks + kBlocks - 1) / kBlocks, h = item / per, rb = (item - h * per) * kBlocks;
       int w = min(kBlocks, seq.blocks - rb);
@@ -172,6 +177,9 @@ struct RowWalk {
   }
 };
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 // One lane of a warp that is together.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -253,11 +261,11 @@ __device__ __forceinline__ constexpr int o_column(int c) {
 }
 
 template <class Src>
-__global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_constant__ typename Src::Params p) {
+__global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kernel(const __grid_constant__ typename Src::Params p) {
   using C = typename Src::Cfg;
   using Bars = RowBars<C>;
   constexpr int D = C::D, KT = C::KT, NG = C::NG;
-  constexpr uint32_t kTmemCols = 512;
+  constexpr uint32_t kTmemCols = C::kTmemCols;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bar_mem[Bars::kNum + Src::kBars];
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
   };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == C::kSrcWarp + 1 && lane == 0) {  // (a warp that has time)
+  if (warp == C::kMmaWarp && lane == 0) {  // (it waits for Q first of all)
     SplitRec rec{};
     if (x1 > x0) {
       int b, item, pos;
@@ -397,33 +405,38 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
         const uint32_t blk = w == 2 ? g : 0, qcol = tm + C::kQCol + blk * (D / 2);
         const uint64_t qd = qd0 + blk * (C::kQBytes >> 4);
         // P V of use i, then S of use i + NB, in whose columns that P lies: its commit says as well that this P V is done.
+        auto give_v = [&](uint32_t t) {
+          if (elected) {
+            mma_commit(bars.v_empty(t));
+            if (alone) mma_commit(bars.v_empty(t));
+          }
+          __syncwarp();
+        };
         for (int i = -C::NB; i < mine.uses; ++i) {
           const int j = i + C::NB;
           const uint32_t buf = (n + j) % C::NB;
           const uint32_t scol = tm + C::kSCol + (g * C::NB + buf) * KT;
+          const uint32_t tv = T + mine.tile(max(i, 0)), tk = T + mine.tile(j);
           if (i >= 0) {
-            const uint32_t t = T + mine.tile(i), st = t % C::NV;
             // (P first: it comes behind the end of the last segment, when all of V there has been read)
             if (!(ok = bars.warp_wait(bars.at(Bars::kP + g * C::NB + buf), ((n + i) / C::NB) & 1))) break;
-            if (!(ok = bars.warp_wait(bars.v_full(t), Bars::v_par(t)))) break;
+            if (!(ok = bars.warp_wait(bars.v_full(tv), Bars::v_par(tv)))) break;
             tc_fence_after();
-            const uint64_t vd = vd0 + st * (C::kTileBytes >> 4);
+            const uint64_t vd = vd0 + tv % C::NV * (C::kTileBytes >> 4);
             if (elected) {
               mma_f16_ts(ocol, scol + C::kPOff, vd, idO, i > 0 ? 1u : 0u);  // (the first of the segment starts O anew)
 #pragma unroll
               for (int kk = 1; kk < KT / 16; ++kk)
                 mma_f16_ts(ocol, scol + C::kPOff + 8u * kk, vd + kk * (2048 >> 4), idO, 1u);
               if (j >= mine.uses) mma_commit(bars.at((i + 1 == mine.uses ? Bars::kPV : Bars::kPV2) + g));
-              mma_commit(bars.v_empty(t));
-              if (alone) mma_commit(bars.v_empty(t));
             }
             __syncwarp();
+            if (!C::kSoftRelease && Src::kVFirst) give_v(tv);
           }
           if (j < mine.uses) {
-            const uint32_t t = T + mine.tile(j), st = t % C::NK;
-            if (!(ok = bars.warp_wait(bars.k_full(t), Bars::k_par(t)))) break;
+            if (!(ok = bars.warp_wait(bars.k_full(tk), Bars::k_par(tk)))) break;
             tc_fence_after();
-            const uint64_t kd = kd0 + st * (C::kTileBytes >> 4);
+            const uint64_t kd = kd0 + tk % C::NK * (C::kTileBytes >> 4);
             if (elected) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
@@ -434,11 +447,18 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
                   mma_bf16(scol, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), bd, idS, kk > 0);
               }
               mma_commit(bars.at(Bars::kS + g * C::NB + buf));
-              mma_commit(bars.k_empty(t));
-              if (alone) mma_commit(bars.k_empty(t));
             }
             __syncwarp();
           }
+          // the stages go back (a commit costs the issuing warp a hundred cycles and more, so behind all products)
+          if (i >= 0 && !C::kSoftRelease && !Src::kVFirst) give_v(tv);
+          if (elected && !C::kSoftRelease) {
+            if (j < mine.uses) {
+              mma_commit(bars.k_empty(tk));
+              if (alone) mma_commit(bars.k_empty(tk));
+            }
+          }
+          __syncwarp();
         }
         T += tiles;
         n += mine.uses;
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
           src = r.q + s.b * r.qs_b + (s.h * G + P % G) * r.qs_h + (P / G) * r.qs_r;
         }
         // (as much of the row at once as registers allow, so that its loads are under way together)
-        constexpr int kMost = Src::kThreads > 512 ? 8 : 16, kVecs = D / 8 < kMost ? D / 8 : kMost;
+        constexpr int kMost = Src::kThreads * C::kCtasPerSm > 448 ? 8 : 16, kVecs = D / 8 < kMost ? D / 8 : kMost;
         uint4 qv[kVecs];
         auto load_q = [&](int c0) {
 #pragma unroll
@@ -527,7 +547,7 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
       // exchanges of two states; and this group's uses before the segment.
       constexpr uint32_t kParT = 1, kParSeg = 2, kParPV = 4, kParPV2 = 16, kParX = 32;
       uint32_t par = 0;
-      int n = 0;
+      int n = 0, T = 0;  // (T: tiles, only for the stages)
       bool ok = true, any = walk.next(p, lane);
       if (any) put_q();
       while (any) {
@@ -542,6 +562,11 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
           me.template mask<KT / 32>(p, walk, share.tile(i), vis);
           if (!(ok = bars.warp_wait(bars.at(Bars::kS + g * C::NB + buf), ((n + i) / C::NB) & 1))) break;
           const uint32_t scol = tl + C::kSCol + (g * C::NB + buf) * KT, pcol = scol + C::kPOff;
+          if (C::kSoftRelease && (warp & 3) == 0 && lane == 0) {
+            const uint32_t count = NG == 2 && w == 1 ? 2 : 1;  // (a tile that the other group has no part in counts twice)
+            mbar_arrive_n(bars.k_empty(T + share.tile(i)), count);
+            if (i > 0) mbar_arrive_n(bars.v_empty(T + share.tile(i - 1)), count);
+          }
           if (warp_idle) {  // (rows of P that nobody uses: whatever is there)
             if (lane == 0) mbar_arrive(bars.at(Bars::kP + g * C::NB + buf));
             continue;
@@ -658,6 +683,9 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
         }
         if (!ok) break;
         tc_fence_after();
+        if (C::kSoftRelease && (warp & 3) == 0 && lane == 0 && share.uses > 0)  // the last use's V
+          mbar_arrive_n(bars.v_empty(T + share.tile(share.uses - 1)), NG == 2 && w == 1 ? 2 : 1);
+        T += tiles;
         const int slot = 2 * blockIdx.x + (ends ? 1 : 0), prow = (w == 2 ? g * kBlockRows : 0) + row;
         float* part = r.part_o + (size_t)slot * r.slot_rows * D + 4 * prow;
         const float inv = l2 == 0.f ? 0.f : v_scale / l2;
@@ -725,7 +753,7 @@ __global__ void __launch_bounds__(Src::kThreads, 1) rows_kernel(const __grid_con
     }
   }
 
-  if (warp == C::kSrcWarp + 1) {
+  if (warp == C::kSrcWarp) {
     // ---- rows that no item covers: zeros, every CTA's warp its share of them
     const int R = r.G() * r.Nq;
     for (int b0 = 0; b0 < r.B; b0 += 32) {
@@ -827,10 +855,12 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
 
 __host__ inline size_t rows_align(size_t x) { return (x + 255) / 256 * 256; }
 // Rows of a part's slot: those of the largest item.
-__host__ inline int rows_slot(int rows, int d) { return d <= 128 && rows > kBlockRows ? 2 * kBlockRows : kBlockRows; }
+__host__ inline bool rows_two_blocks(int rows, int d) { return d <= 128 && rows > kBlockRows; }
+// (one CTA per SM with slots of two blocks, or, d <= 128, two per SM with slots of one)
 __host__ inline size_t rows_workspace(int rows, int d) {
-  const size_t slots = 2 * (size_t)kRowCtas * rows_slot(rows, d);
-  return rows_align(kRowCtas * sizeof(SplitRec)) + rows_align(slots * 8) + slots * d * 4;
+  const size_t ctas = kRowSms * (d <= 128 && !rows_two_blocks(rows, d) ? 2 : 1);
+  const size_t slots = 2 * ctas * (rows_two_blocks(rows, d) ? 2 : 1) * kBlockRows;
+  return rows_align(ctas * sizeof(SplitRec)) + rows_align(slots * 8) + slots * d * 4;
 }
 // What the sources' entry points take alike.
 __host__ inline bool rows_bad_heads(int B, int Hq, int Hkv, int Nq) {
@@ -842,11 +872,12 @@ template <class Src>
 cudaError_t launch_rows(typename Src::Params prm, void* ws, cudaStream_t stream) {
   RowParams& r = prm.r;
   const int rows = r.G() * r.Nq, D = Src::Cfg::D;
-  r.slot_rows = rows_slot(rows, D);
+  constexpr int kCtas = Src::Cfg::kCtas;
+  r.slot_rows = Src::Cfg::NG * kBlockRows;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const size_t slots = 2 * (size_t)kRowCtas * r.slot_rows;
+  const size_t slots = 2 * (size_t)kCtas * r.slot_rows;
   r.rec = (SplitRec*)w;
-  w += rows_align(kRowCtas * sizeof(SplitRec));
+  w += rows_align(kCtas * sizeof(SplitRec));
   r.part_ml = (float2*)w;
   w += rows_align(slots * 8);
   r.part_o = (float*)w;
@@ -859,11 +890,11 @@ cudaError_t launch_rows(typename Src::Params prm, void* ws, cudaStream_t stream)
     if ((e = cudaFuncSetAttribute(rows_kernel<Src>, cudaFuncAttributeMaxDynamicSharedMemorySize, Src::kSmem))) return e;
     if (dev <= 63) ready.fetch_or(bit);
   }
-  rows_kernel<Src><<<kRowCtas, Src::kThreads, Src::kSmem, stream>>>(prm);
+  rows_kernel<Src><<<kCtas, Src::kThreads, Src::kSmem, stream>>>(prm);
   if ((e = cudaGetLastError())) return e;
   cudaLaunchConfig_t cfg{};
   const int most = r.slot_rows < rows ? r.slot_rows : rows;
-  cfg.gridDim = dim3(kRowCtas, (unsigned)((most + 31) / 32 * (D / 16) + 7) / 8);
+  cfg.gridDim = dim3(kCtas, (unsigned)((most + 31) / 32 * (D / 16) + 7) / 8);
   cfg.blockDim = dim3(kRowJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
@@ -871,7 +902,7 @@ cudaError_t launch_rows(typename Src::Params prm, void* ws, cudaStream_t stream)
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rows_join_kernel<Src>, prm, kRowCtas);
+  return cudaLaunchKernelEx(&cfg, rows_join_kernel<Src>, prm, kCtas);
 }
 
 }  // namespace

@@ -107,13 +107,16 @@ class Machine:
                     self.queue[g].append(("PV", n + i, t, i == 0))
                     if j >= len(mine):
                         self.queue[g].append(("commit", (self.pv if i + 1 == len(mine) else self.pv2)[g]))
-                    self.queue[g] += [("commit", self.ve[t % self.NV])] * count
                 if j < len(mine):
                     t = T + mine[j]
                     yield from self.wait("k", self.kf[t % self.NK], (t // self.NK) & 1)
                     self.queue[g].append(("S", n + j, t, seg, g if w == 2 else 0, warps))
                     self.queue[g].append(("commit", self.s[g][buf]))
-                    self.queue[g] += [("commit", self.ke[t % self.NK])] * count
+                if NB == 2:  # (with one buffer the softmax group hands the stages back)
+                    if i >= 0:
+                        self.queue[g] += [("commit", self.ve[(T + mine[i]) % self.NV])] * count
+                    if j < len(mine):
+                        self.queue[g] += [("commit", self.ke[(T + mine[j]) % self.NK])] * count
             T += tiles
             n += len(mine)
 
@@ -125,6 +128,10 @@ class Machine:
             self.Q[g if segs[seg][1] == 2 else 0][warp] = seg
             yield
             self.q.arrive()
+
+        def hand(bar, w):
+            for _ in range(2 if NG == 2 and w == 1 else 1):
+                bar.arrive()
 
         T = nx = npv2 = 0
         n, npv = [0] * NG, [0] * NG
@@ -138,6 +145,10 @@ class Machine:
                 buf = v % NB
                 yield from self.wait("s", self.s[g][buf], (v // NB) & 1)
                 assert self.S[g][buf] == v, "softmax reads another use's scores"
+                if NB == 1 and wi == 0:
+                    hand(self.ke[(T + t) % self.NK], w)
+                    if i:
+                        hand(self.ve[(T + share[i - 1]) % self.NV], w)
                 if self.rng.random() < 0.3 and i:  # O is scaled
                     if NB == 2 and i + 1 < len(share):
                         yield from self.wait("rescale", self.s[g][buf ^ 1], ((v + 1) // NB) & 1)
@@ -169,6 +180,8 @@ class Machine:
                 npv[k] += len(want[k]) > 0
                 n[k] += len(want[k])
             npv2 += NB == 2 and len(share) > 1
+            if NB == 1 and wi == 0 and len(share):
+                hand(self.ve[(T + share[-1]) % self.NV], w)
             reads = [k for k in range(NG) if want[k] and (joint or k == g)]
             for _ in range(2):
                 for k in reads:
