@@ -22,13 +22,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 template <int D, bool F16, bool kTwo>
 struct CrossPick;
 template <bool F16>
-struct CrossPick<64, F16, true> { using Cfg = RowCfg<64, 64, 2, 2, true, 8, 8, F16>; };
-template <bool F16>
-struct CrossPick<64, F16, false> { using Cfg = RowCfg<64, 64, 1, 2, true, 6, 6, F16>; };
+struct CrossPick<64, F16, false> { using Cfg = RowCfg<64, 64, 1, 2, true, 5, 5, F16>; };
 template <bool F16>
 struct CrossPick<128, F16, true> { using Cfg = RowCfg<128, 64, 2, 2, false, 4, 4, F16>; };
 template <bool F16>
-struct CrossPick<128, F16, false> { using Cfg = RowCfg<128, 64, 1, 1, true, 3, 3, F16>; };
+struct CrossPick<128, F16, false> { using Cfg = RowCfg<128, 64, 1, 1, true, 2, 3, F16>; };
 template <bool F16>
 struct CrossPick<256, F16, false> { using Cfg = RowCfg<256, 64, 1, 2, true, 3, 3, F16>; };
 
@@ -41,8 +39,9 @@ struct CrossSrc {
   static constexpr int kBars = Cfg::NV;  // per stage of V: a last tile has landed, values behind the end and all
   static __device__ __forceinline__ uint32_t bar_count(int) { return 1; }
   static constexpr bool kPairedV = false, kOutF16 = F16, kScaledQ = false;
+  static constexpr int kSoftUnroll = 2;
   static constexpr int kSmem = Cfg::kSrcOff + 1024;
-  static_assert(Cfg::kCtasPerSm * (kSmem + 4096 + 1024) <= 233472, "shared memory");
+  static_assert(Cfg::kCtasPerSm * (kSmem + (Cfg::NG == 2 ? 4096 : 2048) + 1024) <= 233472, "shared memory");
 
   struct Params {
     RowParams r;
@@ -74,13 +73,9 @@ struct CrossSrc {
       const int G = p.r.G();
       valid = P < G * p.r.Nq;
       out_row = valid ? (b * p.r.Hq + h * G + P % G) * p.r.Nq + P / G : -1;
+      c2 = kLog2e * rsqrtf((float)D);
       v_scale = 1.f;
     }
-    __device__ __forceinline__ float scale(const Params&, int, float) {
-      c2 = kLog2e * rsqrtf((float)D);
-      return 1.f;
-    }
-    __device__ __forceinline__ void scale_v(const Params&, int) {}
     __device__ __forceinline__ uint32_t convert(uint32_t w, float) const { return w; }
     // which of a tile's keys the row sees, in words of 32
     template <int N>
@@ -222,7 +217,7 @@ cudaError_t launch_cross_rows(const CrossArgs& a, void* ws, cudaStream_t stream)
 }
 template <int D, bool F16>
 cudaError_t launch_cross(const CrossArgs& a, void* ws, cudaStream_t stream) {
-  if constexpr (D <= 128)
+  if constexpr (D == 128)
     if (rows_two_blocks(a.r.G() * a.r.Nq, D)) return launch_cross_rows<D, F16, true>(a, ws, stream);
   return launch_cross_rows<D, F16, false>(a, ws, stream);
 }

@@ -43,13 +43,11 @@ __device__ __forceinline__ uint32_t tree_hmul2(uint32_t a, uint32_t b) {
 template <int D, bool kTwo>
 struct TreePick;
 template <>
-struct TreePick<64, true> { using Cfg = RowCfg<64, 64, 2, 2, true, 4, 4, true>; static constexpr int kRaw = 8; };
-template <>
 struct TreePick<64, false> { using Cfg = RowCfg<64, 64, 1, 2, true, 3, 3, true>; static constexpr int kRaw = 8; };
 template <>
 struct TreePick<128, true> { using Cfg = RowCfg<128, 64, 2, 2, false, 2, 4, true>; static constexpr int kRaw = 4; };
 template <>
-struct TreePick<128, false> { using Cfg = RowCfg<128, 64, 1, 1, true, 2, 2, true>; static constexpr int kRaw = 4; };
+struct TreePick<128, false> { using Cfg = RowCfg<128, 64, 1, 1, true, 2, 2, true>; static constexpr int kRaw = 3; };
 template <>
 struct TreePick<256, false> { using Cfg = RowCfg<256, 64, 1, 2, true, 2, 2, true>; static constexpr int kRaw = 4; };
 
@@ -66,8 +64,9 @@ struct TreeSrc {
   static constexpr int kBars = 2 * kRaw;  // pages there, pages read
   static __device__ __forceinline__ uint32_t bar_count(int i) { return i < kRaw ? 1 : kKWarps + kVWarps; }
   static constexpr bool kPairedV = true, kOutF16 = F16, kScaledQ = true;
+  static constexpr int kSoftUnroll = 1;  // (the teams' code wants room in the instruction caches: 2 here, 221 us for 207)
   static constexpr int kSmem = Cfg::kSrcOff + kRaw * kPageBytes + 1024;
-  static_assert(Cfg::kCtasPerSm * (kSmem + 5120 + 1024) <= 233472, "shared memory");
+  static_assert(Cfg::kCtasPerSm * (kSmem + (Cfg::NG == 2 ? 4096 : 2048) + 1024) <= 233472, "shared memory");
 
   static __device__ __forceinline__ float largest(uint4 v) {  // magnitude of eight values
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -126,20 +125,20 @@ struct TreeSrc {
       pos = P / G;
       valid = pos < s.nodes;
       out_row = pos < p.r.Nq ? (b * p.r.Hq + h * G + P % G) * p.r.Nq + pos : -1;
-      depth = valid && p.depths ? max(0, min(p.depths[b * p.depth_stride + pos], p.r.Nq - 1)) : 0;
+      c2 = p.k_scale[h] * kLog2e * rsqrtf((float)D);
+      v_scale = p.v_scale[h];
+      depth = valid && p.window ? max(0, min(p.depths[b * p.depth_stride + pos], p.r.Nq - 1)) : 0;
     }
     // The row's factors; returns the power of two that brings its largest magnitude to 2^14 .. 2^16.
-    __device__ __forceinline__ float scale(const Params& p, int h, float amax) {
+    __device__ __forceinline__ float scale(float amax) {
       int e = (int)((__float_as_uint(amax) >> 23) & 255) - 127;
       e = max(-100, min(126, e));
       const float down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
       // (a positive finite number, so that a masked score stays -inf and a key of zeros 0)
-      const float f = down * (p.k_scale[h] * kLog2e * rsqrtf((float)D));
+      const float f = down * c2;
       c2 = f < FLT_MIN ? FLT_MIN : f > FLT_MAX ? FLT_MAX : f;
-      v_scale = p.v_scale[h];
       return __uint_as_float((uint32_t)(127 + 14 - e) << 23);
     }
-    __device__ __forceinline__ void scale_v(const Params& p, int h) { v_scale = p.v_scale[h]; }
     __device__ __forceinline__ uint32_t convert(uint32_t w, float up) const {
       const float2 f = unpack2<F16>(w);
       return pack2<true>(f.x * up, f.y * up);
@@ -242,7 +241,7 @@ struct TreeSrc {
           // A lane takes 32 channels (16 code bytes, two scales) of a key.  Eight neighbouring lanes store to four
           // keys and both halves of 64 channels: all banks once.
           constexpr int kQuarters = D / 32 < 4 ? D / 32 : 4, kUnits = kTile * D / 1024;
-#pragma unroll 2
+#pragma unroll 1
           for (int u = 0; u < kUnits / kKWarps; ++u) {
             const int unit = u * kKWarps + w;
             int key, q;
@@ -413,8 +412,7 @@ int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long 
   const bool two = rows_two_blocks(Hq / Hkv * Nq, d);
   switch (d) {
     case 64:
-      e = two ? (f16 ? go(TreeSrc<64, true, true>{}) : go(TreeSrc<64, false, true>{}))
-              : (f16 ? go(TreeSrc<64, true, false>{}) : go(TreeSrc<64, false, false>{}));
+      e = f16 ? go(TreeSrc<64, true, false>{}) : go(TreeSrc<64, false, false>{});
       break;
     case 128:
       e = two ? (f16 ? go(TreeSrc<128, true, true>{}) : go(TreeSrc<128, false, true>{}))

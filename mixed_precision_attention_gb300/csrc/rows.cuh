@@ -28,6 +28,7 @@
 #include <atomic>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/apa.h"
 #include "apa_internal.h"
@@ -99,7 +100,8 @@ struct RowCfg {
   static constexpr uint32_t kOCol = 0, kSCol = NG * D, kQCol = kSCol + NG * NB * KT;  // S: NB buffers per group
   static constexpr uint32_t kPOff = KT / 2;  // P, two keys per column, in the upper half of its S
   static constexpr int kQOff = 0, kKOff = NG * kQBytes, kVOff = kKOff + NK * kTileBytes;
-  static constexpr int kSrcOff = kVOff + NV * kTileBytes;  // the source's own
+  static constexpr int kStagePitch = 144, kStageOff = kVOff + NV * kTileBytes;  // Q on its way to tensor memory: 64 channels
+  static constexpr int kSrcOff = kStageOff + (QT ? NG * 128 * kStagePitch : 0);  // of each row; the source's own
   static constexpr int kSoftWarps = 4 * NG, kMmaWarp = kSoftWarps, kSrcWarp = kSoftWarps + NG;
   // With one buffer the commit of S(i + 1) says that K of that use and V of use i have been read: a lane of the softmax
   // group hands the stages back.  With two, V would wait for another use: the issuer's commits do.
@@ -274,7 +276,8 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   __shared__ float2 xml[NG == 2 ? 2 : 1][NG == 2 ? 128 : 1];  // two groups' (m, l) of a row
   __shared__ RowWalk<Src> walks[Src::kThreads / 32];
   __shared__ long long warp_sum[32];
-  __shared__ int found[2][2];             // sequence, and uses (of a head) before it: of the first and the last use
+  __shared__ int found[2];   // the last use's sequence, and uses (of a head) before it
+  __shared__ int begin[3];   // the first use's sequence, item of it, uses into that
   const RowParams& r = p.r;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
@@ -327,18 +330,29 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   total *= r.Hkv;
   const RowCut cut(total, cut_ctas(total, gridDim.x));
   const long long x0 = cut.first(blockIdx.x), x1 = cut.first(blockIdx.x + 1);
-  for (int k = 0; k < 2; ++k) {
-    const long long at = k ? x1 - 1 : x0;
-    if (x1 > x0 && at >= before * r.Hkv && at < (before + mine) * r.Hkv) {
-      long long sum = before;
-      for (int b = b_lo; b < b_hi; ++b) {
-        const long long n = typename Src::Seq(p, b).uses();
-        if (at >= sum * r.Hkv && at < (sum + n) * r.Hkv) {
-          found[k][0] = b;
-          found[k][1] = (int)sum;
-        }
-        sum += n;
+  // a place in the list, x, of sequence b with `sum` uses (of a head) before it, as its item and uses into that
+  auto place = [&](const typename Src::Seq& s, long long sum, long long x, int& item, int& pos) {
+    const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, head = (int)s.uses();
+    const long long y = x - sum * r.Hkv;
+    const int h = (int)rows_quotient(y, head), z = (int)(y - (long long)h * head), kk = z / (C::kBlocks * s.tiles);
+    item = h * per + kk;
+    pos = z - kk * C::kBlocks * s.tiles;
+  };
+  auto here = [&](long long x) { return x1 > x0 && x >= before * r.Hkv && x < (before + mine) * r.Hkv; };
+  if (here(x0) || here(x1 - 1)) {
+    long long sum = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const typename Src::Seq s(p, b);
+      const long long end = (sum + s.uses()) * r.Hkv;
+      if (x0 >= sum * r.Hkv && x0 < end) {
+        begin[0] = b;
+        place(s, sum, x0, begin[1], begin[2]);
       }
+      if (x1 - 1 >= sum * r.Hkv && x1 - 1 < end) {
+        found[0] = b;
+        found[1] = (int)sum;
+      }
+      sum += s.uses();
     }
   }
   tc_fence_before();
@@ -346,24 +360,13 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  // a place in the list as (item of its sequence, uses into the item)
-  auto place = [&](int k, long long x, int& b, int& item, int& pos) {
-    b = found[k][0];
-    const typename Src::Seq s(p, b);
-    const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, head = (int)s.uses();
-    const long long y = x - (long long)found[k][1] * r.Hkv;
-    const int h = (int)rows_quotient(y, head), z = (int)(y - (long long)h * head), kk = z / (C::kBlocks * s.tiles);
-    item = h * per + kk;
-    pos = z - kk * C::kBlocks * s.tiles;
-  };
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   if (warp == C::kMmaWarp && lane == 0) {  // (it waits for Q first of all)
     SplitRec rec{};
     if (x1 > x0) {
-      int b, item, pos;
-      place(1, x1 - 1, b, item, pos);
+      const int b = found[0];
       const typename Src::Seq s(p, b);
+      int item, pos;
+      place(s, found[1], x1 - 1, item, pos);
       const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, rb = item % per * C::kBlocks;
       const int w = min(C::kBlocks, s.blocks - rb);
       const long long first = x1 - 1 - pos;
@@ -373,11 +376,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   }
   if (x1 > x0) {
     RowWalk<Src>& walk = walks[warp];
-    if (lane == 0) {
-      int sb, sitem, spos;
-      place(0, x0, sb, sitem, spos);
-      walk.start(p, sb, sitem, spos, (int)(x1 - x0));
-    }
+    if (lane == 0) walk.start(p, begin[0], begin[1], begin[2], (int)(x1 - x0));
     if (warp >= C::kSrcWarp) {
       Src::produce(p, walk, smem, sbase, bars, warp - C::kSrcWarp, lane);
     } else if (warp >= C::kMmaWarp) {
@@ -476,61 +475,77 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
       const uint32_t tl = tmem + lane_base;
       typename Src::Row me;  // this thread's row: me.valid, me.out_row (in rows, or -1), what masks and scales it
       float m2 = -INFINITY, l2 = 0.f;
-      // Q of a segment: both groups share the block of an item with one, a half of the channels each
+      // Q of a segment, a warp its 32 rows, so that neighbouring lanes read neighbouring channels.  Both groups share
+      // the block of an item with one, a half of the channels each.
       auto put_q = [&]() {
         const RowSeg& s = walk.g;
-        const int buf = s.w == 2 ? g : 0;  // the block that this group's uses are of
-        me.set(p, walk.seq, s.b, s.h, (s.rb + buf) * kBlockRows + row);
-        const uint16_t* src = nullptr;
-        if (me.valid) {
-          const int P = (s.rb + buf) * kBlockRows + row, G = r.G();
-          src = r.q + s.b * r.qs_b + (s.h * G + P % G) * r.qs_h + (P / G) * r.qs_r;
-        }
-        // (as much of the row at once as registers allow, so that its loads are under way together)
-        constexpr int kMost = Src::kThreads * C::kCtasPerSm > 448 ? 8 : 16, kVecs = D / 8 < kMost ? D / 8 : kMost;
-        uint4 qv[kVecs];
-        auto load_q = [&](int c0) {
-#pragma unroll
-          for (int k = 0; k < kVecs; ++k)
-            qv[k] = src ? *reinterpret_cast<const uint4*>(src + c0 + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+        const int buf = s.w == 2 ? g : 0, P = (s.rb + buf) * kBlockRows + row, G = r.G();
+        me.set(p, walk.seq, s.b, s.h, P);
+        const uint16_t* base = r.q + s.b * r.qs_b + (long long)s.h * G * r.qs_h;
+        const long long off = (P % G) * r.qs_h + (P / G) * r.qs_r;
+        const unsigned used = __ballot_sync(0xffffffffu, me.valid);
+        // rows kRows i + lane / kLanes of the warp, channels c + 8 (lane % kLanes) ..
+        auto fetch = [&](auto lanes, int i, int c) {
+          constexpr int kLanes = decltype(lanes)::value, kRows = 32 / kLanes;
+          const int from = kRows * i + lane / kLanes;
+          const long long o = __shfl_sync(0xffffffffu, off, from);
+          return (used >> from) & 1 ? *reinterpret_cast<const uint4*>(base + o + c + 8 * (lane % kLanes))
+                                    : make_uint4(0u, 0u, 0u, 0u);
         };
-        float amax = 0.f;
+        float up = 1.f;
         if constexpr (Src::kScaledQ) {
+          constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+          float amax = 0.f;
 #pragma unroll 1
-          for (int c0 = D - 8 * kVecs; c0 >= 0; c0 -= 8 * kVecs) {  // (the first half last: it stays)
-            load_q(c0);
+          for (int i0 = 0; i0 < 32 / kRows; i0 += 8) {
+            uint4 v[8];
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) amax = fmaxf(amax, Src::largest(qv[k]));
-          }
-        } else {
-          load_q(0);
-        }
-        const float up = me.scale(p, s.h, amax);
-        const bool halves = NG == 2 && s.w == 1;
+            for (int i = 0; i < 8; ++i) v[i] = fetch(std::integral_constant<int, kLanes>{}, i0 + i, 0);
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 8 * kVecs) {
-          if (c0 > 0) load_q(c0);
+            for (int i = 0; i < 8; ++i) {
+              float a = Src::largest(v[i]);
 #pragma unroll
-          for (int c = 0; c < kVecs; c += 4) {  // 32 channels
-            if (halves && (c0 + 8 * c >= D / 2) != (g == 1)) continue;
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              w[4 * k] = me.convert(qv[c + k].x, up);
-              w[4 * k + 1] = me.convert(qv[c + k].y, up);
-              w[4 * k + 2] = me.convert(qv[c + k].z, up);
-              w[4 * k + 3] = me.convert(qv[c + k].w, up);
+              for (int d = kLanes / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+              a = __shfl_sync(0xffffffffu, a, lane % kRows * kLanes);  // that of row kRows (i0 + i) + lane % kRows
+              if (lane / kRows == i0 + i) amax = a;
             }
-            if constexpr (C::QT) {
-              tmem_st_x16(tl + C::kQCol + buf * (D / 2) + c0 / 2 + 4 * c, w);
-            } else {
+          }
+          up = me.scale(amax);
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          if (NG == 2 && s.w == 1 && c0 / 64 != g) continue;
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = fetch(std::integral_constant<int, 8>{}, i, c0);
+          if constexpr (C::QT) {
+            uint8_t* stage = smem + C::kStageOff + warp * 32 * C::kStagePitch;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(stage + (4 * i + lane / 8) * C::kStagePitch + lane % 8 * 16) = v[i];
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[16];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const int ch = c0 / 8 + c + k;
-                *reinterpret_cast<uint4*>(smem + C::kQOff + buf * C::kQBytes + (ch >> 3) * 16384 + row * 128 +
-                                          (((ch & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * C::kStagePitch + 64 * h + 16 * k);
+                w[4 * k] = me.convert(x.x, up);
+                w[4 * k + 1] = me.convert(x.y, up);
+                w[4 * k + 2] = me.convert(x.z, up);
+                w[4 * k + 3] = me.convert(x.w, up);
               }
+              tmem_st_x16(tl + C::kQCol + buf * (D / 2) + c0 / 2 + 16 * h, w);
+            }
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int from = 4 * i + lane / 8, at = (warp & 3) * 32 + from;
+              const float f = __shfl_sync(0xffffffffu, up, from);
+              *reinterpret_cast<uint4*>(smem + C::kQOff + buf * C::kQBytes + (c0 / 64) * 16384 + at * 128 +
+                                        ((lane % 8 ^ (at & 7)) << 4)) =
+                  make_uint4(me.convert(v[i].x, f), me.convert(v[i].y, f), me.convert(v[i].z, f), me.convert(v[i].w, f));
             }
           }
         }
@@ -580,13 +595,16 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 32; ++k) sv[k] = __uint_as_float(raw[k]);
-            if (__any_sync(0xffffffffu, vis[c] != ~0u)) {
+            uint32_t v = vis[0];
+#pragma unroll
+            for (int k = 1; k < KT / 32; ++k) v = c == k ? vis[k] : v;
+            if (__any_sync(0xffffffffu, v != ~0u)) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!((vis[c] >> k) & 1u)) sv[k] = -INFINITY;
+                if (!((v >> k) & 1u)) sv[k] = -INFINITY;
             }
           };
-#pragma unroll
+#pragma unroll Src::kSoftUnroll
           for (int c = 0; c < KT / 32; ++c) {
             load(c);
             float g8[4];
@@ -609,9 +627,9 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
           // a row that has seen no key yet: its scores are -inf and its weights 0
           const float nb = m2 == -INFINITY ? 0.f : C::kLift - m2;
           float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll Src::kSoftUnroll
           for (int c = KT / 32 - 1; c >= 0; --c) {
-            if (c < KT / 32 - 1) load(c);
+            if (Src::kSoftUnroll == 1 || c < KT / 32 - 1) load(c);
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k) rows_p8<C::F16>(sv + 8 * k, me.c2, nb, pk + 4 * k, ps[k & 1], ps[2 + (k & 1)]);
@@ -842,7 +860,6 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
   typename Src::Row me;
   me.set(p, seq, rec.b, rec.h, rec.rb * kBlockRows + row);
   if (me.out_row < 0) return;
-  me.scale_v(p, rec.h);
   const float inv = L == 0.f ? 0.f : me.v_scale / L;
   uint32_t y[8];
 #pragma unroll
@@ -855,7 +872,7 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
 
 __host__ inline size_t rows_align(size_t x) { return (x + 255) / 256 * 256; }
 // Rows of a part's slot: those of the largest item.
-__host__ inline bool rows_two_blocks(int rows, int d) { return d <= 128 && rows > kBlockRows; }
+__host__ inline bool rows_two_blocks(int rows, int d) { return d == 128 && rows > kBlockRows; }
 // (one CTA per SM with slots of two blocks, or, d <= 128, two per SM with slots of one)
 __host__ inline size_t rows_workspace(int rows, int d) {
   const size_t ctas = kRowSms * (d <= 128 && !rows_two_blocks(rows, d) ? 2 : 1);
