@@ -42,7 +42,6 @@ constexpr int kRowSms = 152;
 constexpr int kMaxRowSeqs = 8192;
 constexpr float kTauRows = 8.f;    // lazy-maximum threshold, log2 units
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMinUses = 4;        // a CTA takes no fewer uses than these while others have none
 
 // x / n for x >= 0; nearly always a 32-bit division.
 __device__ __forceinline__ long long rows_quotient(long long x, int n) {
@@ -59,15 +58,20 @@ struct RowCut {
   }
   __device__ __forceinline__ long long first(int i) const { return i >= k ? q * k + r : q * i + min(i, r); }
 };
-__device__ __forceinline__ int cut_ctas(long long total, int grid) {
-  const long long n = rows_quotient(total + kMinUses - 1, kMinUses);
+// How many CTAs share `total` uses.  A CTA takes no fewer than k uses, where k follows the tiles of an item: joining the
+// parts costs in their number (four parts a microsecond), a tile about one itself (17 tiles an item: 22 us with
+// k = 1, 25 with 2, 26 with 4; 128 tiles: 54, and 29 with 4).
+__device__ __forceinline__ int cut_ctas(long long total, long long items, int grid) {
+  int k = 1;
+  while (k < 8 && 20 * k * k * items < total) k *= 2;
+  const long long n = rows_quotient(total + k - 1, k);
   return n < 1 ? 1 : n < grid ? (int)n : grid;
 }
 
 // The item that begins in a CTA and goes on behind it (n = 0: none).
 struct SplitRec {
   long long first, total;  // its first use in the list; the list's length
-  int b, h, rb, n, w, pad;
+  int b, h, rb, n, w, ctas;  // (ctas: how many share the list)
 };
 
 struct RowParams {
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
     before += x - mine;
   }
   total *= r.Hkv;
-  const RowCut cut(total, cut_ctas(total, gridDim.x));
+  const RowCut cut(total, cut_ctas(total, (long long)r.B * r.Hkv * ((r.G() * r.Nq + kBlockRows - 1) / kBlockRows), gridDim.x));
   const long long x0 = cut.first(blockIdx.x), x1 = cut.first(blockIdx.x + 1);
   // a place in the list, x, of sequence b with `sum` uses (of a head) before it, as its item and uses into that
   auto place = [&](const typename Src::Seq& s, long long sum, long long x, int& item, int& pos) {
@@ -360,6 +364,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == C::kMmaWarp && lane == 0) {  // (it waits for Q first of all)
     SplitRec rec{};
     if (x1 > x0) {
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
       const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, rb = item % per * C::kBlocks;
       const int w = min(C::kBlocks, s.blocks - rb);
       const long long first = x1 - 1 - pos;
-      if (first >= x0 && first + (long long)s.tiles * w > x1) rec = SplitRec{first, total, b, item / per, rb, s.tiles, w, 0};
+      if (first >= x0 && first + (long long)s.tiles * w > x1) rec = SplitRec{first, total, b, item / per, rb, s.tiles, w, cut.k};
     }
     r.rec[blockIdx.x] = rec;
   }
@@ -806,7 +811,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
 // in order: a warp takes 32 rows, one per lane, and 16 channels of them.
 constexpr int kRowJoinThreads = 256;
 template <class Src>
-__global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid_constant__ typename Src::Params p, int ctas) {
+__global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid_constant__ typename Src::Params p) {
   using C = typename Src::Cfg;
   constexpr int D = C::D, kCols = D / 16, kAhead = 4;  // parts whose loads are under way together
   const RowParams& r = p.r;
@@ -815,7 +820,7 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SplitRec rec = r.rec[blockIdx.x];
   if (rec.n == 0 || task / kCols * 32 >= rec.w * kBlockRows) return;
-  const RowCut cut(rec.total, cut_ctas(rec.total, ctas));
+  const RowCut cut(rec.total, rec.ctas);
   const long long uses = (long long)rec.n * rec.w;
   float acc[16], M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -919,7 +924,7 @@ cudaError_t launch_rows(typename Src::Params prm, void* ws, cudaStream_t stream)
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rows_join_kernel<Src>, prm, kCtas);
+  return cudaLaunchKernelEx(&cfg, rows_join_kernel<Src>, prm);
 }
 
 }  // namespace
