@@ -38,7 +38,7 @@ struct CrossSrc {
   static constexpr bool kVFirst = true;  // stages of V go back before S is issued: the copies behind them are long
   static constexpr int kBars = Cfg::NV;  // per stage of V: a last tile has landed, values behind the end and all
   static __device__ __forceinline__ uint32_t bar_count(int) { return 1; }
-  static constexpr bool kPairedV = false, kOutF16 = F16, kScaledQ = false;
+  static constexpr bool kPairedV = false, kOutF16 = F16, kScaledQ = false, kMasked = false;
   static constexpr int kSoftUnroll = 2;
   static constexpr int kSmem = Cfg::kSrcOff + 1024;
   static_assert(Cfg::kCtasPerSm * (kSmem + (Cfg::NG == 2 ? 4096 : 2048) + 1024) <= 233472, "shared memory");

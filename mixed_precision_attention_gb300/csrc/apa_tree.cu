@@ -63,7 +63,7 @@ struct TreeSrc {
   static constexpr bool kVFirst = false;
   static constexpr int kBars = 2 * kRaw;  // pages there, pages read
   static __device__ __forceinline__ uint32_t bar_count(int i) { return i < kRaw ? 1 : kKWarps + kVWarps; }
-  static constexpr bool kPairedV = true, kOutF16 = F16, kScaledQ = true;
+  static constexpr bool kPairedV = true, kOutF16 = F16, kScaledQ = true, kMasked = true;
   static constexpr int kSoftUnroll = 1;  // (the teams' code wants room in the instruction caches: 2 here, 221 us for 207)
   static constexpr int kSmem = Cfg::kSrcOff + kRaw * kPageBytes + 1024;
   static_assert(Cfg::kCtasPerSm * (kSmem + (Cfg::NG == 2 ? 4096 : 2048) + 1024) <= 233472, "shared memory");
@@ -171,21 +171,23 @@ struct TreeSrc {
     __device__ __forceinline__ void mask(const Params& p, const RowWalk<TreeSrc>& walk, int tile, uint32_t* vis) const {
       const Seq& s = walk.seq;
       const int j0 = s.page(walk.g.t0 + tile) * kTile;
-      // all rows see all keys?
-      if (j0 + 32 * N <= s.base && (!p.window || j0 + 32 * N <= p.sinks || j0 > s.base + p.r.Nq - 1 - p.window)) {
-#pragma unroll
-        for (int c = 0; c < N; ++c) vis[c] = valid ? ~0u : 0u;
-      } else {
 #pragma unroll 1
-        for (int c = 0; c < N; ++c) {
-          const uint32_t v = valid ? sees(p, s, walk.g.b, pos, depth, j0 + 32 * c) : 0u;
+      for (int c = 0; c < N; ++c) {
+        const uint32_t v = valid ? sees(p, s, walk.g.b, pos, depth, j0 + 32 * c) : 0u;
 #pragma unroll
-          for (int k = 0; k < N; ++k)
-            if (k == c) vis[k] = v;
-        }
+        for (int k = 0; k < N; ++k)
+          if (k == c) vis[k] = v;
       }
     }
   };
+  // Pages of the context alone, behind the sinks' and past the last position that a window may begin at.
+  static __device__ __forceinline__ void plain(const Params& p, const RowWalk<TreeSrc>& walk, int& lo, int& hi) {
+    const Seq& s = walk.seq;
+    const int off = s.n_sink - s.lo - walk.g.t0;  // from a page to the segment's tile
+    const int first = s.base + p.r.Nq - 1 - p.window;  // (a key at or before it may be hidden)
+    lo = max(s.lo, p.window && first >= 0 ? first / kTile + 1 : 0) + off;
+    hi = s.base / kTile + off;
+  }
 
   template <class Bars>
   static __device__ __forceinline__ void produce(const Params& p, RowWalk<TreeSrc>& walk, uint8_t* smem, uint32_t sbase,

@@ -574,12 +574,19 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
         const int tiles = walk.g.t1 - walk.g.t0, w = walk.g.w;
         const RowShare share(NG, w, tiles, g, par & kParT);
         const bool warp_idle = !__any_sync(0xffffffffu, me.valid);
+        int plain_lo = 0, plain_hi = 0;  // the segment's tiles of which every row sees every key
+        if constexpr (Src::kMasked) Src::plain(p, walk, plain_lo, plain_hi);
         m2 = -INFINITY;
         l2 = 0.f;
         for (int i = 0; i < share.uses; ++i) {
           const int buf = (n + i) % C::NB;
           uint32_t vis[KT / 32];
-          me.template mask<KT / 32>(p, walk, share.tile(i), vis);
+          if (Src::kMasked && share.tile(i) >= plain_lo && share.tile(i) < plain_hi) {
+#pragma unroll
+            for (int c = 0; c < KT / 32; ++c) vis[c] = me.valid ? ~0u : 0u;
+          } else {
+            me.template mask<KT / 32>(p, walk, share.tile(i), vis);
+          }
           if (!(ok = bars.warp_wait(bars.at(Bars::kS + g * C::NB + buf), ((n + i) / C::NB) & 1))) break;
           const uint32_t scol = tl + C::kSCol + (g * C::NB + buf) * KT, pcol = scol + C::kPOff;
           if (C::kSoftRelease && (warp & 3) == 0 && lane == 0) {
