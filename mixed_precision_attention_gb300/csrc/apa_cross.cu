@@ -39,6 +39,7 @@ struct CrossSrc {
   static constexpr int kBars = Cfg::NV;  // per stage of V: a last tile has landed, values behind the end and all
   static __device__ __forceinline__ uint32_t bar_count(int) { return 1; }
   static constexpr bool kPairedV = false, kOutF16 = F16, kScaledQ = false, kMasked = false;
+  static constexpr int kItemCost = Cfg::kItemCost;
   static constexpr int kSoftUnroll = 2;
   static constexpr int kSmem = Cfg::kSrcOff + 1024;
   static_assert(Cfg::kCtasPerSm * (kSmem + (Cfg::NG == 2 ? 4096 : 2048) + 1024) <= 233472, "shared memory");
@@ -58,7 +59,6 @@ struct CrossSrc {
       tiles = (len + Cfg::KT - 1) / Cfg::KT;
       blocks = (p.r.G() * p.r.Nq + kBlockRows - 1) / kBlockRows;
     }
-    __device__ __forceinline__ long long uses() const { return (long long)blocks * tiles; }
     __device__ __forceinline__ void report(const Params& p, int b) const {
       if (blockIdx.x == 0 && p.lens && p.lens[b] != len && p.r.err) atomicCAS(p.r.err, 0, APA_DEVERR_BOUNDS);
     }
@@ -244,7 +244,7 @@ int apa_attention_cross(const void* q, int dtype, long long q_batch_stride, long
   if (d != 64 && d != 128 && d != 256) return APA_ERR_HEAD_DIM;
   if (dtype != APA_DTYPE_BF16 && dtype != APA_DTYPE_F16) return APA_ERR_DTYPE;
   // (uses are counted in 32 bits per head, and per CTA)
-  const double uses = (double)B * ((Nkv + 63) / 64) * (((double)(Hq / Hkv) * Nq + 127) / 128 + 1);
+  const double uses = (double)B * ((Nkv + 63) / 64 + 16.0) * (((double)(Hq / Hkv) * Nq + 127) / 128 + 1);
   if (uses >= 2147483648.0 || uses * Hkv >= 137438953472.0) return APA_ERR_SHAPE;
   // (the stride of an axis of length 1 is never used: any value will do)
   if (B == 1) q_batch_stride = k_batch_stride = v_batch_stride = 0;

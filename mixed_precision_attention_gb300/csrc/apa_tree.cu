@@ -64,6 +64,7 @@ struct TreeSrc {
   static constexpr int kBars = 2 * kRaw;  // pages there, pages read
   static __device__ __forceinline__ uint32_t bar_count(int i) { return i < kRaw ? 1 : kKWarps + kVWarps; }
   static constexpr bool kPairedV = true, kOutF16 = F16, kScaledQ = true, kMasked = true;
+  static constexpr int kItemCost = Cfg::kItemCost;
   static constexpr int kSoftUnroll = 1;  // (the teams' code wants room in the instruction caches: 2 here, 221 us for 207)
   static constexpr int kSmem = Cfg::kSrcOff + kRaw * kPageBytes + 1024;
   static_assert(Cfg::kCtasPerSm * (kSmem + (Cfg::NG == 2 ? 4096 : 2048) + 1024) <= 233472, "shared memory");
@@ -108,7 +109,6 @@ struct TreeSrc {
       n_sink = p.window ? min((p.sinks + kTile - 1) / kTile, lo) : 0;
       tiles = nodes ? n_sink + (len + kTile - 1) / kTile - lo : 0;
     }
-    __device__ __forceinline__ long long uses() const { return (long long)blocks * tiles; }
     __device__ __forceinline__ void report(const Params& p, int b) const {
       if (blockIdx.x == 0 && p.r.err && (p.lens[b] != len || (p.nodes ? p.nodes[b] : p.r.Nq) != nodes))
         atomicCAS(p.r.err, 0, APA_DEVERR_BOUNDS);
@@ -362,7 +362,7 @@ int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long 
   if (dtype != APA_DTYPE_BF16 && dtype != APA_DTYPE_F16) return APA_ERR_DTYPE;
   if (window < 0 || sinks < 0) return APA_ERR_WINDOW;
   // (uses are counted in 32 bits per head, and per CTA)
-  const double uses = (double)B * max_pages * (((double)(Hq / Hkv) * Nq + 127) / 128 + 1);
+  const double uses = (double)B * (max_pages + 16.0) * (((double)(Hq / Hkv) * Nq + 127) / 128 + 1);
   if (uses >= 2147483648.0 || uses * Hkv >= 137438953472.0) return APA_ERR_SHAPE;
   // (the stride of an axis of length 1 is never used: any value will do)
   if (B == 1) q_batch_stride = mask_stride = depth_stride = 0;

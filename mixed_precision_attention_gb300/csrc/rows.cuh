@@ -111,6 +111,10 @@ struct RowCfg {
   // group hands the stages back.  With two, V would wait for another use: the issuer's commits do.
   static constexpr bool kSoftRelease = NB == 1;
   static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
+  // What beginning an item takes, in uses.  Without it (0) CTAs with many short items end last: trees of 32 nodes over 32
+  // contexts to 8192 keys 127 us, 104 with 7 (106 with 10); prompts of 2048 rows 440 us, 413 with 20 (420 with 34); 333 rows
+  // at d = 256 40 us, 32 with 12.
+  static constexpr int kItemCost = NG == 2 ? 20 : D == 256 ? 12 : 7;
   static_assert(NG == 1 || (NK % 2 == 0 && NV % 2 == 0), "RowShare");
   static_assert(kQCol + (QT ? NG * D / 2 : 0) <= kTmemCols, "tensor memory");
 };
@@ -131,13 +135,20 @@ struct RowShare {
   }
   __device__ __forceinline__ int tile(int i) const { return first + step * i; }  // counted from the segment's first
 };
+// The list in units of a use's time: an item is its uses behind kItemCost units for what beginning one takes (Q, the last
+// item's epilogue, the first S).
+template <class Src>
+__device__ __forceinline__ long long rows_cost(const typename Src::Seq& s) {  // of one head
+  const int per = (s.blocks + Src::Cfg::kBlocks - 1) / Src::Cfg::kBlocks;
+  return s.tiles ? (long long)s.blocks * s.tiles + (long long)per * Src::kItemCost : 0;
+}
 // A warp's way through the segments of its CTA, in shared memory: what is the same for all its lanes, and
 // looked up now and then, does not take every lane's registers.
 template <class Src>
 struct RowWalk {
   static constexpr int kBlocks = Src::Cfg::kBlocks;
   using Params = typename Src::Params;
-  int b, item, pos, left;     // item of the sequence, uses into it, uses left
+  int b, item, pos, left;     // item of the sequence, units into it, units left
   typename Src::Seq seq;      // the source's numbers of the segment's sequence
   RowSeg g;                   // the segment
   __device__ __forceinline__ void start(const Params& p, int b_, int item_, int pos_, int left_) {
@@ -152,21 +163,21 @@ struct RowWalk {
     while (left > 0) {
       int per = (seq.blocks + kBlocks - 1) / kBlocks, h = item / per, rb = (item - h * per) * kBlocks;
       int w = min(kBlocks, seq.blocks - rb);
-      if (pos == seq.tiles * w) {  // the next item
+      if (pos == Src::kItemCost + seq.tiles * w) {  // the next item
         pos = 0;
         if (++item == per * p.r.Hkv) {
           item = 0;
           do {
             seq = typename Src::Seq(p, ++b);
-          } while (seq.uses() == 0);
+          } while (seq.blocks == 0 || seq.tiles == 0);
           per = (seq.blocks + kBlocks - 1) / kBlocks;
         }
         h = item / per;
         rb = (item - h * per) * kBlocks;
         w = min(kBlocks, seq.blocks - rb);
       }
-      const int end = min(seq.tiles * w, pos + left);
-      g = RowSeg{b, h, rb, w, pos / w, end / w, seq.tiles};
+      const int end = min(Src::kItemCost + seq.tiles * w, pos + left);
+      g = RowSeg{b, h, rb, w, max(0, pos - Src::kItemCost) / w, max(0, end - Src::kItemCost) / w, seq.tiles};
       left -= end - pos;
       pos = end;
       if (g.t1 > g.t0) return true;  // (half a tile of two blocks is the next CTA's)
@@ -280,8 +291,8 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   __shared__ float2 xml[NG == 2 ? 2 : 1][NG == 2 ? 128 : 1];  // two groups' (m, l) of a row
   __shared__ RowWalk<Src> walks[Src::kThreads / 32];
   __shared__ long long warp_sum[32];
-  __shared__ int found[2];   // the last use's sequence, and uses (of a head) before it
-  __shared__ int begin[3];   // the first use's sequence, item of it, uses into that
+  __shared__ int found[2];   // the last unit's sequence, and units (of a head) before it
+  __shared__ int begin[3];   // the first unit's sequence, item of it, units into that
   const RowParams& r = p.r;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   for (int b = b_lo; b < b_hi; ++b) {
     const typename Src::Seq s(p, b);
     s.report(p, b);
-    mine += s.uses();
+    mine += rows_cost<Src>(s);
   }
   {
     long long x = mine;
@@ -334,20 +345,21 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   total *= r.Hkv;
   const RowCut cut(total, cut_ctas(total, (long long)r.B * r.Hkv * ((r.G() * r.Nq + kBlockRows - 1) / kBlockRows), gridDim.x));
   const long long x0 = cut.first(blockIdx.x), x1 = cut.first(blockIdx.x + 1);
-  // a place in the list, x, of sequence b with `sum` uses (of a head) before it, as its item and uses into that
+  // a place in the list, x, of a sequence with `sum` units (of a head) before it, as its item and units into that
   auto place = [&](const typename Src::Seq& s, long long sum, long long x, int& item, int& pos) {
-    const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, head = (int)s.uses();
+    const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, head = (int)rows_cost<Src>(s);
+    const int full = C::kBlocks * s.tiles + Src::kItemCost;
     const long long y = x - sum * r.Hkv;
-    const int h = (int)rows_quotient(y, head), z = (int)(y - (long long)h * head), kk = z / (C::kBlocks * s.tiles);
+    const int h = (int)rows_quotient(y, head), z = (int)(y - (long long)h * head), kk = z / full;
     item = h * per + kk;
-    pos = z - kk * C::kBlocks * s.tiles;
+    pos = z - kk * full;
   };
   auto here = [&](long long x) { return x1 > x0 && x >= before * r.Hkv && x < (before + mine) * r.Hkv; };
   if (here(x0) || here(x1 - 1)) {
     long long sum = before;
     for (int b = b_lo; b < b_hi; ++b) {
       const typename Src::Seq s(p, b);
-      const long long end = (sum + s.uses()) * r.Hkv;
+      const long long n = rows_cost<Src>(s), end = (sum + n) * r.Hkv;
       if (x0 >= sum * r.Hkv && x0 < end) {
         begin[0] = b;
         place(s, sum, x0, begin[1], begin[2]);
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
         found[0] = b;
         found[1] = (int)sum;
       }
-      sum += s.uses();
+      sum += n;
     }
   }
   tc_fence_before();
@@ -375,7 +387,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
       const int per = (s.blocks + C::kBlocks - 1) / C::kBlocks, rb = item % per * C::kBlocks;
       const int w = min(C::kBlocks, s.blocks - rb);
       const long long first = x1 - 1 - pos;
-      if (first >= x0 && first + (long long)s.tiles * w > x1) rec = SplitRec{first, total, b, item / per, rb, s.tiles, w, cut.k};
+      if (first >= x0 && first + Src::kItemCost + (long long)s.tiles * w > x1) rec = SplitRec{first, total, b, item / per, rb, s.tiles, w, cut.k};
     }
     r.rec[blockIdx.x] = rec;
   }
@@ -790,7 +802,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
       int from = R;
       if (b0 + lane < r.B) {
         const typename Src::Seq s(p, b0 + lane);
-        from = s.uses() > 0 ? min(R, s.blocks * kBlockRows) : 0;
+        from = s.tiles > 0 ? min(R, s.blocks * kBlockRows) : 0;
       }
       for (unsigned todo = __ballot_sync(0xffffffffu, from < R); todo; todo &= todo - 1) {
         const int k = __ffs(todo) - 1, b = b0 + k, first = __shfl_sync(0xffffffffu, from, k);
@@ -832,14 +844,16 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
   float acc[16], M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-  for (int cta = blockIdx.x; cut.first(cta) - rec.first < uses; cta += kAhead) {
+  const long long begin = rec.first + Src::kItemCost;  // of its uses in the list
+  for (int cta = blockIdx.x; cut.first(cta) - begin < uses; cta += kAhead) {
     float2 ml[kAhead];
     float4 o[kAhead][4];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       // the tiles t0 .. t1-1 of CTA cta + k
-      const long long a = cut.first(cta + k) - rec.first, e = cut.first(cta + k + 1) - rec.first;
-      const int t0 = a <= 0 ? 0 : (int)((a < uses ? a : uses) >> (rec.w - 1)), t1 = (int)((e < uses ? e : uses) >> (rec.w - 1));
+      const long long a = cut.first(cta + k) - begin, e = cut.first(cta + k + 1) - begin;
+      const int t0 = a <= 0 ? 0 : (int)((a < uses ? a : uses) >> (rec.w - 1));
+      const int t1 = e <= 0 ? 0 : (int)((e < uses ? e : uses) >> (rec.w - 1));
       if (t0 == 0 && t1 == rec.n) return;  // it has the item alone, and wrote it
       ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll

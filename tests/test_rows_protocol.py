@@ -254,28 +254,29 @@ def _first(n, k):
     return lambda i: n if i >= k else q * i + min(i, r)
 
 
-def _check_list(seqs, H, KB, grid, least):
-    """seqs: (blocks, tiles) of each sequence.  Every (sequence, head, block, tile) falls to one CTA once, a CTA
-    keeps at most one part of an item that ends in it and one of an item that goes on, and the joining finds them all."""
-    uses = [b * t for b, t in seqs]
-    total = sum(uses) * H
+def _check_list(seqs, H, KB, grid, least, E):
+    """seqs: (blocks, tiles) of each sequence; E: units that beginning an item counts as.  Every (sequence, head, block,
+    tile) falls to one CTA once, a CTA keeps at most one part of an item that ends in it and one of an item that goes on,
+    and the joining finds them all."""
+    per_of = lambda blocks: -(-blocks // KB)  # noqa: E731
+    cost = [b * t + E * per_of(b) if b and t else 0 for b, t in seqs]
+    total = sum(cost) * H
     f = _first(total, max(1, min(grid, -(-total // least))))
 
     def place(x):
         before = 0
-        for b, u in enumerate(uses):
+        for b, u in enumerate(cost):
             if u and before * H <= x < (before + u) * H:
                 break
             before += u
         blocks, tiles = seqs[b]
         h, z = divmod(x - before * H, u)
-        k = z // (KB * tiles)
-        return b, h * -(-blocks // KB) + k, z - k * KB * tiles
+        k = z // (KB * tiles + E)
+        return b, h * per_of(blocks) + k, z - k * (KB * tiles + E)
 
     def item_of(b, item):
-        blocks = seqs[b][0]
-        per = -(-blocks // KB)
-        return item // per, item % per * KB, min(KB, blocks - item % per * KB), per
+        per = per_of(seqs[b][0])
+        return item // per, item % per * KB, min(KB, seqs[b][0] - item % per * KB), per
 
     seen, parts, recs = set(), {}, []
     for c in range(grid):
@@ -283,20 +284,20 @@ def _check_list(seqs, H, KB, grid, least):
         if x1 > x0:
             b, item, pos = place(x1 - 1)
             h, rb, w, _ = item_of(b, item)
-            if x1 - 1 - pos >= x0 and x1 - 1 - pos + seqs[b][1] * w > x1:
+            if x1 - 1 - pos >= x0 and x1 - 1 - pos + E + seqs[b][1] * w > x1:
                 rec = (x1 - 1 - pos, b, h, rb, seqs[b][1], w)
             b, item, pos = place(x0)
             left = x1 - x0
             while left > 0:
                 h, rb, w, per = item_of(b, item)
-                if pos == seqs[b][1] * w:
+                if pos == E + seqs[b][1] * w:
                     pos, item = 0, item + 1
                     if item == per * H:
-                        item, b = 0, next(i for i in range(b + 1, len(seqs)) if uses[i])
+                        item, b = 0, next(i for i in range(b + 1, len(seqs)) if cost[i])
                     h, rb, w, per = item_of(b, item)
                 n = seqs[b][1]
-                end = min(n * w, pos + left)
-                t0, t1, left, pos = pos // w, end // w, left - (end - pos), end
+                end = min(E + n * w, pos + left)
+                t0, t1, left, pos = max(0, pos - E) // w, max(0, end - E) // w, left - (end - pos), end
                 for t in range(t0, t1):
                     for k in range(w):
                         assert (b, h, rb + k, t) not in seen
@@ -313,9 +314,9 @@ def _check_list(seqs, H, KB, grid, least):
         first, b, h, rb, n, w = rec
         got = []
         for d in range(c, grid):
-            if f(d) >= first + n * w:
+            if f(d) >= first + E + n * w:
                 break
-            got.append((d, max(0, min(f(d) - first, n * w)) // w, min(f(d + 1) - first, n * w) // w))
+            got.append((d, *(max(0, min(x - first - E, n * w)) // w for x in (f(d), f(d + 1)))))
         if any((t0, t1) == (0, n) for _, t0, t1 in got):
             continue
         for d, t0, t1 in got:
@@ -328,4 +329,5 @@ def test_list_is_cut_without_gaps_and_joined_whole():
     rng = random.Random(5)
     for _ in range(1500):
         seqs = [(rng.choice([0, 1, 2, 3, 5]), rng.choice([0, 1, 2, 7, 30])) for _ in range(rng.randint(1, 6))]
-        _check_list(seqs, rng.randint(1, 3), rng.choice([1, 2]), rng.choice([1, 2, 5, 16, 152, 304]), rng.choice([1, 2, 4, 8]))
+        _check_list(seqs, rng.randint(1, 3), rng.choice([1, 2]), rng.choice([1, 2, 5, 16, 152, 304]), rng.choice([1, 2, 4, 8]),
+                    rng.choice([0, 1, 7, 20]))
