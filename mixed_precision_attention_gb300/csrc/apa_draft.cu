@@ -12,7 +12,7 @@ namespace {
 // S(i) = {i} + S(parent(i)).  A CTA per sequence, a thread per node, which walks up its own
 // ancestors: they come in falling order, so the words of its row are filled from the last to
 // the first and each is written once.  What bounds it is latency: a launch, one load of the
-// parents, and a shared-memory load per level.
+// parents, and a shared-memory load per level (64 trees of 64 nodes 2.0 us, 256 of 250 2.4).
 struct TreeParams {
   const int32_t *parents, *nodes;
   int Nq, words;
@@ -70,7 +70,10 @@ __global__ void __launch_bounds__(APA_TREE_MAX_NODES) draft_tree_kernel(const Tr
 // that hold one V code byte of it in each word, and as many of V scales: a thread takes one
 // such piece of one key.  A CTA moves all keys of a sequence for a few heads of one layer, in
 // rounds: all pieces are read, then, behind a barrier, written.  A path rises, so path[k] > k
-// wherever something moves: no later key is read where an earlier one has been written.
+// wherever something moves: no later key is read where an earlier one has been written.  A
+// V code byte is alone in its 4 bytes and 16 of a key's lie in sectors of their own, so what moves is
+// five times a key's bytes; 32 sequences in 28 layers of 8 heads take 16 us, 64 in one layer 4.2
+// (launch, path, table entry and key, one load behind the other).
 constexpr int kAcceptThreads = 256;
 struct AcceptParams {
   uint8_t* pages;

@@ -1,4 +1,4 @@
-// rows.cuh -- exact attention of packed query rows over tiles of keys, for sources of keys
+// rows.cuh -- exact attention of packed query rows over tiles of 64 keys, for sources of keys
 // that bring their own producers (rows_kernel), and the joining of split walks.
 //
 // out = softmax(q K^T c + mask) V for the G * Nq rows that share a KV head's keys, taken
@@ -7,23 +7,38 @@
 // swizzle, a key per row), and masks scores.
 //
 // Work: an item is one block, or two neighbouring ones, of one KV head against all its
-// tiles; a use is one block against one tile.  The uses of all sequences form one list, cut
-// evenly over one CTA per SM, so lengths need not be alike and no length is read on the
-// host.  A CTA's run of tiles of one item is a segment.  An item that one CTA holds entirely
-// is written out at once; the states (m, l, O) of the others go to the workspace and a
-// second kernel joins them in order, so results do not depend on timing.
+// tiles; a use is one block against one tile.  The items of all sequences form one list in
+// units of a use's time (beginning an item counts, too), cut evenly over the CTAs, so
+// lengths need not be alike and no length is read on the host.  A CTA's run of tiles of one
+// item is a segment.  An item that one CTA holds entirely is written out at once; the states
+// (m, l, O) of the others go to the workspace and a second kernel joins them in order, so
+// results do not depend on timing.
 //
-// Inside a CTA (d <= 128) there are two softmax groups, four warps each with one thread per
-// row, and a warp for each that issues its products: either the two blocks of an item
-// against the same tiles, or one block against every other tile each, whose two states are
-// then joined over tensor memory.  A group's issuer runs through P V of use i, S of use
-// i + NB: those products execute in that order, so S may go over the P that lies in its
-// columns, and the commit of S says that the P V before it is done.  While a group works on
-// its scores the tensor cores have the other's products and, with NB = 2 buffers of S, its
-// own next S.  At d = 256 O takes half of tensor memory: one group.
+// A softmax group is four warps with a thread per row, and a warp that issues its products: P V
+// of use i, then S of use i + NB.  Those execute in that order, so S may go over the P that
+// lies in its columns, and the commit of S says that the P V before it is done.  P goes to
+// the product from tensor memory; O stays there, and moves with the running maximum only
+// when a score exceeds that by 8 (log2 units).
+//   Items of two blocks (d = 128, more than 128 rows): one CTA per SM with two groups, both
+//     blocks against the same tiles, or one block (the last of an odd number) against every
+//     other tile each, whose two states are then joined over tensor memory.  Two buffers of
+//     S, so that a group's next S is there when it has stored P; Q in shared memory, as tensor
+//     memory is full.
+//   Items of one block at d <= 128: two CTAs per SM with one group and half of tensor memory
+//     each, so that one works while the other begins an item (64 rows of G = 3 over 4096 keys
+//     each: 116 us, 129 with one CTA of two groups; d = 64, any number of rows, likewise: 2048
+//     rows of prompts 493 us, 537).  Q is an operand in tensor memory: S of 64 keys would
+//     otherwise read 6 KB of shared memory per 32 cycles of product, 1.5 times what it delivers.
+//   d = 256: O takes half of tensor memory: one group, one CTA.
 //
-// Q is an operand in tensor memory where it fits (kQT): S = Q K^T of 64 keys would otherwise
-// read 6 KB of shared memory per 32 cycles of product, 1.5 times what it delivers.
+// What bounds it, by traces of single CTAs: at 128 channels a use's products take 512 cycles
+// (640 with Q in shared memory), its exponentials 512 of the special-function units (16 a
+// cycle and SM), and it costs 770 to 850; a segment's beginning and end 10 000 to 15 000,
+// most of it latency, which is why the list counts them.  Tried and not kept: one diverged
+// thread as issuer (1900 cycles a use), one issuer for both groups (1140), tiles of 128 keys
+// (1230 TF/s on prompts where this form has 1350, and registers spill), all 64 scores in
+// registers at once where there are more than 12 warps (spills that miss the cache), register
+// shares by setmaxnreg (the compiler keeps to the launch's count).
 #pragma once
 #include <atomic>
 #include <cfloat>
