@@ -402,9 +402,10 @@ size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  *   workspace  apa_attention_tree_workspace_bytes() bytes, 256-byte aligned, or null to have
  *            it allocated stream-ordered for the call.  Two calls that overlap on the GPU
  *            must not share one.
- * Keys that no row sees are never used, whatever a page holds there; a NaN in V at a key that
- * some of the sequence's rows see may reach the others' outputs too.  Numerics are those of
- * apa_attention_cache.  Nq <= APA_TREE_MAX_NODES, B <= 8192, B * max_pages < 2^29.  The work
+ * Keys past lens[b], and keys up to base - window that are no sinks (which no depth sees), are
+ * never used, whatever a page holds there; scores that a row does not see are dropped whatever
+ * they are, but a NaN in V at any other key may reach rows that do not see it.  Numerics are
+ * those of apa_attention_cache.  Nq <= APA_TREE_MAX_NODES, B <= 8192, B * max_pages < 2^29.  The work
  * is split over the GPU by the lengths alone, so reruns are bitwise equal. */
 int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
                        long long q_row_stride, const uint8_t* pages, int num_pages, const int32_t* block_table,

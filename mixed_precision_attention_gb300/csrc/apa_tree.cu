@@ -288,7 +288,8 @@ struct TreeSrc {
           uint8_t* dst = smem + C::kVOff + T % C::NV * C::kTileBytes;
           const Seq& s = walk.seq;
           const int j0 = s.page(t) * kTile;
-          // keys that no row sees count as 0 whatever the page holds there: a weight of 0 does not hide a NaN
+          // keys past the end, and before every window, count as 0 whatever the page holds there: a weight of 0 does not
+          // hide a NaN
           const int gap = p.window ? s.base - p.window : -1;  // the last key before every row's window
           const bool edge = j0 + kTile > s.len || (j0 <= gap && j0 + kTile > p.sinks);
           // A lane takes four keys and four of the eight byte rows (channels g, g + 8) of 64 channels.

@@ -54,7 +54,7 @@ def _need_tree(name, t, dim, index, B, Nq):
         raise TypeError(f"{name} must be a {dim}-D tensor of torch.int32")
     if t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, not {t.device}")
-    if t.shape[0] not in (1, B) or t.shape[1] != Nq or dim == 3 and t.shape[2] != (Nq + 31) // 32:
+    if B == 0 or t.shape[0] not in (1, B) or t.shape[1] != Nq or dim == 3 and t.shape[2] != (Nq + 31) // 32:
         raise ValueError(f"{name} must be [B or 1, Nq{', ceil(Nq / 32)' if dim == 3 else ''}]")
     if not t[0].is_contiguous():
         raise ValueError(f"each sequence's {name} must be contiguous")
