@@ -166,17 +166,17 @@ struct RowWalk {
   int b, item, pos, left;     // item of the sequence, units into it, units left
   typename Src::Seq seq;      // the source's numbers of the segment's sequence
   RowSeg g;                   // the segment
-  __device__ __forceinline__ void start(const Params& p, int b_, int item_, int pos_, int left_) {
-    b = b_;
-    item = item_;
-    pos = pos_;
+  __device__ __forceinline__ void start(const int* begin, const typename Src::Seq& first, int left_) {
+    b = begin[0];
+    item = begin[1];
+    pos = begin[2];
     left = left_;
-    seq = typename Src::Seq(p, b_);
+    seq = first;
   }
   // one lane's work
   __device__ __forceinline__ bool step(const Params& p) {
     while (left > 0) {
-      int per = (seq.blocks + kBlocks - 1) / kBlocks, h = item / per, rb = (item - h * per) * kBlocks;
+      int per = (seq.blocks + kBlocks - 1) / kBlocks, h = per == 1 ? item : item / per, rb = (item - h * per) * kBlocks;
       int w = min(kBlocks, seq.blocks - rb);
       if (pos == Src::kItemCost + seq.tiles * w) {  // the next item
         pos = 0;
@@ -187,12 +187,12 @@ struct RowWalk {
           } while (seq.blocks == 0 || seq.tiles == 0);
           per = (seq.blocks + kBlocks - 1) / kBlocks;
         }
-        h = item / per;
+        h = per == 1 ? item : item / per;
         rb = (item - h * per) * kBlocks;
         w = min(kBlocks, seq.blocks - rb);
       }
       const int end = min(Src::kItemCost + seq.tiles * w, pos + left);
-      g = RowSeg{b, h, rb, w, max(0, pos - Src::kItemCost) / w, max(0, end - Src::kItemCost) / w, seq.tiles};
+      g = RowSeg{b, h, rb, w, max(0, pos - Src::kItemCost) >> (w - 1), max(0, end - Src::kItemCost) >> (w - 1), seq.tiles};
       left -= end - pos;
       pos = end;
       if (g.t1 > g.t0) return true;  // (half a tile of two blocks is the next CTA's)
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   __shared__ long long warp_sum[32];
   __shared__ int found[2];   // the last unit's sequence, and units (of a head) before it
   __shared__ int begin[3];   // the first unit's sequence, item of it, units into that
+  __shared__ typename Src::Seq first_seq;
   const RowParams& r = p.r;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
@@ -332,6 +333,8 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
     tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  // (launched early: what is above needs nothing that the kernel before this one writes)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- the list's length, and this CTA's place in it: each thread sums up a run of sequences
   constexpr int kWarps = Src::kThreads / 32;
   const int run = (r.B + Src::kThreads - 1) / Src::kThreads, b_lo = min(r.B, tid * run), b_hi = min(r.B, b_lo + run);
@@ -377,6 +380,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
       const long long n = rows_cost<Src>(s), end = (sum + n) * r.Hkv;
       if (x0 >= sum * r.Hkv && x0 < end) {
         begin[0] = b;
+        first_seq = s;
         place(s, sum, x0, begin[1], begin[2]);
       }
       if (x1 - 1 >= sum * r.Hkv && x1 - 1 < end) {
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
   }
   if (x1 > x0) {
     RowWalk<Src>& walk = walks[warp];
-    if (lane == 0) walk.start(p, begin[0], begin[1], begin[2], (int)(x1 - x0));
+    if (lane == 0) walk.start(begin, first_seq, (int)(x1 - x0));
     if (warp >= C::kSrcWarp) {
       Src::produce(p, walk, smem, sbase, bars, warp - C::kSrcWarp, lane);
     } else if (warp >= C::kMmaWarp) {
@@ -948,18 +952,21 @@ cudaError_t launch_rows(typename Src::Params prm, void* ws, cudaStream_t stream)
     if ((e = cudaFuncSetAttribute(rows_kernel<Src>, cudaFuncAttributeMaxDynamicSharedMemorySize, Src::kSmem))) return e;
     if (dev <= 63) ready.fetch_or(bit);
   }
-  rows_kernel<Src><<<kCtas, Src::kThreads, Src::kSmem, stream>>>(prm);
-  if ((e = cudaGetLastError())) return e;
+  cudaLaunchAttribute at{};  // both kernels begin while the one before them ends, and wait for it where they read
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(Src::kThreads);
+  cfg.dynamicSmemBytes = Src::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, rows_kernel<Src>, prm))) return e;
   const int most = r.slot_rows < rows ? r.slot_rows : rows;
   cfg.gridDim = dim3(kCtas, (unsigned)((most + 31) / 32 * (D / 16) + 7) / 8);
   cfg.blockDim = dim3(kRowJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, rows_join_kernel<Src>, prm);
 }
 

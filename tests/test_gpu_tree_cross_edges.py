@@ -445,3 +445,78 @@ def test_speculative_steps_in_a_graph():
                 assert all(np.array_equal(g.double().cpu().numpy(), w) for g, w in zip(got, seen[b]))
     held = sum((k.shape[2] + 63) // 64 for k in kept)
     assert int(count) == pool - held
+
+
+@pytest.mark.parametrize("before", ["copy from the host", "fill", "kernel", "joined stream", "its own call"])
+def test_cross_sees_what_the_work_before_it_wrote(before):
+    """The kernel begins before the work before it has ended: queries and lengths written just before, of every kind of
+    work that a stream holds, run at once and captured and replayed, give the bits of a call after a synchronize."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    B, N = 16, 500
+    q, k, v = _cross_inputs(B, 4, 2, 30, N, 128, seed=8)
+    rng = np.random.default_rng(8)
+    lens, host, big = _i32([0] * B), torch.zeros(B, dtype=torch.int32).pin_memory(), torch.ones(1 << 27, device="cuda")
+    src, other = _i32([0] * B), torch.cuda.Stream()
+    x = torch.empty_like(q)
+
+    def run():
+        x.fill_(0)
+        lens.fill_(0)
+        big.mul_(1.0)  # what is before it takes some time
+        if before == "copy from the host":
+            x.copy_(q)
+            lens.copy_(host, non_blocking=True)
+        elif before == "fill":
+            lens.fill_(321)
+            x.copy_(q)
+            x[:, 1].zero_()
+        elif before == "kernel":
+            torch.mul(q, 1, out=x)
+            torch.add(src, 0, out=lens)
+        elif before == "joined stream":
+            now = torch.cuda.current_stream()
+            other.wait_stream(now)
+            with torch.cuda.stream(other):
+                big.mul_(1.0)
+                lens.copy_(src)
+                x.copy_(q)
+            big[:1000].mul_(1.0)
+            now.wait_stream(other)
+        else:
+            lens.copy_(src)
+            x.copy_(apa.attention_cross(q, k, v, lens)[0])
+            return apa.attention_cross(apa.attention_cross(x, k, v, lens)[0], k, v, lens)
+        return apa.attention_cross(x, k, v, lens)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        captured = run()
+    for _ in range(3):
+        n = rng.integers(0, N + 1, B).astype(np.int32)
+        q.copy_(_torch(rng.standard_normal(q.shape), torch.bfloat16))
+        host.copy_(torch.from_numpy(n))
+        src.copy_(host)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        with torch.cuda.stream(side):
+            eager = run()
+        torch.cuda.synchronize()
+        a = q.clone()
+        at = _i32([321] * B) if before == "fill" else _i32(n)
+        if before == "fill":
+            a[:, 1] = 0
+        want = apa.attention_cross(a, k, v, at)
+        if before == "its own call":
+            for _ in range(2):
+                torch.cuda.synchronize()
+                want = apa.attention_cross(want[0], k, v, at)
+        torch.cuda.synchronize()
+        assert _same(got, want) and _same(eager, want)
+    apa.check_error()
