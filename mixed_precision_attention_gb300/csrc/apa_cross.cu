@@ -4,9 +4,9 @@
 // K and V tiles come by TMA (any strides); keys past Nkv arrive as zeros, and where a
 // sequence ends before, its last tile's values behind the end are set to zero in shared
 // memory, as a weight of 0 does not hide a NaN.
-// A decoding step is bound by HBM: 64 sequences of up to 4096 keys, G = 3, d = 128, 116 us, 5.8
+// A decoding step is bound by HBM: 64 sequences of up to 4096 keys, G = 3, d = 128, 118 us, 5.7
 // TB/s of the copy's 6.8.  Prompts are bound by the products and what lies between them (rows.cuh):
-// 4 x 2048 rows, 24 heads on 8, to 8192 keys, 413 us, 0.67 of the measured BF16 rate; with all
+// 4 x 2048 rows, 24 heads on 8, to 8192 keys, 410 us, 0.68 of the measured BF16 rate; with all
 // lengths 8192 604 us, 0.71.
 #include "rows.cuh"
 

@@ -13,8 +13,8 @@
 // holds channels g and 8 + g of 16, one FP16 pair: the pairs are stored side by side (kPairedV),
 // and the epilogue puts O's columns in order again, which costs no instruction.
 //
-// Trees of up to 64 nodes, G = 4, over 4 contexts to 131072 keys: 198 us (the products alone 90 at
-// the measured rate, the pages' bytes 31); of up to 32 nodes, G = 3, over 32 contexts to 8192 keys 104 us.
+// Trees of up to 64 nodes, G = 4, over 4 contexts to 131072 keys: 194 us (the products alone 90 at
+// the measured rate, the pages' bytes 31); of up to 32 nodes, G = 3, over 32 contexts to 8192 keys 100 us.
 // A page costs a CTA's four decoding warps 1900 to 2400 cycles (some 200 instructions each, 5
 // cycles apart: fixed latencies, instruction fetch and the softmax warps' slots), and the SM
 // twice the issue slots of the softmax of one block.  Eight such warps in two teams were slower

@@ -25,8 +25,8 @@
 //     S, so that a group's next S is there when it has stored P; Q in shared memory, as tensor
 //     memory is full.
 //   Items of one block at d <= 128: two CTAs per SM with one group and half of tensor memory
-//     each, so that one works while the other begins an item (64 rows of G = 3 over 4096 keys
-//     each: 116 us, 129 with one CTA of two groups; d = 64, any number of rows, likewise: 2048
+//     each, so that one works while the other begins an item (a row of 64 sequences, G = 3, over
+//     up to 4096 keys: 118 us, 129 with one CTA of two groups; d = 64, any number of rows, likewise: 2048
 //     rows of prompts 493 us, 537).  Q is an operand in tensor memory: S of 64 keys would
 //     otherwise read 6 KB of shared memory per 32 cycles of product, 1.5 times what it delivers.
 //   d = 256: O takes half of tensor memory: one group, one CTA.
@@ -38,7 +38,13 @@
 // thread as issuer (1900 cycles a use), one issuer for both groups (1140), tiles of 128 keys
 // (1230 TF/s on prompts where this form has 1350, and registers spill), all 64 scores in
 // registers at once where there are more than 12 warps (spills that miss the cache), register
-// shares by setmaxnreg (the compiler keeps to the launch's count).
+// shares by setmaxnreg (the compiler keeps to the launch's count), two threads per row, each
+// with half of a tile's keys, where a block has at most 64 rows (trees of 32 nodes 114 us for 100).
+//
+// The kernel is launched while the one before it ends (programmatic dependent launch): barriers
+// and tensor memory are set up meanwhile.  Everything that another kernel may have written is
+// read behind griddepcontrol.wait (with it, and segments found without divisions, trees of 32
+// nodes over 32 contexts went from 104 to 100 us, 64-node trees over 131072 keys from 197 to 194).
 #pragma once
 #include <atomic>
 #include <cfloat>
@@ -75,7 +81,7 @@ struct RowCut {
 };
 // How many CTAs share `total` uses.  A CTA takes no fewer than k uses, where k follows the tiles of an item: joining the
 // parts costs in their number (four parts a microsecond), a tile about one itself (17 tiles an item: 22 us with
-// k = 1, 25 with 2, 26 with 4; 128 tiles: 54, and 29 with 4).
+// k = 1, 25 with 2, 26 with 4; 128 tiles: 54, and 29 with 4; taken before beginning an item counted as uses).
 __device__ __forceinline__ int cut_ctas(long long total, long long items, int grid) {
   int k = 1;
   while (k < 8 && 20 * k * k * items < total) k *= 2;
@@ -127,7 +133,7 @@ struct RowCfg {
   static constexpr bool kSoftRelease = NB == 1;
   static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
   // What beginning an item takes, in uses.  Without it (0) CTAs with many short items end last: trees of 32 nodes over 32
-  // contexts to 8192 keys 127 us, 104 with 7 (106 with 10); prompts of 2048 rows 440 us, 413 with 20 (420 with 34); 333 rows
+  // contexts to 8192 keys 127 us, 104 with 7 (106 with 10); prompts of 2048 rows 440 us, 410 with 20 (420 with 34); 333 rows
   // at d = 256 40 us, 32 with 12.
   static constexpr int kItemCost = NG == 2 ? 20 : D == 256 ? 12 : 7;
   static_assert(NG == 1 || (NK % 2 == 0 && NV % 2 == 0), "RowShare");

@@ -520,3 +520,15 @@ def test_cross_sees_what_the_work_before_it_wrote(before):
         torch.cuda.synchronize()
         assert _same(got, want) and _same(eager, want)
     apa.check_error()
+
+
+def test_an_empty_batch_is_refused():
+    import mixed_precision_attention_gb300 as apa
+    a, _, _ = _step(np.random.default_rng(9), 2, 4, 2, 40, 64, [100, 40], [40, 4])
+    none = {k: a[k][:0] for k in ("q", "block_table", "lens", "nodes", "mask", "depths")}
+    for kw in (none, dict(none, mask=a["mask"][:1], depths=a["depths"][:1])):
+        with pytest.raises((ValueError, apa.ApaError)):
+            apa.attention_tree(**dict(a, **kw))
+    q, k, v = _cross_inputs(2, 4, 2, 5, 20, 64)
+    with pytest.raises((ValueError, apa.ApaError)):
+        apa.attention_cross(q[:0], k[:0], v[:0])
