@@ -384,7 +384,7 @@ size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
 /* Attention of the drafted rows over the cache.  Row i < nodes[b] of sequence b sees the
  * context's keys j < base and the keys of the nodes n < nodes[b] whose bit it has; with
  * window >= 1 only those of them whose position is above base + depth(i) - window, or below
- * sinks.  window = 0: all of them.
+ * sinks (more than 2^31 - 64 count as that many).  window = 0: all of them.
  *   q        dtype (APA_DTYPE_*) [B][Hq][Nq][d]; channels contiguous, the rest at the given
  *            strides (in elements, multiples of 8; of an axis of length 1 any); 16-byte aligned
  *   pages, block_table, k_scale, v_scale  as in apa_attention_cache

@@ -104,6 +104,8 @@ struct TreeSrc {
     int window, sinks;
   };
   // Keys len, of which the last `nodes` are the drafted ones; tiles: pages that hold sinks, then those from lo on.
+  // len is at most 2^31 - 64 (tables have fewer than 2^25 entries), and so is a context key's position; a node's, base +
+  // depth, may pass 2^31: what compares it does so from base.
   struct Seq {
     int blocks, tiles, len, base, nodes, n_sink, lo;
     Seq() = default;
@@ -162,13 +164,15 @@ struct TreeSrc {
         drafted = __funnelshift_r(lo, hi, sh) & below(s.nodes - at) & ~ctx;
       }
       if (p.window) {
-        const int first = s.base + depth - p.window + 1;  // the window's first position
-        ctx &= ~below(first - j) | below(p.sinks - j);
+        // The window's first position is base - back; all of the context is before it if that is past base.  (Where j is past
+        // base there is no context, and the difference may wrap.)
+        const int back = p.window - 1 - depth;
+        ctx &= ~below((int)((unsigned)(s.base - j) - (unsigned)max(back, 0))) | below(p.sinks - j);
         if (p.window < p.r.Nq)  // only then may a drafted key lie behind it
           for (uint32_t x = drafted; x; x &= x - 1) {
             const int k = __ffs(x) - 1;
-            const int pk = s.base + max(0, min(p.depths[b * p.depth_stride + at + k], p.r.Nq - 1));
-            if (pk < first && pk >= p.sinks) drafted &= ~(1u << k);
+            const int dk = max(0, min(p.depths[b * p.depth_stride + at + k], p.r.Nq - 1));
+            if (dk < -back && dk >= p.sinks - s.base) drafted &= ~(1u << k);
           }
       }
       return ctx | drafted;
@@ -191,8 +195,8 @@ struct TreeSrc {
   static __device__ __forceinline__ void plain(const Params& p, const RowWalk<TreeSrc>& walk, int& lo, int& hi) {
     const Seq& s = walk.seq;
     const int off = s.n_sink - s.lo - walk.g.t0;  // from a page to the segment's tile
-    const int first = s.base + p.r.Nq - 1 - p.window;  // (a key at or before it may be hidden)
-    lo = max(s.lo, p.window && first >= 0 ? first / kTile + 1 : 0) + off;
+    const long long first = (long long)s.base + p.r.Nq - 1 - p.window;  // (a key at or before it may be hidden)
+    lo = max(s.lo, p.window && first >= 0 ? (int)(first / kTile) + 1 : 0) + off;
     hi = s.base / kTile + off;
   }
 
@@ -381,10 +385,10 @@ int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long 
   const size_t need = apa_attention_tree_workspace_bytes(B, Hq, Hkv, Nq, d);
   void* ws = workspace;
   if (ws && (workspace_bytes < need || ((uintptr_t)ws & 255))) return APA_ERR_NOMEM;
-  // (positions stay within 32 bits: none exceeds 64 * max_pages + Nq)
-  const int most = max_pages * kTile + Nq;
-  if (window > most) window = 0;
-  if (sinks > most) sinks = most;
+  // (past every position, of which none exceeds 64 * max_pages + Nq: that may pass 2^31)
+  if (window > (long long)max_pages * kTile + Nq) window = 0;
+  // (past every key of the largest table; whole pages of them are counted in 32 bits)
+  if (sinks > 0x7FFFFFFF - (kTile - 1)) sinks = 0x7FFFFFFF - (kTile - 1);
   if (!ws && cudaMallocAsync(&ws, need, stream) != cudaSuccess) return APA_ERR_NOMEM;
   const bool f16 = dtype == APA_DTYPE_F16;
   auto go = [&](auto src) {
