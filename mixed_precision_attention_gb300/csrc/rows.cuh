@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
       const float fo = L == 0.f ? 0.f : ex2_approx(M - mx);
       const float f = ml[k].y == 0.f ? 0.f : ex2_approx(ml[k].x - mx);  // (a NaN sum goes on to the output)
       M = mx;
-      L = f == 0.f ? L * fo : fmaf(f, ml[k].y, L * fo);
+      L = fmaf(f, ml[k].y, L * fo);  // (also with f = 0: a part of scores that are no numbers has no maximum, but a NaN sum)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {  // (a part without weight may hold anything)
         acc[4 * c] = f == 0.f ? acc[4 * c] * fo : fmaf(f, o[k][c].x, acc[4 * c] * fo);

@@ -68,3 +68,43 @@ def test_tree_sinks_past_every_position_of_the_largest_table():
     for sinks in (1064, 2 ** 31 - 64, 2 ** 31 - 1, 2 ** 40):
         assert _same(apa.attention_tree(**dict(a, block_table=table), window=2, sinks=sinks), want), sinks
     apa.check_error()
+
+
+# ------------------------------------------------------------------ no numbers in a part of a split walk
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [1, 90, 150])
+@pytest.mark.parametrize("at", [0, 300, 576])
+def test_cross_a_key_that_is_no_number_reaches_every_row(d, Nq, at):
+    """Every row sees it, so by the formula every output is NaN; key 576 is alone in the last of ten tiles, which a CTA of
+    its own takes, and whose part has a sum but no maximum."""
+    import mixed_precision_attention_gb300 as apa
+    q, k, v = _cross_inputs(1, 4, 2, Nq, 577, d, seed=at)
+    k[0, :, at, 3] = math.nan
+    out, lse = apa.attention_cross(q, k, v)
+    apa.check_error()
+    assert out.isnan().all() and lse.isnan().all()
+    want = apa.attention_cross(q[:, :2], k[:, :1], v[:, :1])
+    k[0, 1, at, 3] = 0  # head 1 has numbers again, head 0 keeps its own
+    got = apa.attention_cross(q, k, v)
+    assert not got[0][:, 2:].isnan().any() and got[0][:, :2].isnan().all() and want[0].isnan().all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [3, 40])
+@pytest.mark.parametrize("page", [0, 4, 9])
+def test_tree_a_page_of_keys_that_are_no_numbers_reaches_the_rows_that_see_it(d, Nq, page):
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    a, _, _ = _step(np.random.default_rng(d + page), 1, 4, 1, Nq, d, [640], [Nq])
+    want = apa.attention_tree(**a, window=200, sinks=1)
+    pool = a["pages"][int(a["block_table"][0, page])].view(1, 4, 18 * d)
+    pool[:, :, 16 * d: 17 * d] = 0x7F  # K's scales
+    out, lse = apa.attention_tree(**a)
+    apa.check_error()
+    assert out.isnan().all() and lse.isnan().all()
+    out, lse = apa.attention_tree(**a, window=200, sinks=1)  # page 4 lies between the sink and every window
+    if page == 4:
+        assert _same((out, lse), want)
+    else:
+        assert out.isnan().all() and lse.isnan().all()
