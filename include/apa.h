@@ -405,7 +405,8 @@ size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  * Keys past lens[b], and keys up to base - window that are no sinks (which no depth sees), are
  * never used, whatever a page holds there; scores that a row does not see are dropped whatever
  * they are, but a NaN in V at any other key may reach rows that do not see it.  Numerics are
- * those of apa_attention_cache.  Nq <= APA_TREE_MAX_NODES, B <= 8192, B * max_pages < 2^29.  The work
+ * those of apa_attention_cache.  Scores times log2(e) lie within +-2^24: a row whose largest is
+ * beyond is NaN, lse too; one with others beyond may be.  Nq <= APA_TREE_MAX_NODES, B <= 8192, B * max_pages < 2^29.  The work
  * is split over the GPU by the lengths alone, so reruns are bitwise equal. */
 int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
                        long long q_row_stride, const uint8_t* pages, int num_pages, const int32_t* block_table,
@@ -458,7 +459,9 @@ int apa_cache_accept(uint8_t* pages, int layers, int num_pages, int Hkv, int d, 
  *            have it allocated stream-ordered for the call.  Two calls that overlap on the
  *            GPU must not share one.
  * Scores, softmax statistics and sums are FP32; the softmax weights are rounded to dtype for
- * the product with V (2^-8 relative at most in BF16, 2^-11 in FP16).  Nq = 1 (a decoding step)
+ * the product with V (2^-8 relative at most in BF16, 2^-11 in FP16).  Scores times log2(e)
+ * lie within +-2^29 in BF16, +-2^24 in FP16: a row whose largest is beyond is NaN, lse too;
+ * one with others beyond may be.  Nq = 1 (a decoding step)
  * reads each KV head's states once for its G = Hq / Hkv rows.  B <= 8192.  The work is split
  * over the GPU by the lengths alone, so reruns are bitwise equal. */
 int apa_attention_cross(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,

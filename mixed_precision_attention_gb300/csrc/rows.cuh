@@ -132,6 +132,10 @@ struct RowCfg {
   // group hands the stages back.  With two, V would wait for another use: the issuer's commits do.
   static constexpr bool kSoftRelease = NB == 1;
   static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
+  // Where |m| reaches this the roundings of m and kLift - m (an ulp of m: 1 below 2^24, 32 below 2^29) take P out of its
+  // type's range: such rows are NaN.  Rounding x c2 to FP32 before m comes off has no such limit, but cost 1 to 5 % in
+  // each of eight forms tried (a branch per tile, its code in line or not): the loop is bound by its own latency.
+  static constexpr float kFar = F16 ? 16777216.f : 536870912.f;
   // What beginning an item takes, in uses.  Without it (0) CTAs with many short items end last: trees of 32 nodes over 32
   // contexts to 8192 keys 127 us, 104 with 7 (106 with 10); prompts of 2048 rows 440 us, 410 with 20 (420 with 34); 333 rows
   // at d = 256 40 us, 32 with 12.
@@ -291,6 +295,19 @@ struct RowBars {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
   }
 };
+
+// What a row's O is multiplied by, and its lse: 0 and -inf where it has seen no key, NaN where its maximum is too far from 0
+// (its weights, and their sum, may have become 0 there).
+template <class C>
+__device__ __forceinline__ float rows_inverse(float m, float l, float v_scale) {
+  if (m == -INFINITY && l == 0.f) return 0.f;
+  return fabsf(m) < C::kFar ? v_scale / l : __int_as_float(0x7FFFFFFF);
+}
+template <class C>
+__device__ __forceinline__ float rows_lse(float m, float l) {
+  if (m == -INFINITY && l == 0.f) return -INFINITY;
+  return fabsf(m) < C::kFar ? kLn2 * (m - C::kLift + log2f(l)) : __int_as_float(0x7FFFFFFF);
+}
 
 // The column of O that holds channel c: sources may store V's channels in another order within each 16.
 template <class Src>
@@ -663,10 +680,10 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
                            fmaxf(sv[8 * k + 6], sv[8 * k + 7]));
             rmax = fmaxf(rmax, max3(max3(g8[0], g8[1], g8[2]), g8[3], g8[3]));
           }
-          const float top = rmax * me.c2;  // (c2 > 0)
+          const float top = __fmul_rn(rmax, me.c2);  // (c2 > 0)
           float f = 1.f;
           bool rescale = false;
-          if (top > m2 + kTauRows || (m2 == -INFINITY && top > -INFINITY)) {
+          if (top - m2 > kTauRows) {  // (infinite for a row's first score; a NaN, so false, before it)
             if (l2 > 0.f) {
               f = ex2_approx(m2 - top);
               rescale = true;
@@ -755,7 +772,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
         T += tiles;
         const int slot = 2 * blockIdx.x + (ends ? 1 : 0), prow = (w == 2 ? g * kBlockRows : 0) + row;
         float* part = r.part_o + (size_t)slot * r.slot_rows * D + 4 * prow;
-        const float inv = l2 == 0.f ? 0.f : v_scale / l2;
+        const float inv = rows_inverse<C>(m2, l2, v_scale);
         const uint32_t own = tl + C::kOCol + g * D, other = tl + C::kOCol + (NG == 2 ? (g ^ 1) * D : 0);
         const int c_lo = joint ? g * (D / 2) : 0, c_hi = joint ? c_lo + D / 2 : D;
         if (__any_sync(0xffffffffu, out_row >= 0)) {
@@ -802,7 +819,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
             if (!whole)
               r.part_ml[(size_t)slot * r.slot_rows + prow] = make_float2(m2, l2);
             else if (r.lse)
-              r.lse[out_row] = l2 == 0.f ? -INFINITY : kLn2 * (m2 - C::kLift + log2f(l2));
+              r.lse[out_row] = rows_lse<C>(m2, l2);
           }
         }
         if (joint) {  // no P of the next segment before both groups have read both states
@@ -911,14 +928,14 @@ __global__ void __launch_bounds__(kRowJoinThreads) rows_join_kernel(const __grid
   typename Src::Row me;
   me.set(p, seq, rec.b, rec.h, rec.rb * kBlockRows + row);
   if (me.out_row < 0) return;
-  const float inv = L == 0.f ? 0.f : me.v_scale / L;
+  const float inv = rows_inverse<C>(M, L, me.v_scale);
   uint32_t y[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) y[k] = pack2<Src::kOutF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
   uint4* dst = reinterpret_cast<uint4*>(r.out + (size_t)me.out_row * D + c0);
   dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
   dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-  if (c0 == 0 && r.lse) r.lse[me.out_row] = L == 0.f ? -INFINITY : kLn2 * (M - C::kLift + log2f(L));
+  if (c0 == 0 && r.lse) r.lse[me.out_row] = rows_lse<C>(M, L);
 }
 
 __host__ inline size_t rows_align(size_t x) { return (x + 255) / 256 * 256; }

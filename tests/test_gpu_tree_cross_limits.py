@@ -108,3 +108,93 @@ def test_tree_a_page_of_keys_that_are_no_numbers_reaches_the_rows_that_see_it(d,
         assert _same((out, lse), want)
     else:
         assert out.isnan().all() and lse.isnan().all()
+
+
+# ------------------------------------------------------------------ scores far from 0
+def _far(out, lse, ref, ref_lse, size, half, limit, reach):
+    """Rows whose largest score (ref_lse, but for the log of a sum of few weights) is beyond the limit, in log2 units, are
+    NaN; of the others all are right but those with any score beyond it (reach: the largest magnitude), which may be NaN.
+    What is rounded is the weights (half a step of 16 bits at most), their FP32 sums and the output; scores, sums of up to
+    256 FP32 terms, are off by 256 * 2^-24 = 2^-16 of their size at most, and so is the lse.  Weights that the formula has
+    below 2^-149 are 0 here: 2^-126 covers what they bring to an output."""
+    ln2 = math.log(2)
+    beyond = ref_lse.abs() >= limit * ln2 * 1.01
+    within = ref_lse.abs() <= limit * ln2 * 0.99
+    assert bool(out[beyond].isnan().all()) and bool(lse[beyond].isnan().all())
+    tol = size * (half + 2 ** -14) + ref.abs() * half + 2.0 ** -126
+    right = ((out.double() - ref).abs() <= tol).all(-1)
+    may = within & (reach >= limit * ln2 * 0.99) & out.isnan().all(-1)
+    assert bool((right | may)[within].all())
+    assert bool(((lse.double() - ref_lse).abs() <= ref_lse.abs() * 2 ** -16 + 2 ** -14)[within & right].all())
+    return int(beyond.sum()), int((within & right).sum())
+
+
+LIMIT = {"bf16": 2.0 ** 29, "fp16": 2.0 ** 24}  # by the type of the weights
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power", [3, 6, 9, 12, 14])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_cross_scores_far_from_zero(dtype, d, power, sign):
+    """q.k / sqrt(d) of up to 2^32 or from -2^31: the largest scores win and equal ones share, up to the stated limit."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    from .test_gpu_cross import formula
+    t = _types()[dtype]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(power)
+    N, Nq = 700, 40
+    step = torch.randint(1, 4, (1, 2, N, 1), device="cuda", generator=g).double()   # a key's size, 1 .. 3 eighths below
+    for at in (2, 5, 77, 500, 699):                                                # the ones of the largest score
+        step[:, :, at] = 0 if sign > 0 else 4
+    u = 1 - 2 * torch.randint(0, 2, (1, 1, 1, d), device="cuda", generator=g).double()
+    k = (u * sign * 2.0 ** power * (1 - step / 8)).to(t).expand(1, 2, N, d).contiguous()
+    q = (u * 2.0 ** power).to(t).expand(1, 4, Nq, d).contiguous()
+    v = torch.randn(1, 2, N, d, device="cuda", generator=g).to(t)
+    out, lse = apa.attention_cross(q, k, v)
+    apa.check_error()
+    if power > 3:  # (below, more keys than the largest have weight, which formula() counts as well)
+        w = torch.softmax(q[0, 0, :1].double() @ k[0, 0].double().T / math.sqrt(d), -1)
+        assert int((w > 2.0 ** -100).sum()) == 5
+    ref, ref_lse, size = formula(q, k, v, [N])
+    most = (q[:, :, :1].double() @ k.repeat_interleave(2, 1).double().transpose(2, 3)).abs().max() / math.sqrt(d)
+    beyond, right = _far(out, lse, ref, ref_lse, size, torch.finfo(t).eps / 2, LIMIT[dtype], most)
+    assert beyond + right == lse.numel() and (power < 10 or dtype == "bf16" and power < 13 or beyond == lse.numel())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [3, 60])
+@pytest.mark.parametrize("up", [8, 20, 30, 60])
+def test_tree_scores_far_from_zero(d, Nq, up):
+    """Keys scaled up by powers of two, through their head scales."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    a, kv, parents = _step(np.random.default_rng(d + up), 2, 4, 2, Nq, d, [500, 70], [Nq, Nq])
+    scale = 2.0 ** up
+    a["k_scale"] = a["k_scale"] * scale
+    a["q"] = a["q"].round() * 16  # (whole numbers)
+    from .test_gpu_tree import _tree
+    sees, depths = _tree(parents, [Nq, Nq])
+    q = a["q"].double().cpu().numpy()
+    lens = [500 + Nq, 70 + Nq]
+    far = [np.stack([x[0] * scale, x[1]]) for x in kv]
+    ref, ref_lse, mag = _attend(q, far, lens, [Nq, Nq], sees, depths, 0, 0)
+    out, lse = apa.attention_tree(**a)
+    apa.check_error()
+    # a row counts where its largest score leaves the next different one 200 behind after an error of 2^-15 of it
+    sure, reach = np.zeros(ref_lse.shape, bool), np.zeros(ref_lse.shape)
+    for b in range(2):
+        vis = np.ones((Nq, lens[b]), bool)
+        vis[:, lens[b] - Nq:] = sees[b]
+        for h in range(4):
+            s = np.where(vis, q[b, h] @ far[b][0][h // 2].T / math.sqrt(d), -np.inf)
+            top = s.max(1, keepdims=True)
+            sure[b, h] = ~((s < top) & (s > top - 200 - np.abs(top) * 2.0 ** -15)).any(1)
+            reach[b, h] = np.where(vis, np.abs(s), 0).max(1)
+    at = np.nonzero(sure)
+    pick = lambda x: _torch(x[at]) if isinstance(x, np.ndarray) else x[tuple(_torch(i) for i in at)]  # noqa: E731
+    beyond, right = _far(pick(out), pick(lse), pick(ref), pick(ref_lse), pick(mag), 2.0 ** -8, LIMIT["fp16"], pick(reach))
+    assert beyond > 0 if up >= 20 else beyond == 0 and right > 0
