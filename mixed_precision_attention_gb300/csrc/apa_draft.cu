@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(APA_TREE_MAX_NODES) draft_tree_kernel(const Tr
 // five times a key's bytes; 32 sequences in 28 layers of 8 heads take 16 us, 64 in one layer 4.2
 // (launch, path, table entry and key, one load behind the other).
 constexpr int kAcceptThreads = 256;
+constexpr int kAcceptHeads = 1 << 15;  // of a CTA, at most: it counts its pieces in 32 bits
 struct AcceptParams {
   uint8_t* pages;
   size_t layer_bytes;
@@ -90,6 +91,7 @@ struct AcceptParams {
 template <int D>
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptParams p) {
   constexpr int kKVec = D / 32, kVVec = D / 8, kSVec = D / 64, kPieces = kKVec + 1 + kVVec + kSVec;
+  static_assert((long long)APA_TREE_MAX_NODES * kAcceptHeads * kPieces + kAcceptThreads < (1ll << 31), "pieces of a CTA");
   const int b = blockIdx.x, h0 = blockIdx.y * p.heads, heads = min(p.heads, p.H - h0);
   const int len = p.lens[b], nodes = p.nodes[b], count = p.counts[b];
   const int32_t* path = p.path + (size_t)b * p.path_len;
@@ -197,8 +199,7 @@ int apa_cache_accept(uint8_t* pages, int layers, int num_pages, int Hkv, int d, 
   if ((uintptr_t)pages & 15) return APA_ERR_ALIGN;
   // one head per CTA, several where there are ten thousand CTAs anyway (28 layers x 32 sequences x 8 heads: 16 us, 21 with all heads in one)
   int heads = 1;
-  while (heads < Hkv && (long long)B * layers * ((Hkv + heads - 1) / heads) > 152 * 64) heads *= 2;
-  while ((Hkv + heads - 1) / heads > 65535) heads *= 2;
+  while (heads < Hkv && heads < kAcceptHeads && (long long)B * layers * ((Hkv + heads - 1) / heads) > 152 * 64) heads *= 2;
   const AcceptParams prm{pages, (size_t)num_pages * Hkv * page_head_bytes(d), num_pages, Hkv, heads, block_table, max_pages,
                          lens,  nodes, path, counts, path_len, new_lens, device_error_word()};
   const dim3 grid(B, (Hkv + heads - 1) / heads, layers);

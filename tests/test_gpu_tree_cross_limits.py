@@ -198,3 +198,31 @@ def test_tree_scores_far_from_zero(d, Nq, up):
     pick = lambda x: _torch(x[at]) if isinstance(x, np.ndarray) else x[tuple(_torch(i) for i in at)]  # noqa: E731
     beyond, right = _far(pick(out), pick(lse), pick(ref), pick(ref_lse), pick(mag), 2.0 ** -8, LIMIT["fp16"], pick(reach))
     assert beyond > 0 if up >= 20 else beyond == 0 and right > 0
+
+
+# ------------------------------------------------------------------ the accepted path
+@pytest.mark.parametrize("layers,H,B,Nq,most", [(6, 6, 300, 9, 5), (1, 20, 1500, 6, 6), (2, 257, 40, 20, 4)])
+def test_cache_accept_several_heads_of_a_cta(layers, H, B, Nq, most):
+    """Where layers, sequences and heads are many a CTA takes two, four or more heads, the last one what is left."""
+    import mixed_precision_attention_gb300 as apa
+    from .test_gpu_tree import _accept
+    rng = np.random.default_rng(B)
+    base = rng.integers(0, 64, B)
+    nodes = rng.integers(1, Nq + 1, B)
+    lens = base + nodes
+    held = (lens + 63) // 64
+    table, at = np.full((B, 2), -1), np.cumsum(held) - held
+    ids = rng.permutation(int(held.sum()))
+    for b in range(B):
+        table[b, :held[b]] = ids[at[b]:at[b] + held[b]]
+    counts = np.minimum(rng.integers(0, most + 1, B), nodes)
+    path = np.full((B, most), 7)
+    for b in range(B):
+        path[b, :counts[b]] = np.sort(rng.choice(nodes[b], counts[b], replace=False))
+    pages = rng.integers(0, 256, (layers, len(ids), H, 72 * 64), dtype=np.uint8)
+    want = _accept(pages, table, base, path, counts)
+    p = _torch(pages)
+    new = apa.cache_accept(p, _i32(table), _i32(lens), _i32(nodes), _i32(path), _i32(counts))
+    apa.check_error()
+    assert np.array_equal(new.cpu().numpy(), base + counts)
+    assert np.array_equal(p.cpu().numpy(), want)
