@@ -435,7 +435,8 @@ int apa_draft_tree(const int32_t* parents, const int32_t* nodes, int B, int Nq, 
  *   lens, nodes  int32 [B], as in apa_attention_tree
  *   path     int32 [B][path_len], rising node numbers below nodes[b] in the first counts[b]
  *            places; counts int32 [B], each in [0, min(path_len, nodes[b])]
- *   new_lens int32 [B]: base + counts[b]; not lens itself
+ *   new_lens int32 [B]: base + counts[b]; memory of its own (APA_ERR_SHAPE where it overlaps
+ *            block_table, lens, nodes, path or counts)
  * A sequence whose lengths, count or path break this keeps its context (new_lens is base) and
  * nothing of it moves; that, and a table entry outside the pool (nothing is moved from or to
  * it), is reported by apa_check_error.  Keys move as whole bytes: nothing is quantized anew. */

@@ -193,7 +193,15 @@ int apa_cache_accept(uint8_t* pages, int layers, int num_pages, int Hkv, int d, 
                      int B, int32_t* new_lens, cudaStream_t stream) {
   if (!pages || !block_table || !lens || !nodes || !path || !counts || !new_lens) return APA_ERR_NULL;
   if (layers < 1 || layers > 65535 || num_pages < 1 || num_pages >= (1 << 25) || Hkv < 1 || Hkv > (1 << 16) || max_pages < 1 ||
-      max_pages >= (1 << 25) || path_len < 1 || path_len > APA_TREE_MAX_NODES || B < 1 || new_lens == lens)
+      max_pages >= (1 << 25) || path_len < 1 || path_len > APA_TREE_MAX_NODES || B < 1)
+    return APA_ERR_SHAPE;
+  // a sequence's first CTA writes new_lens while its others may not have read theirs
+  auto within = [&](const int32_t* in, long long words) {
+    const uintptr_t a = (uintptr_t)in, n = (uintptr_t)new_lens;
+    return n < a + 4 * (uintptr_t)words && a < n + 4 * (uintptr_t)B;
+  };
+  if (within(lens, B) || within(nodes, B) || within(counts, B) || within(path, (long long)B * path_len) ||
+      within(block_table, (long long)B * max_pages))
     return APA_ERR_SHAPE;
   if (d != 64 && d != 128 && d != 256) return APA_ERR_HEAD_DIM;
   if ((uintptr_t)pages & 15) return APA_ERR_ALIGN;

@@ -1,0 +1,26 @@
+"""Refusals of drafted trees and cross attention at the ends of their ranges, on the host (CPU only: the fake pointers below
+are never dereferenced, and what is not refused ends at the launch, without a GPU)."""
+import pytest
+import torch
+
+from .test_tree_cross_abi import A, P, _accept, lib  # noqa: F401 (lib: the fixture)
+
+W = 4  # bytes of a word
+
+
+@pytest.mark.parametrize("of", ["lens", "nodes", "counts", "path", "table"])
+@pytest.mark.parametrize("B,shift", [(2, 0), (2, 1), (2, -1), (300, 299), (300, -299)])
+def test_accept_refuses_new_lens_inside_what_it_reads(lib, of, B, shift):  # noqa: F811
+    """Other CTAs of a sequence may read these when its first has written new_lens."""
+    at = dict(lens=A[2], nodes=A[3], counts=A[5], path=A[4], table=A[1])[of].value
+    assert _accept(lib, B=B, new=P(at + W * shift)) == -2
+
+
+@pytest.mark.parametrize("of,words", [("lens", 2), ("nodes", 2), ("counts", 2), ("path", 2 * 3), ("table", 2 * 4)])
+def test_accept_takes_new_lens_next_to_what_it_reads(lib, of, words):  # noqa: F811
+    at = dict(lens=A[2], nodes=A[3], counts=A[5], path=A[4], table=A[1])[of].value
+    if torch.cuda.is_available():
+        pytest.skip("would run on made-up pointers")
+    for new in (at + W * words, at - W * 2):
+        assert _accept(lib, new=P(new)) == -5
+    assert _accept(lib, new=P(at + W * (words - 1))) == -2
