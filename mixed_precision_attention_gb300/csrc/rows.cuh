@@ -42,9 +42,9 @@
 // with half of a tile's keys, where a block has at most 64 rows (trees of 32 nodes 114 us for 100).
 //
 // The kernel is launched while the one before it ends (programmatic dependent launch): barriers
-// and tensor memory are set up meanwhile.  Everything that another kernel may have written is
-// read behind griddepcontrol.wait (with it, and segments found without divisions, trees of 32
-// nodes over 32 contexts went from 104 to 100 us, 64-node trees over 131072 keys from 197 to 194).
+// are set up meanwhile.  Everything that another kernel may have written is read, and tensor
+// memory taken, behind griddepcontrol.wait (with it, and segments found without divisions, trees
+// of 32 nodes over 32 contexts went from 104 to 100 us, 64-node trees over 131072 keys from 197 to 194).
 #pragma once
 #include <atomic>
 #include <cfloat>
@@ -352,12 +352,13 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
     for (int i = 0; i < Src::kBars; ++i) mbar_init(bars.at(Bars::kNum + i), Src::bar_count(i));
     fence_mbar_init();
   }
+  // (launched early: what is above needs nothing that the kernel before this one writes, and takes nothing that it may still
+  // want: columns of tensor memory, held here, could keep it from ending, and this CTA waits for that)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  // (launched early: what is above needs nothing that the kernel before this one writes)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- the list's length, and this CTA's place in it: each thread sums up a run of sequences
   constexpr int kWarps = Src::kThreads / 32;
   const int run = (r.B + Src::kThreads - 1) / Src::kThreads, b_lo = min(r.B, tid * run), b_hi = min(r.B, b_lo + run);

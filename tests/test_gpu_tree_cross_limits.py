@@ -226,3 +226,56 @@ def test_cache_accept_several_heads_of_a_cta(layers, H, B, Nq, most):
     apa.check_error()
     assert np.array_equal(new.cpu().numpy(), base + counts)
     assert np.array_equal(p.cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ behind a product of matrices
+@pytest.mark.parametrize("d,Nq", [(64, 20), (128, 20), (128, 60), (256, 20)])
+def test_calls_right_behind_products_of_matrices(d, Nq):
+    """As a layer makes them: q out of a projection just before, the output into one just behind, many times without a
+    wait, and captured."""
+    import torch
+
+    import mixed_precision_attention_gb300 as apa
+    B, Hq, H, N = 3, 4, 2, 300
+    a, _, _ = _step(np.random.default_rng(d + Nq), B, Hq, H, Nq, d, [500, 3, 70], [Nq, 1, Nq])
+    _, k, v = _cross_inputs(B, Hq, H, Nq, N, d)
+    wide = Hq * d
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    w1, w2 = (torch.randn(wide, wide, device="cuda", generator=g).div_(math.sqrt(wide)).bfloat16() for _ in range(2))
+    x = torch.randn(B, Nq, wide, device="cuda", generator=g).bfloat16()
+    rows = lambda y: y.view(B, Nq, Hq, d).transpose(1, 2)  # noqa: E731
+    flat = lambda y: y.transpose(1, 2).reshape(B, Nq, wide)  # noqa: E731
+
+    def layer(x, wait=lambda: None):
+        y = x @ w1
+        wait()
+        t, _ = apa.attention_tree(**dict(a, q=rows(y)))
+        wait()
+        y = flat(t) @ w2
+        wait()
+        c, _ = apa.attention_cross(rows(y), k, v)
+        wait()
+        return flat(c) @ w1
+
+    want = x
+    for _ in range(4):
+        want = layer(want, torch.cuda.synchronize)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+    def run():
+        y = x
+        for _ in range(4):
+            y = layer(y)
+        return y
+
+    with torch.cuda.stream(side):
+        eager = run()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        captured = run()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    apa.check_error()
+    assert torch.equal(eager, want) and torch.equal(captured, want)

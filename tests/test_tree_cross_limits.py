@@ -24,3 +24,26 @@ def test_accept_takes_new_lens_next_to_what_it_reads(lib, of, words):  # noqa: F
     for new in (at + W * words, at - W * 2):
         assert _accept(lib, new=P(new)) == -5
     assert _accept(lib, new=P(at + W * (words - 1))) == -2
+
+
+def test_an_early_kernel_takes_tensor_memory_behind_its_wait():
+    """A kernel that is launched while the one before it runs, and takes tensor memory before it waits for that, may keep it
+    from ending: in every kernel text the wait comes first, and what follows is let in only when the columns are taken."""
+    import glob
+    import os
+    import re
+
+    from mixed_precision_attention_gb300 import build
+    found = 0
+    for path in glob.glob(os.path.join(build.CSRC, "*.cu*")):
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for body in text.split("__global__")[1:]:
+            wait, let = body.find('"griddepcontrol.wait;"'), body.find('"griddepcontrol.launch_dependents;"')
+            take = body.find("tmem_alloc(")
+            if take >= 0 and wait >= 0:
+                found += 1
+                assert wait < take, path
+            if take >= 0 and let >= 0:
+                assert take < let, path
+    assert found == 1  # rows_kernel
