@@ -28,6 +28,8 @@ def attention_cross(q, k, v, lens=None, return_lse: bool = True, workspace=None)
     b, Hkv, Nkv, dk = k.shape
     if b != B or dk != d:
         raise ValueError("k and v must be [B, Hkv, Nkv, d] with q's B and d")
+    if (B | Hq | Nq | Hkv | Nkv | d) >> 31:  # (an expanded axis may be as long; a C int would lose its upper bits)
+        raise ValueError("sizes must be below 2^31")
     if lens is not None:
         _need("lens", lens, _i32, 1, index)
         if lens.shape[0] != B:

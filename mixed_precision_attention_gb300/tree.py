@@ -78,6 +78,8 @@ def attention_tree(q, pages, block_table, lens, nodes, mask, k_scale, v_scale, d
     index = _need_rows("q", q, 4)
     B, Hq, Nq, d = q.shape
     num_pages, Hkv, dim = _need_pool(pages, k_scale, v_scale, index)
+    if (B | Hq | Nq | Hkv | num_pages) >> 31:  # (a C int would lose the upper bits)
+        raise ValueError("sizes must be below 2^31")
     if dim != d:
         raise ValueError("pages must be [num_pages, Hkv, 72 * d] with q's d")
     _need("block_table", block_table, _i32, 2, index)

@@ -279,3 +279,15 @@ def test_calls_right_behind_products_of_matrices(d, Nq):
     torch.cuda.synchronize()
     apa.check_error()
     assert torch.equal(eager, want) and torch.equal(captured, want)
+
+
+# ------------------------------------------------------------------ sizes past 32 bits
+def test_cross_refuses_sizes_past_32_bits():
+    """An expanded axis may be longer than 2^32: its length does not lose its upper bits on the way."""
+    import mixed_precision_attention_gb300 as apa
+    q, k, v = _cross_inputs(1, 4, 1, 3, 40, 64)
+    apa.attention_cross(q, k.expand(1, 2, 40, 64), v.expand(1, 2, 40, 64))
+    for heads in (2 ** 32 + 1, 2 ** 32 + 2, 2 ** 31):
+        with pytest.raises(ValueError):
+            apa.attention_cross(q, k.expand(1, heads, 40, 64), v.expand(1, heads, 40, 64))
+    apa.check_error()

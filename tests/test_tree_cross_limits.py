@@ -47,3 +47,49 @@ def test_an_early_kernel_takes_tensor_memory_behind_its_wait():
             if take >= 0 and let >= 0:
                 assert take < let, path
     assert found == 1  # rows_kernel
+
+
+# ------------------------------------------------------------------ lengths past 32 bits
+LONG = 2 ** 32 + 2  # its lower 32 bits alone would be a size that is taken
+
+
+def _bind(monkeypatch, module):
+    """The binding without a GPU: what it hands on to the library."""
+    got = []
+    monkeypatch.setattr(module, "_empty", lambda *a, **k: torch.empty(4, dtype=torch.uint8))
+    monkeypatch.setattr(module, "_enqueue", lambda index, name, *a: got.append(a))
+    for name in ("_need_rows", "_need"):
+        monkeypatch.setattr(module, name, lambda *a: 0)
+    return got
+
+
+@pytest.mark.parametrize("axis", [None, "B", "Hq", "Nq", "Hkv", "Nkv"])
+def test_cross_binding_refuses_lengths_past_32_bits(lib, monkeypatch, axis):  # noqa: F811
+    from mixed_precision_attention_gb300 import cross
+    got = _bind(monkeypatch, cross)
+    n = dict(dict(B=2, Hq=4, Nq=2, Hkv=2, Nkv=8), **({axis: LONG} if axis else {}))
+    q = torch.empty_strided((n["B"], n["Hq"], n["Nq"], 64), (8, 8, 8, 1), dtype=torch.bfloat16, device="meta")
+    k = torch.empty_strided((n["B"], n["Hkv"], n["Nkv"], 64), (8, 8, 8, 1), dtype=torch.bfloat16, device="meta")
+    if axis:
+        with pytest.raises(ValueError):
+            cross.attention_cross(q, k, k)
+    else:
+        cross.attention_cross(q, k, k)
+    assert len(got) == (0 if axis else 1)
+
+
+@pytest.mark.parametrize("axis", [None, "B", "Hq", "Nq", "Hkv", "num_pages"])
+def test_tree_binding_refuses_lengths_past_32_bits(lib, monkeypatch, axis):  # noqa: F811
+    from mixed_precision_attention_gb300 import tree
+    got = _bind(monkeypatch, tree)
+    n = dict(dict(B=2, Hq=4, Nq=2, Hkv=2, num_pages=3), **({axis: LONG} if axis else {}))
+    monkeypatch.setattr(tree, "_need_pool", lambda *a: (n["num_pages"], n["Hkv"], 64))
+    monkeypatch.setattr(tree, "_need_tree", lambda *a: 0)
+    q = torch.empty_strided((n["B"], n["Hq"], n["Nq"], 64), (8, 8, 8, 1), dtype=torch.bfloat16, device="meta")
+    x = torch.empty(n["B"], 1, device="meta")
+    if axis:
+        with pytest.raises(ValueError):
+            tree.attention_tree(q, x, x, x, None, x, x, x)
+    else:
+        tree.attention_tree(q, x, x, x, None, x, x, x)
+    assert len(got) == (0 if axis else 1)
