@@ -128,9 +128,10 @@ struct RowCfg {
   static constexpr int kStagePitch = 144, kStageOff = kVOff + NV * kTileBytes;  // Q on its way to tensor memory: 64 channels
   static constexpr int kSrcOff = kStageOff + (QT ? NG * 128 * kStagePitch : 0);  // of each row; the source's own
   static constexpr int kSoftWarps = 4 * NG, kMmaWarp = kSoftWarps, kSrcWarp = kSoftWarps + NG;
-  // With one buffer the commit of S(i + 1) says that K of that use and V of use i have been read: a lane of the softmax
-  // group hands the stages back.  With two, V would wait for another use: the issuer's commits do.
+  // With one buffer (and one group) the commit of S(i + 1) says that K of that use and V of use i have been read: a lane of
+  // the softmax group hands the stages back.  With two, V would wait for another use: the issuer's commits do.
   static constexpr bool kSoftRelease = NB == 1;
+  static_assert(NG == 1 || NB == 2, "two groups have two buffers each");
   static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
   // Where |m| reaches this the roundings of m and kLift - m (an ulp of m: 1 below 2^24, 32 below 2^29) take P out of its
   // type's range: such rows are NaN.  Rounding x c2 to FP32 before m comes off has no such limit, but cost 1 to 5 % in
@@ -219,9 +220,6 @@ struct RowWalk {
   }
 };
 
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
-}
 // One lane of a warp that is together.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -645,9 +643,8 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
           if (!(ok = bars.warp_wait(bars.at(Bars::kS + g * C::NB + buf), ((n + i) / C::NB) & 1))) break;
           const uint32_t scol = tl + C::kSCol + (g * C::NB + buf) * KT, pcol = scol + C::kPOff;
           if (C::kSoftRelease && (warp & 3) == 0 && lane == 0) {
-            const uint32_t count = NG == 2 && w == 1 ? 2 : 1;  // (a tile that the other group has no part in counts twice)
-            mbar_arrive_n(bars.k_empty(T + share.tile(i)), count);
-            if (i > 0) mbar_arrive_n(bars.v_empty(T + share.tile(i - 1)), count);
+            mbar_arrive(bars.k_empty(T + share.tile(i)));
+            if (i > 0) mbar_arrive(bars.v_empty(T + share.tile(i - 1)));
           }
           if (warp_idle) {  // (rows of P that nobody uses: whatever is there)
             if (lane == 0) mbar_arrive(bars.at(Bars::kP + g * C::NB + buf));
@@ -769,7 +766,7 @@ __global__ void __launch_bounds__(Src::kThreads, Src::Cfg::kCtasPerSm) rows_kern
         if (!ok) break;
         tc_fence_after();
         if (C::kSoftRelease && (warp & 3) == 0 && lane == 0 && share.uses > 0)  // the last use's V
-          mbar_arrive_n(bars.v_empty(T + share.tile(share.uses - 1)), NG == 2 && w == 1 ? 2 : 1);
+          mbar_arrive(bars.v_empty(T + share.tile(share.uses - 1)));
         T += tiles;
         const int slot = 2 * blockIdx.x + (ends ? 1 : 0), prow = (w == 2 ? g * kBlockRows : 0) + row;
         float* part = r.part_o + (size_t)slot * r.slot_rows * D + 4 * prow;
