@@ -406,8 +406,11 @@ size_t apa_attention_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d
  * never used, whatever a page holds there; scores that a row does not see are dropped whatever
  * they are, but a NaN in V at any other key may reach rows that do not see it.  Numerics are
  * those of apa_attention_cache.  Scores times log2(e) lie within +-2^24: a row whose largest is
- * beyond is NaN, lse too; one with others beyond may be.  Nq <= APA_TREE_MAX_NODES, B <= 8192, B * max_pages < 2^29.  The work
- * is split over the GPU by the lengths alone, so reruns are bitwise equal. */
+ * beyond is NaN, lse too; one with others beyond may be.  The work is split over the GPU by the
+ * lengths alone, so reruns are bitwise equal.
+ * Sizes (else APA_ERR_SHAPE), G = Hq / Hkv: Nq <= APA_TREE_MAX_NODES, B <= 8192, Hkv <= 2^16,
+ * G * Nq <= 2^20, B * Hq * Nq <= 2^31 - 16, num_pages and max_pages < 2^25, B * max_pages < 2^29;
+ * U = B * (max_pages + 16) * (G * Nq + 255) / 128, not rounded, < 2^31, and U * Hkv < 2^37. */
 int apa_attention_tree(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
                        long long q_row_stride, const uint8_t* pages, int num_pages, const int32_t* block_table,
                        int max_pages, const int32_t* lens, const int32_t* nodes, const uint32_t* mask,
@@ -420,7 +423,8 @@ size_t apa_attention_tree_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d)
  *   parents  int32 [B][Nq]: a node's parent, a node before it, or -1: the context (others
  *            count as -1 and are reported by apa_check_error)
  *   nodes    int32 [B], each in [0, Nq] (clamped and reported); null: Nq for all
- *   mask     uint32 [B][Nq][ceil(Nq/32)]: a node's ancestors and itself; 0 from nodes[b] on
+ *   mask     uint32 [B][Nq][ceil(Nq/32)]: a node's ancestors and itself; 0 from nodes[b] on.
+ *            16-byte aligned (else APA_ERR_ALIGN)
  *   depths   int32 [B][Nq]: its ancestors' number (a rotary position is base + depth); 0 from
  *            nodes[b] on
  * Nq <= APA_TREE_MAX_NODES. */
@@ -439,7 +443,9 @@ int apa_draft_tree(const int32_t* parents, const int32_t* nodes, int B, int Nq, 
  *            block_table, lens, nodes, path or counts)
  * A sequence whose lengths, count or path break this keeps its context (new_lens is base) and
  * nothing of it moves; that, and a table entry outside the pool (nothing is moved from or to
- * it), is reported by apa_check_error.  Keys move as whole bytes: nothing is quantized anew. */
+ * it), is reported by apa_check_error.  Keys move as whole bytes: nothing is quantized anew.
+ * Sizes (else APA_ERR_SHAPE): layers <= 65535, Hkv <= 2^16, path_len <= APA_TREE_MAX_NODES,
+ * num_pages and max_pages < 2^25. */
 int apa_cache_accept(uint8_t* pages, int layers, int num_pages, int Hkv, int d, const int32_t* block_table, int max_pages,
                      const int32_t* lens, const int32_t* nodes, const int32_t* path, int path_len, const int32_t* counts,
                      int B, int32_t* new_lens, cudaStream_t stream);
@@ -463,8 +469,11 @@ int apa_cache_accept(uint8_t* pages, int layers, int num_pages, int Hkv, int d, 
  * the product with V (2^-8 relative at most in BF16, 2^-11 in FP16).  Scores times log2(e)
  * lie within +-2^29 in BF16, +-2^24 in FP16: a row whose largest is beyond is NaN, lse too;
  * one with others beyond may be.  Nq = 1 (a decoding step)
- * reads each KV head's states once for its G = Hq / Hkv rows.  B <= 8192.  The work is split
- * over the GPU by the lengths alone, so reruns are bitwise equal. */
+ * reads each KV head's states once for its G = Hq / Hkv rows.  The work is split over the GPU by
+ * the lengths alone, so reruns are bitwise equal.
+ * Sizes (else APA_ERR_SHAPE): B <= 8192, Hkv <= 2^16, G * Nq <= 2^20, B * Hq * Nq <= 2^31 - 16,
+ * 1 <= Nkv <= 2^30; U = B * (ceil(Nkv / 64) + 16) * (G * Nq + 255) / 128, not rounded,
+ * < 2^31, and U * Hkv < 2^37.  Strides of k and v are below 2^39 (else APA_ERR_ALIGN). */
 int apa_attention_cross(const void* q, int dtype, long long q_batch_stride, long long q_head_stride,
                         long long q_row_stride, const void* k, long long k_batch_stride, long long k_head_stride,
                         long long k_token_stride, const void* v, long long v_batch_stride, long long v_head_stride,

@@ -3,7 +3,7 @@ are never dereferenced, and what is not refused ends at the launch, without a GP
 import pytest
 import torch
 
-from .test_tree_cross_abi import A, P, _accept, lib  # noqa: F401 (lib: the fixture)
+from .test_tree_cross_abi import A, P, _accept, _cross, _draft, _tree, lib  # noqa: F401 (lib: the fixture)
 
 W = 4  # bytes of a word
 
@@ -93,3 +93,65 @@ def test_tree_binding_refuses_lengths_past_32_bits(lib, monkeypatch, axis):  # n
     else:
         tree.attention_tree(q, x, x, x, None, x, x, x)
     assert len(got) == (0 if axis else 1)
+
+
+# ------------------------------------------------------------------ the sizes that the header names
+def _taken(status):
+    """Not refused: there is no GPU to launch on."""
+    return status == -5
+
+
+gpu_free = pytest.mark.skipif(torch.cuda.is_available(), reason="would run on made-up pointers")
+ONE = dict(Hq=1, Hkv=1, Nq=1)  # (G * Nq + 255) / 128 = 2
+
+
+@gpu_free
+@pytest.mark.parametrize("kw,last,past", [
+    (dict(ONE, B=32), dict(max_pages=2 ** 24 - 1), dict(max_pages=2 ** 24)),                          # B * max_pages
+    (dict(ONE, B=1), dict(max_pages=2 ** 25 - 1), dict(max_pages=2 ** 25)),
+    (dict(ONE, B=1), dict(num_pages=2 ** 25 - 1), dict(num_pages=2 ** 25)),
+    (dict(B=64, Hq=257, Hkv=1, Nq=1), dict(max_pages=2 ** 23 - 17), dict(max_pages=2 ** 23 - 16)),     # U = 2^31: factor 4
+    (dict(B=64, Hq=128, Hkv=128, Nq=1), dict(max_pages=2 ** 23 - 17), dict(max_pages=2 ** 23 - 16)),   # U * Hkv = 2^37
+    (dict(B=1, Hkv=1, Nq=1024), dict(Hq=1024), dict(Hq=1025)),                                         # G * Nq = 2^20
+    (dict(B=1, Nq=1), dict(Hq=2 ** 16, Hkv=2 ** 16), dict(Hq=2 ** 16 + 1, Hkv=2 ** 16 + 1)),
+    (dict(Hq=2 ** 16, Hkv=2 ** 16, Nq=1), dict(B=8192), dict(B=8193)),
+    (dict(Hq=2 ** 16, Hkv=2 ** 16, Nq=1023), dict(B=32), dict(B=33)),                                  # B * Hq * Nq
+])
+def test_tree_sizes(lib, kw, last, past):  # noqa: F811
+    assert _taken(_tree(lib, **dict(kw, **last)))
+    assert _tree(lib, **dict(kw, **past)) == -2
+
+
+@gpu_free
+@pytest.mark.parametrize("kw,last,past", [
+    (dict(ONE, B=8192), dict(Nkv=64 * (2 ** 17 - 17)), dict(Nkv=64 * (2 ** 17 - 17) + 1)),             # U = 2^31
+    (dict(B=4096, Hq=128, Hkv=128, Nq=1), dict(Nkv=64 * (2 ** 17 - 17)), dict(Nkv=64 * (2 ** 17 - 17) + 1)),
+    (dict(ONE, B=1), dict(Nkv=2 ** 30), dict(Nkv=2 ** 30 + 1)),
+    (dict(B=1), dict(Nq=2 ** 19), dict(Nq=2 ** 19 + 1)),                                               # G * Nq = 2^20
+    (dict(Nq=2 ** 19), dict(B=1023), dict(B=1024)),                                                    # B * Hq * Nq
+    (dict(ONE), dict(B=8192), dict(B=8193)),
+    (dict(B=1, Nq=1), dict(Hq=2 ** 16, Hkv=2 ** 16), dict(Hq=2 ** 16 + 1, Hkv=2 ** 16 + 1)),
+])
+def test_cross_sizes(lib, kw, last, past):  # noqa: F811
+    assert _taken(_cross(lib, **dict(kw, **last)))
+    assert _cross(lib, **dict(kw, **past)) == -2
+
+
+@gpu_free
+def test_cross_strides(lib):  # noqa: F811
+    assert _taken(_cross(lib, ks=(2 ** 39 - 8, 64, 128))) and _cross(lib, ks=(2 ** 39, 64, 128)) == -8
+    assert _taken(_cross(lib, vs=(64, 2 ** 39 - 8, 128))) and _cross(lib, vs=(64, 2 ** 39, 128)) == -8
+
+
+@gpu_free
+@pytest.mark.parametrize("last,past", [
+    (dict(layers=65535), dict(layers=65536)), (dict(Hkv=2 ** 16), dict(Hkv=2 ** 16 + 1)), (dict(most=1024), dict(most=1025)),
+    (dict(num_pages=2 ** 25 - 1), dict(num_pages=2 ** 25))])
+def test_accept_sizes(lib, last, past):  # noqa: F811
+    assert _taken(_accept(lib, **last)) and _accept(lib, **past) == -2
+
+
+@gpu_free
+def test_draft_sizes_and_alignment(lib):  # noqa: F811
+    assert _taken(_draft(lib, Nq=1024)) and _draft(lib, Nq=1025) == -2
+    assert all(_draft(lib, Nq=n, mask=P(A[1].value + 4)) == -8 for n in (1, 5, 128))
