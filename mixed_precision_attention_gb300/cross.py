@@ -17,7 +17,8 @@ def attention_cross(q, k, v, lens=None, return_lse: bool = True, workspace=None)
     stride that is a multiple of 8 elements (projections' [B, N, H, d] outputs go in as ``x.transpose(1, 2)``;
     k and v may be expanded over the batch or the heads).  lens: int32 [B], the keys of each sequence, or None:
     all Nkv.  Returns (out [B, Hq, Nq, d] of q's dtype, contiguous; lse fp32 [B, Hq, Nq] or None); rows of a
-    sequence without keys give zeros and -inf.
+    sequence without keys give zeros and -inf; those whose largest score is beyond 2^29 in bf16, 2^24 in fp16
+    (times log2 e) NaN.
     workspace: optional uint8 CUDA tensor of at least attention_cross_workspace_bytes(...) bytes, 256-byte
     aligned; calls that can overlap on the GPU need one each."""
     index = _need_rows("q", q, 4)

@@ -6,8 +6,8 @@
 // memory, as a weight of 0 does not hide a NaN.
 // A decoding step is bound by HBM: 64 sequences of up to 4096 keys, G = 3, d = 128, 118 us, 5.7
 // TB/s of the copy's 6.8.  Prompts are bound by the products and what lies between them (rows.cuh):
-// 4 x 2048 rows, 24 heads on 8, to 8192 keys, 410 us, 0.68 of the measured BF16 rate; with all
-// lengths 8192 604 us, 0.71.
+// 4 x 2048 rows, 24 heads on 8, to 8192 keys, 413 us, 0.67 of the measured BF16 rate; with all
+// lengths 8192 597 us, 0.71 (d = 64: 485 us, 0.44; d = 256: 1243 us, 0.69).
 #include "rows.cuh"
 
 namespace apa {

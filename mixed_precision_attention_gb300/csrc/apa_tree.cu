@@ -15,9 +15,9 @@
 //
 // Trees of up to 64 nodes, G = 4, over 4 contexts to 131072 keys: 194 us (the products alone 90 at
 // the measured rate, the pages' bytes 31); of up to 32 nodes, G = 3, over 32 contexts to 8192 keys 100 us.
-// A page costs a CTA's four decoding warps 1900 to 2400 cycles (some 200 instructions each, 5
-// cycles apart: fixed latencies, instruction fetch and the softmax warps' slots), and the SM
-// twice the issue slots of the softmax of one block.  Eight such warps in two teams were slower
+// A page of a head takes the K and V warps 1160 and 1100 cycles in the first case, 1410 and 1900 in the second (some
+// 200 instructions of each of the four warps, 5 to 9 cycles apart: fixed latencies, instruction fetch and the softmax
+// warps' slots), and the SM twice the issue slots of the softmax of one block.  Eight such warps in two teams were slower
 // (155 us for 145 at the time), and so were deeper rings.
 #include "rows.cuh"
 

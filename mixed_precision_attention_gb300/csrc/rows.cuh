@@ -26,15 +26,18 @@
 //     memory is full.
 //   Items of one block at d <= 128: two CTAs per SM with one group and half of tensor memory
 //     each, so that one works while the other begins an item (a row of 64 sequences, G = 3, over
-//     up to 4096 keys: 118 us, 129 with one CTA of two groups; d = 64, any number of rows, likewise: 2048
-//     rows of prompts 493 us, 537).  Q is an operand in tensor memory: S of 64 keys would
-//     otherwise read 6 KB of shared memory per 32 cycles of product, 1.5 times what it delivers.
+//     up to 4096 keys: 118 us, 129 with one CTA of two groups; d = 64, any number of rows, likewise: 4 x 2048
+//     rows, 24 heads on 8, over 8192 keys 493 us, 537; now 485).  Q is an operand in tensor memory: S of 64
+//     keys would otherwise read 6 KB of shared memory per 32 cycles of product, 1.5 times what it delivers.
 //   d = 256: O takes half of tensor memory: one group, one CTA.
 //
 // What bounds it, by traces of single CTAs: at 128 channels a use's products take 512 cycles
-// (640 with Q in shared memory), its exponentials 512 of the special-function units (16 a
-// cycle and SM), and it costs 770 to 850; a segment's beginning and end 10 000 to 15 000,
-// most of it latency, which is why the list counts them.  Tried and not kept: one diverged
+// (640 with Q in shared memory), its 8192 exponentials some 290 of the special-function units (28.5
+// a cycle and SM, measured), and it costs 770 to 850: what is left is hand-overs.  A segment's
+// beginning and end cost 10 000 to 15 000, most of it latency, which is why the list counts them: once per
+// item, in front of its uses, not for the later CTAs that take a part of it.  Where items have few tiles that
+// leaves the work uneven: 24 of the 96 CTAs that share 8 items of 17 tiles get the beginning of one alone, and
+// of 8 x 333 rows (G = 3, d = 256, to 1021 keys) the busiest CTA has 16 uses where the mean is 8.7.  Tried and not kept: one diverged
 // thread as issuer (1900 cycles a use), one issuer for both groups (1140), tiles of 128 keys
 // (1230 TF/s on prompts where this form has 1350, and registers spill), all 64 scores in
 // registers at once where there are more than 12 warps (spills that miss the cache), register
@@ -79,9 +82,10 @@ struct RowCut {
   }
   __device__ __forceinline__ long long first(int i) const { return i >= k ? q * k + r : q * i + min(i, r); }
 };
-// How many CTAs share `total` uses.  A CTA takes no fewer than k uses, where k follows the tiles of an item: joining the
-// parts costs in their number (four parts a microsecond), a tile about one itself (17 tiles an item: 22 us with
-// k = 1, 25 with 2, 26 with 4; 128 tiles: 54, and 29 with 4; taken before beginning an item counted as uses).
+// How many CTAs share a list of `total` units.  A CTA takes no fewer than k, where k follows the units of an item: joining
+// the parts costs in their number, and a use about a microsecond itself (8 items of 17 tiles: trees of 26 nodes over 1000
+// keys 22 us with k = 1, 19 with 2, 19.6 with 4; of 24 tiles: a row over 1500 keys 20, 16.5, 16.2; of 128: over 8192 keys
+// 28, 28, 25).
 __device__ __forceinline__ int cut_ctas(long long total, long long items, int grid) {
   int k = 1;
   while (k < 8 && 20 * k * k * items < total) k *= 2;
@@ -244,6 +248,10 @@ __device__ __forceinline__ void rows_wait_in_flight(uint32_t bar, uint32_t parit
 
 // P of eight consecutive keys, 2^(x*c2 + nb), as four words of two 16-bit values (key 2k in the low
 // half of word k); the FP32 values are added into (s0, s1): even keys into s0, odd keys into s1.
+// The rounding (half a step: 2^-11 in FP16, 2^-8 in BF16) is what the product with V asks for: both its operands have one
+// 16-bit type, and V comes as BF16 or is exact in FP16.  Against 64 bits the outputs' error grows by it from 0.0017, their own
+// rounding's, to 0.0023 of their norm where both are BF16, from 0.00021 to 0.00029 where both are FP16, and not
+// visibly where weights are FP16 and outputs BF16.  Weights in two terms would take twice the products with V.
 // The affine step and the sums run as packed FP32 pairs.
 template <bool F16>
 __device__ __forceinline__ void rows_p8(const float* x, float c2, float nb, uint32_t* h, float& s0, float& s1) {

@@ -72,7 +72,7 @@ def attention_tree(q, pages, block_table, lens, nodes, mask, k_scale, v_scale, d
     Nq] (draft_tree(); one sequence's are for all).  With window >= 1 (which needs depths) a row sees, of those keys,
     the ones whose position is above its own - window, or below sinks; a node's position is lens - nodes + depth.
     Returns (out [B, Hq, Nq, d] of q's dtype, contiguous; lse fp32 [B, Hq, Nq] or None); a row that sees no key, and
-    those from nodes on, give zeros and -inf.
+    those from nodes on, give zeros and -inf; one whose largest score is beyond 2^24 (times log2 e) NaN.
     workspace: optional uint8 CUDA tensor of at least attention_tree_workspace_bytes(...) bytes, 256-byte aligned;
     calls that can overlap on the GPU need one each."""
     index = _need_rows("q", q, 4)
