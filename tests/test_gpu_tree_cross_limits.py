@@ -291,3 +291,30 @@ def test_cross_refuses_sizes_past_32_bits():
         with pytest.raises(ValueError):
             apa.attention_cross(q, k.expand(1, heads, 40, 64), v.expand(1, heads, 40, 64))
     apa.check_error()
+
+
+# ------------------------------------------------------------------ short lists
+@pytest.mark.parametrize("B,Hq,H,Nq,N,d", [(1, 24, 8, 1, 1500, 128), (1, 24, 8, 64, 1500, 128), (1, 8, 8, 100, 700, 256),
+                                           (1, 24, 8, 26, 1026, 64), (3, 6, 2, 333, 1021, 256), (1, 1, 1, 1, 64, 128)])
+def test_cross_lists_that_leave_ctas_without_a_tile(B, Hq, H, Nq, N, d):
+    import mixed_precision_attention_gb300 as apa
+    from .test_gpu_cross import check
+    q, k, v = _cross_inputs(B, Hq, H, Nq, N, d, seed=N)
+    lens = [N, max(1, N // 3), N][:B]
+    got = apa.attention_cross(q, k, v, _i32(lens))
+    apa.check_error()
+    check(q, k, v, lens, got)
+    assert _same(got, apa.attention_cross(q, k, v, _i32(lens)))
+
+
+@pytest.mark.parametrize("Hq,H,Nq,d,base", [(24, 8, 26, 128, 1000), (24, 8, 60, 128, 1400), (8, 8, 100, 256, 600), (16, 4, 5, 64, 700)])
+def test_tree_lists_that_leave_ctas_without_a_tile(Hq, H, Nq, d, base):
+    import mixed_precision_attention_gb300 as apa
+    from .test_gpu_cache import _near
+    from .test_gpu_tree import _tree
+    a, kv, parents = _step(np.random.default_rng(Nq), 1, Hq, H, Nq, d, [base], [Nq])
+    got = apa.attention_tree(**a)
+    apa.check_error()
+    sees, depths = _tree(parents, [Nq])
+    _near(*got, _attend(a["q"].double().cpu().numpy(), kv, [base + Nq], [Nq], sees, depths, 0, 0), "bf16")
+    assert _same(got, apa.attention_tree(**a))

@@ -11,7 +11,7 @@ import pytest
 
 from mixed_precision_attention_gb300 import build
 
-from .test_rows_protocol import Bar, Machine, _segs
+from .test_rows_protocol import Bar, Machine, _check_list, _segs
 
 CORE = ["k", "v", "q", "s", "p", "pv", "rescale", "x", "xd", "qfree"]
 BOTH = {"x", "xd", "qfree"}  # waits of two groups for one another
@@ -213,3 +213,34 @@ def test_each_wait_left_out_is_seen(form, drop):
         except AssertionError:
             return
     raise AssertionError(f"no schedule shows that the wait {drop} is needed")
+
+
+# ------------------------------------------------------------------ the list, by the kernel's own rule
+def _least(units, items):  # cut_ctas
+    k = 1
+    while k < 8 and 20 * k * k * items < units:
+        k *= 2
+    return k
+
+
+@pytest.mark.parametrize("KB,grid,cost", [(1, 304, 7), (1, 152, 12), (2, 152, 20)])  # one block, d = 256, two blocks
+def test_list_by_the_kernels_rule(KB, grid, cost):
+    """Short lists, in which CTAs get the beginning of an item and no tile of it, and long ones."""
+    with open(os.path.join(build.CSRC, "rows.cuh")) as f:
+        text = f.read()
+    assert "while (k < 8 && 20 * k * k * items < total) k *= 2;" in text
+    assert "kItemCost = NG == 2 ? 20 : D == 256 ? 12 : 7;" in text
+    rng = random.Random(KB + cost)
+    lists = [([(1, 17)], 8), ([(2, 24)], 8), ([(1, 1)], 1), ([(3, 11)], 8), ([(1, 129)], 2), ([(0, 0), (1, 3), (0, 9), (5, 0)], 3)]
+    lists += [([(rng.randint(0, 5), rng.choice([0, 1, 2, 9, 40])) for _ in range(rng.randint(1, 12))], rng.randint(1, 8))
+              for _ in range(150)]
+    idle = 0
+    for seqs, H in lists:
+        units = H * sum(b * t + cost * -(-b // KB) for b, t in seqs if b and t)
+        if not units:
+            continue
+        least = _least(units, len(seqs) * H * max(b for b, _ in seqs))
+        _check_list(seqs, H, KB, grid, least, cost)
+        ctas = max(1, min(grid, -(-units // least)))
+        idle += ctas > H * sum(b * t for b, t in seqs)
+    assert idle > 5  # lists with CTAs that have nothing but beginnings
