@@ -138,8 +138,8 @@ struct RowCfg {
   static_assert(NG == 1 || NB == 2, "two groups have two buffers each");
   static constexpr float kLift = F16 ? 6.f : 0.f;  // P is 2^(x - m + kLift): at most 2^14, within FP16
   // Where |m| reaches this the roundings of m and kLift - m (an ulp of m: 1 below 2^24, 32 below 2^29) take P out of its
-  // type's range: such rows are NaN.  Rounding x c2 to FP32 before m comes off has no such limit, but cost 1 to 5 % in
-  // each of eight forms tried (a branch per tile, its code in line or not): the loop is bound by its own latency.
+  // type's range: such rows are NaN.  Rounding x c2 to FP32 before m comes off has no such limit, but cost 2 to 8 % on
+  // some case in each of eight forms (a branch per tile, its code in line or not): the loop is bound by its own latency.
   static constexpr float kFar = F16 ? 16777216.f : 536870912.f;
   // What beginning an item takes, in uses.  Without it (0) CTAs with many short items end last: trees of 32 nodes over 32
   // contexts to 8192 keys 127 us, 104 with 7 (106 with 10); prompts of 2048 rows 440 us, 410 with 20 (420 with 34); 333 rows
